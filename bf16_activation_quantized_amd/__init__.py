@@ -66,6 +66,14 @@ def _lib():
         "w4a16_gemm_batched": (ctypes.c_int, [P, P, P, P, I32, I64, I64, I64, I32, I32, P, SZ, P]),
         "w4a16_splitk_reduce": (ctypes.c_int, [P, P, I32, I64, I64, P]),
         "w4a16_gemm_noalloc": (ctypes.c_int, [P, P, P, P, I64, I64, I64, I32, I32, P]),
+        "w4a16_gemm_lora_workspace_bytes": (SZ, [I64, I64, I64, I32, I32, I32, I32]),
+        "w4a16_gemm_lora": (ctypes.c_int, [P, P, P, P, P, P, P, P, I64, I64, I64, I32, I32, I32, I32, P, SZ, P]),
+        "w4a16_expert_sort_workspace_bytes": (SZ, [I64, I32, I32]),
+        "w4a16_expert_sort": (ctypes.c_int, [P, P, P, P, I64, I32, I32, P, SZ, P]),
+        "w4a16_expert_gather": (ctypes.c_int, [P, P, P, I64, I32, I64, I64, P]),
+        "w4a16_expert_gather_grad": (ctypes.c_int, [P, P, P, I64, I32, I64, I64, P]),
+        "w4a16_expert_combine": (ctypes.c_int, [P, P, P, P, I64, I32, I64, I64, P]),
+        "w4a16_expert_combine_grad": (ctypes.c_int, [P, P, P, P, P, P, I64, I32, I64, I64, P]),
         # internal entry points that force a kernel (tests, benchmarks)
         "w4a16_gemm_auto_config": (ctypes.c_int, [I64, I64, I64, I32, P, P]),
         "w4a16_gemm_workspace_bytes_ex": (SZ, [I64, I64, I64, I32, I32, P]),
@@ -296,3 +304,170 @@ def w4a16_splitk_reduce(workspace: torch.Tensor, y: Optional[torch.Tensor] = Non
     _check(y, "y", torch.bfloat16, (M, N))
     _raise(_lib().w4a16_splitk_reduce(_ptr(workspace), _ptr(y), SK, M, N, _stream(stream)), "w4a16_splitk_reduce")
     return y
+
+
+# ------------------------------------------------------------------ low-rank adapters, rows of a mixture of experts
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """torch.empty from the memory pool of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(name: str, tensors, stream, *args) -> None:
+    """Calls a C entry point with the tensors' device current (they all have to
+    be on one device), on `stream` or that device's current stream."""
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: tensors on {device} and {t.device}")
+    f = getattr(_lib(), name)
+    if device.index == torch.cuda.current_device():
+        _raise(f(*args, _stream(stream)), name)
+    else:
+        with torch.cuda.device(device):
+            _raise(f(*args, _stream(stream)), name)
+
+
+def w4a16_gemm_lora_workspace_bytes(M: int, N: int, K: int, L: int, R: int, split_k: int = 0,
+                                    group_size: int = GROUP_SIZE) -> int:
+    return int(_lib().w4a16_gemm_lora_workspace_bytes(M, N, K, group_size, L, R, split_k))
+
+
+def w4a16_gemm_lora(x: torch.Tensor, w_packed: torch.Tensor, scales: torch.Tensor, a: torch.Tensor,
+                    b: torch.Tensor, adapter_ids: torch.Tensor, scaling: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, split_k: int = 0,
+                    workspace: Optional[torch.Tensor] = None, stream=None,
+                    group_size: int = GROUP_SIZE) -> torch.Tensor:
+    """w4a16_gemm with each row's own low-rank adapter added before the one
+    rounding: Y[m] = X[m] . dequant(W)^T + scaling[l] (X[m] . A[l]^T) . B[l]^T,
+    l = adapter_ids[m] (int32 [M]; outside [0, L): no adapter), a [L, R, K],
+    b [L, N, R], scaling fp32 [L] or None (all 1)."""
+    _check(x, "x", torch.bfloat16)
+    M, K = x.shape
+    N = w_packed.shape[0]
+    _check(w_packed, "w_packed", torch.uint8, (N, K // 2))
+    _check(scales, "scales", torch.bfloat16, (N, K // group_size))
+    _check(a, "a", torch.bfloat16)
+    L, R = a.shape[0], a.shape[1]
+    _check(a, "a", torch.bfloat16, (L, R, K))
+    _check(b, "b", torch.bfloat16, (L, N, R))
+    _check(adapter_ids, "adapter_ids", torch.int32, (M,))
+    if scaling is not None:
+        _check(scaling, "scaling", torch.float32, (L,))
+    if y is None:
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
+    _check(y, "y", torch.bfloat16, (M, N))
+    if workspace is None:
+        need = _lib().w4a16_gemm_lora_workspace_bytes(M, N, K, group_size, L, R, split_k)
+        workspace = _empty((need // 4,), torch.float32, x.device, stream)
+    _check(workspace, "workspace", torch.float32)
+    _call("w4a16_gemm_lora", (x, w_packed, scales, a, b, adapter_ids, scaling, y, workspace), stream, _ptr(x),
+          _ptr(w_packed), _ptr(scales), _ptr(a), _ptr(b), _ptr(adapter_ids), _ptr(scaling), _ptr(y), M, N, K,
+          group_size, L, R, split_k, _ptr(workspace), workspace.numel() * 4)
+    return y
+
+
+def w4a16_expert_sort(ids: torch.Tensor, G: int, order: Optional[torch.Tensor] = None,
+                      pos: Optional[torch.Tensor] = None, m_sizes: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> tuple:
+    """Slots of ids [T, k] (int32; outside [0, G): dropped) in expert order:
+    (order [T k], pos [T, k], m_sizes [G]), all int32. m_sizes is the argument
+    of w4a16_gemm_grouped, pos that of the gather and combine calls."""
+    _check(ids, "ids", torch.int32)
+    T, k = ids.shape
+    if order is None:
+        order = _empty((T * k,), torch.int32, ids.device, stream)
+    if pos is None:
+        pos = _empty((T, k), torch.int32, ids.device, stream)
+    if m_sizes is None:
+        m_sizes = _empty((G,), torch.int32, ids.device, stream)
+    _check(order, "order", torch.int32, (T * k,))
+    _check(pos, "pos", torch.int32, (T, k))
+    _check(m_sizes, "m_sizes", torch.int32, (G,))
+    if workspace is None:
+        need = _lib().w4a16_expert_sort_workspace_bytes(T, k, G)
+        workspace = _empty((need // 4,), torch.int32, ids.device, stream)
+    _check(workspace, "workspace", torch.int32)
+    _call("w4a16_expert_sort", (ids, order, pos, m_sizes, workspace), stream, _ptr(ids), _ptr(order), _ptr(pos),
+          _ptr(m_sizes), T, k, G, _ptr(workspace), workspace.numel() * 4)
+    return order, pos, m_sizes
+
+
+def w4a16_expert_sort_workspace_bytes(T: int, k: int, G: int) -> int:
+    return int(_lib().w4a16_expert_sort_workspace_bytes(T, k, G))
+
+
+def w4a16_expert_gather(x: torch.Tensor, pos: torch.Tensor, xs: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """xs[pos[t, j]] = x[t] (rows that no slot names are left as they were)."""
+    _check(x, "x", torch.bfloat16)
+    _check(pos, "pos", torch.int32)
+    T, k = pos.shape
+    width = x.shape[1]
+    _check(x, "x", torch.bfloat16, (T, width))
+    if xs is None:
+        xs = _empty((T * k, width), torch.bfloat16, x.device, stream)
+    rows = xs.shape[0]
+    _check(xs, "xs", torch.bfloat16, (rows, width))
+    _call("w4a16_expert_gather", (x, pos, xs), stream, _ptr(x), _ptr(pos), _ptr(xs), T, k, rows, width)
+    return xs
+
+
+def w4a16_expert_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """dx[t] = sum_j dxs[pos[t, j]]: the gradient of w4a16_expert_gather."""
+    _check(dxs, "dxs", torch.bfloat16)
+    _check(pos, "pos", torch.int32)
+    T, k = pos.shape
+    rows, width = dxs.shape
+    if dx is None:
+        dx = _empty((T, width), torch.bfloat16, dxs.device, stream)
+    _check(dx, "dx", torch.bfloat16, (T, width))
+    _call("w4a16_expert_gather_grad", (dxs, pos, dx), stream, _ptr(dxs), _ptr(pos), _ptr(dx), T, k, rows, width)
+    return dx
+
+
+def w4a16_expert_combine(z: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                         y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[t] = sum_j weights[t, j] z[pos[t, j]] (weights fp32 [T, k], or None: all 1)."""
+    _check(z, "z", torch.bfloat16)
+    _check(pos, "pos", torch.int32)
+    T, k = pos.shape
+    rows, width = z.shape
+    if weights is not None:
+        _check(weights, "weights", torch.float32, (T, k))
+    if y is None:
+        y = _empty((T, width), torch.bfloat16, z.device, stream)
+    _check(y, "y", torch.bfloat16, (T, width))
+    _call("w4a16_expert_combine", (z, pos, weights, y), stream, _ptr(z), _ptr(pos), _ptr(weights), _ptr(y), T, k,
+          rows, width)
+    return y
+
+
+def w4a16_expert_combine_grad(dy: torch.Tensor, z: torch.Tensor, pos: torch.Tensor, weights: torch.Tensor,
+                              dz: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None,
+                              stream=None) -> tuple:
+    """Gradients of w4a16_expert_combine: (dz, dweights). Rows of dz that no
+    slot names are left as they were."""
+    _check(dy, "dy", torch.bfloat16)
+    _check(z, "z", torch.bfloat16)
+    _check(pos, "pos", torch.int32)
+    T, k = pos.shape
+    rows, width = z.shape
+    _check(dy, "dy", torch.bfloat16, (T, width))
+    _check(weights, "weights", torch.float32, (T, k))
+    if dz is None:
+        dz = _empty((rows, width), torch.bfloat16, z.device, stream)
+    if dweights is None:
+        dweights = _empty((T, k), torch.float32, z.device, stream)
+    _check(dz, "dz", torch.bfloat16, (rows, width))
+    _check(dweights, "dweights", torch.float32, (T, k))
+    _call("w4a16_expert_combine_grad", (dy, z, pos, weights, dz, dweights), stream, _ptr(dy), _ptr(z), _ptr(pos),
+          _ptr(weights), _ptr(dz), _ptr(dweights), T, k, rows, width)
+    return dz, dweights

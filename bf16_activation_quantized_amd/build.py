@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libw4a16.so")
 
-SOURCES = ["api.cpp", "pack_reduce.hip", "gemv.hip", "skinny.hip", "skinny_lds.hip", "prefill.hip"]
+SOURCES = ["api.cpp", "pack_reduce.hip", "gemv.hip", "skinny.hip", "skinny_lds.hip", "prefill.hip", "lora.hip",
+           "experts.hip"]
 # MFMA accumulators that the VALU reads (diagonal extraction, per-group
 # rescale) stay in VGPRs (the default heuristic moved them through AGPRs with
 # extra copies); the decode GEMV's kernel arguments arrive preloaded in SGPRs

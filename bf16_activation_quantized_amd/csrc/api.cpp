@@ -477,6 +477,70 @@ void* scratch_ptr() {
   return g_scratch_ptr[dev];
 }
 
+// ---------------------------------------------------------------- low-rank adapters
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+struct LoraPlan {
+  Plan base;
+  int32_t ks, kgps;   // K slices of x . A^T and their 128-groups
+  uint64_t ws_h;      // bytes of the [ks, M, R] fp32 parts of x . A^T
+  uint64_t ws_part;   // bytes of the projection's [SK, M, N] fp32 slices
+};
+
+w4a16_status make_lora_plan(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t L, int32_t R,
+                            int32_t split_k, LoraPlan* p) {
+  if (!valid_split(split_k)) return W4A16_ERR_SPLIT_K;
+  w4a16_status st = check_dims(M, N, K, group_size);
+  if (st != W4A16_OK) return st;
+  if (L < 1 || R < 8 || R > w4a16::kLoraMaxRank || R % 8 != 0) return W4A16_ERR_SHAPE;
+  if ((uint64_t)N * (uint64_t)R * 2u > kMaxBytes || (uint64_t)K * (uint64_t)R * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if (M == 0) return W4A16_OK;
+  const bool small = group_size == kGroup && M <= w4a16::kSkinnyMaxRows;
+  const w4a16_config cfg = {small ? kPathSkinny : kPathTile, small ? 1 : -1};
+  st = make_plan(M, N, K, split_k, &cfg, group_size, &p->base);
+  if (st != W4A16_OK) return st;
+  const int64_t Gk = K / kGroup, row_tiles = ceil_div(M, 16);
+  p->ks = (int32_t)std::min<int64_t>(std::min<int64_t>(8, ceil_div(Gk, 4)), std::max<int64_t>(1, 512 / row_tiles));
+  p->kgps = (int32_t)ceil_div(Gk, p->ks);
+  p->ws_h = round_up((uint64_t)p->ks * (uint64_t)M * (uint64_t)R * 4u, 256);
+  p->ws_part = round_up((uint64_t)p->base.sk * (uint64_t)M * (uint64_t)N * 4u, 256);
+  if ((uint64_t)p->base.sk * (uint64_t)M * (uint64_t)N * 4u > kMaxBytes) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
+uint64_t lora_bytes(const LoraPlan& p) { return p.ws_h + p.ws_part + p.base.ws_sx; }
+
+// ---------------------------------------------------------------- rows of a mixture of experts
+bool expert_slots_ok(int64_t T, int32_t k) { return T >= 0 && k >= 1 && T <= kMaxDim / k; }
+
+uint64_t expert_sort_bytes(int64_t T, int32_t k, int32_t G) {
+  return round_up((uint64_t)w4a16::expert_sort_blocks(T * k) * (uint64_t)(G + 1) * 4u, 256);
+}
+
+// Checks of the calls on rows; *empty: nothing to enqueue.
+w4a16_status check_expert_rows(int64_t T, int32_t k, int64_t rows, int64_t width, const int32_t* pos, bool* empty) {
+  *empty = false;
+  if (!expert_slots_ok(T, k) || rows < 0 || rows > kMaxDim || width < 1 || width > kMaxDim) return W4A16_ERR_SHAPE;
+  if (T == 0) {
+    *empty = true;
+    return W4A16_OK;
+  }
+  if (pos == nullptr) return W4A16_ERR_NULL;
+  if (!aligned4(pos)) return W4A16_ERR_ALIGN;
+  return W4A16_OK;
+}
+
+w4a16_status run_expert_combine(const uint16_t* z, const int32_t* pos, const float* weights, uint16_t* y, int64_t T,
+                                int32_t k, int64_t rows, int64_t width, void* stream) {
+  bool empty = false;
+  const w4a16_status st = check_expert_rows(T, k, rows, width, pos, &empty);
+  if (st != W4A16_OK || empty) return st;
+  if (y == nullptr || (z == nullptr && rows > 0)) return W4A16_ERR_NULL;
+  if (!aligned16(y) || !aligned16(z) || !aligned4(weights)) return W4A16_ERR_ALIGN;
+  return launched(w4a16::launch_expert_combine(z, pos, weights, y, T, k, rows, (int)width,
+                                               reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -672,6 +736,104 @@ w4a16_status w4a16_splitk_reduce(const float* workspace, uint16_t* y, int32_t sp
   if ((uint64_t)M > (uint64_t)INT64_MAX / (uint64_t)N / 64u) return W4A16_ERR_SHAPE;
   return launched(w4a16::launch_splitk_reduce(workspace, y, (uint64_t)M * (uint64_t)N, split_k,
                                               reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t w4a16_gemm_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t L, int32_t R,
+                                       int32_t split_k) {
+  LoraPlan p;
+  if (make_lora_plan(M, N, K, group_size, L, R, split_k, &p) != W4A16_OK || M == 0) return 0;
+  return (size_t)lora_bytes(p);
+}
+
+w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed, const uint16_t* scales, const uint16_t* a,
+                             const uint16_t* b, const int32_t* adapter_ids, const float* scaling, uint16_t* y,
+                             int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t L, int32_t R,
+                             int32_t split_k, float* workspace, size_t workspace_bytes, void* stream) {
+  LoraPlan p;
+  const w4a16_status st = make_lora_plan(M, N, K, group_size, L, R, split_k, &p);
+  if (st != W4A16_OK || M == 0) return st;
+  if (x == nullptr || w_packed == nullptr || scales == nullptr || a == nullptr || b == nullptr ||
+      adapter_ids == nullptr || y == nullptr)
+    return W4A16_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w_packed) || !aligned16(scales) || !aligned16(a) || !aligned16(b) || !aligned16(y))
+    return W4A16_ERR_ALIGN;
+  if (!aligned4(adapter_ids) || !aligned4(scaling)) return W4A16_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < lora_bytes(p)) return W4A16_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+  hipStream_t strm = reinterpret_cast<hipStream_t>(stream);
+  uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
+  float* h = workspace;
+  float* part = reinterpret_cast<float*>(base + p.ws_h);
+  float* rowsums = reinterpret_cast<float*>(base + p.ws_h + p.ws_part);
+  const int iM = (int)M, iN = (int)N, iK = (int)K;
+  hipError_t e = w4a16::launch_lora_shrink(x, a, adapter_ids, scaling, h, iM, iK, L, R, p.kgps, p.ks, strm);
+  if (e != hipSuccess) return W4A16_ERR_LAUNCH;
+  if (p.base.path == kPathSkinny) {
+    e = w4a16::launch_skinny(x, w_packed, scales, y, part, iM, iN, iK, p.base.gps, p.base.sk, p.base.variant,
+                             kSkinnyWaves, strm);
+  } else {
+    const int ld = (int)round_up((uint64_t)M, 4);
+    if (p.base.ws_sx > 0) e = w4a16::launch_rowsum_neg136(x, rowsums, iM, iK, ld, group_size, strm);
+    if (e == hipSuccess)
+      e = w4a16::launch_tile(x, w_packed, scales, p.base.ws_sx > 0 ? rowsums : nullptr, ld, y, part, nullptr, 0, iM,
+                             iN, iK, 1, p.base.gps, p.base.sk, p.base.variant, group_size, strm);
+  }
+  if (e != hipSuccess) return W4A16_ERR_LAUNCH;
+  return launched(w4a16::launch_lora_expand(part, h, b, adapter_ids, y, iM, iN, L, R, p.base.sk, p.ks, strm));
+}
+
+size_t w4a16_expert_sort_workspace_bytes(int64_t T, int32_t k, int32_t G) {
+  if (!expert_slots_ok(T, k) || G < 1 || G > w4a16::kExpertMaxGroups || T == 0) return 0;
+  return (size_t)expert_sort_bytes(T, k, G);
+}
+
+w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t T,
+                               int32_t k, int32_t G, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!expert_slots_ok(T, k) || G < 1 || G > w4a16::kExpertMaxGroups) return W4A16_ERR_SHAPE;
+  if (m_sizes == nullptr) return W4A16_ERR_NULL;
+  if (T > 0 && (ids == nullptr || order == nullptr || pos == nullptr)) return W4A16_ERR_NULL;
+  if (!aligned4(ids) || !aligned4(order) || !aligned4(pos) || !aligned4(m_sizes)) return W4A16_ERR_ALIGN;
+  if (T > 0) {
+    if (workspace == nullptr || workspace_bytes < expert_sort_bytes(T, k, G)) return W4A16_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+  }
+  return launched(w4a16::launch_expert_sort(ids, order, pos, m_sizes, T * k, G, reinterpret_cast<int32_t*>(workspace),
+                                            reinterpret_cast<hipStream_t>(stream)));
+}
+
+w4a16_status w4a16_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int32_t k,
+                                 int64_t rows, int64_t width, void* stream) {
+  bool empty = false;
+  const w4a16_status st = check_expert_rows(T, k, rows, width, pos, &empty);
+  if (st != W4A16_OK || empty || rows == 0) return st;
+  if (x == nullptr || xs == nullptr) return W4A16_ERR_NULL;
+  if (!aligned16(x) || !aligned16(xs)) return W4A16_ERR_ALIGN;
+  return launched(w4a16::launch_expert_gather(x, pos, xs, T, k, rows, (int)width,
+                                              reinterpret_cast<hipStream_t>(stream)));
+}
+
+w4a16_status w4a16_expert_gather_grad(const uint16_t* dxs, const int32_t* pos, uint16_t* dx, int64_t T, int32_t k,
+                                      int64_t rows, int64_t width, void* stream) {
+  return run_expert_combine(dxs, pos, nullptr, dx, T, k, rows, width, stream);
+}
+
+w4a16_status w4a16_expert_combine(const uint16_t* z, const int32_t* pos, const float* weights, uint16_t* y, int64_t T,
+                                  int32_t k, int64_t rows, int64_t width, void* stream) {
+  return run_expert_combine(z, pos, weights, y, T, k, rows, width, stream);
+}
+
+w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z, const int32_t* pos,
+                                       const float* weights, uint16_t* dz, float* dweights, int64_t T, int32_t k,
+                                       int64_t rows, int64_t width, void* stream) {
+  bool empty = false;
+  const w4a16_status st = check_expert_rows(T, k, rows, width, pos, &empty);
+  if (st != W4A16_OK || empty) return st;
+  if (dy == nullptr || weights == nullptr || dweights == nullptr) return W4A16_ERR_NULL;
+  if (rows > 0 && (z == nullptr || dz == nullptr)) return W4A16_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(z) || !aligned16(dz) || !aligned4(weights) || !aligned4(dweights))
+    return W4A16_ERR_ALIGN;
+  return launched(w4a16::launch_expert_combine_grad(dy, z, pos, weights, dz, dweights, T, k, rows, (int)width,
+                                                    reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -66,4 +66,28 @@ hipError_t launch_tile(const uint16_t* x, const uint8_t* w, const uint16_t* s, c
 bool tile_rows_ok(int bm, int gsize);
 constexpr int kTileCols = 256;
 
+// ---- low-rank adapters beside the projection (lora.hip)
+constexpr int kLoraMaxRank = 128;
+// hp[s, m, r] = sc * partial sum of x[m, :] . A[ids[m], r, :] over K slice s of ks (gps 128-groups each)
+hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
+                              float* hp, int M, int K, int L, int R, int gps, int ks, hipStream_t stream);
+// y = bf16(sum of the sk slices ws[s, m, n] + sum_r h[m, r] B[ids[m], n, r])
+hipError_t launch_lora_expand(const float* ws, const float* hp, const uint16_t* b, const int32_t* ids, uint16_t* y,
+                              int M, int N, int L, int R, int sk, int ks, hipStream_t stream);
+
+// ---- rows of a mixture of experts (experts.hip)
+constexpr int kExpertMaxGroups = 4096;
+int expert_sort_chunk(int64_t S);    // slots per block
+int expert_sort_blocks(int64_t S);   // blocks, one row of G + 1 counts of workspace each
+hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t S, int G,
+                              int32_t* ws, hipStream_t stream);
+hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int k, int64_t rows,
+                                int width, hipStream_t stream);
+// w == nullptr: all weights 1
+hipError_t launch_expert_combine(const uint16_t* z, const int32_t* pos, const float* w, uint16_t* y, int64_t T, int k,
+                                 int64_t rows, int width, hipStream_t stream);
+hipError_t launch_expert_combine_grad(const uint16_t* dy, const uint16_t* z, const int32_t* pos, const float* w,
+                                      uint16_t* dz, float* dw, int64_t T, int k, int64_t rows, int width,
+                                      hipStream_t stream);
+
 }  // namespace w4a16

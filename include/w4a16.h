@@ -53,7 +53,8 @@ typedef enum {
   W4A16_OK = 0,
   W4A16_ERR_NULL = 1,        /* a required pointer is NULL                       */
   W4A16_ERR_SHAPE = 2,       /* a dimension is negative, zero where not allowed,
-                                odd K, or a size limit is exceeded               */
+                                odd K, an adapter rank that is no multiple of 8
+                                in 8 .. 128, or a size limit is exceeded         */
   W4A16_ERR_GROUP_SIZE = 3,  /* group_size not 128 or 32, K % 128 != 0, or group
                                 size 32 with a kernel that takes 128 only        */
   W4A16_ERR_SPLIT_K = 4,     /* split_k not in {0, 1, 2, 4, 8, 16}               */
@@ -191,7 +192,10 @@ w4a16_status w4a16_gemm_noalloc(const uint16_t* x, const uint8_t* w_packed,
  *               (checking would need a sync): m_sizes[g] >= 0 and
  *               sum == M_total. If they are broken the kernel still writes
  *               only rows inside [0, M_total) of y and reads only rows inside
- *               x; which rows are then written is unspecified. A group with
+ *               x; which rows are then written is unspecified, except that
+ *               with sizes >= 0 and a sum below M_total (slots dropped by
+ *               w4a16_expert_sort) the first sum rows are computed and the
+ *               rows behind them are neither read nor written. A group with
  *               m_sizes[g] == 0 contributes nothing.
  *   y         : [M_total, N] bf16, device, written
  *   G >= 1, M_total >= 0 (0: W4A16_OK, nothing enqueued), N >= 1, K >= 128,
@@ -260,6 +264,116 @@ w4a16_status w4a16_gemm_batched(const uint16_t* x, const uint8_t* w_packed,
 w4a16_status w4a16_splitk_reduce(const float* workspace, uint16_t* y,
                                  int32_t split_k, int64_t M, int64_t N,
                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside the shared projection.
+ *
+ *   l = adapter_ids[m]
+ *   Y[m] = X[m] . dequant(W)^T + scaling[l] * (X[m] . A[l]^T) . B[l]^T
+ *
+ * (the second term only where 0 <= l < L), with both terms summed in fp32 and
+ * one rounding to bf16.
+ *   x, w_packed, scales, y, M, N, K, group_size, split_k: as for w4a16_gemm.
+ *   a           : [L, R, K] bf16, device (adapter l, rank r: a row of K)
+ *   b           : [L, N, R] bf16, device (adapter l, output column n: a row of R)
+ *   adapter_ids : [M] int32, device, 4-byte aligned, read by the kernels (never
+ *                 copied to the host): the adapter of each row, in any order;
+ *                 any value outside [0, L) means none.
+ *   scaling     : [L] fp32, device, 4-byte aligned, or NULL (all 1)
+ *   L >= 1; R a multiple of 8, 8 <= R <= 128 (pad an adapter of another rank
+ *   with zeros: W4A16_ERR_SHAPE otherwise); N * R * 2 < 2^32 bytes. a and b may
+ *   be larger than 2^32 bytes. Adapters of the parts of a fused projection
+ *   (gate and up, or q, k and v) are one adapter of the ranks' sum, with zeros
+ *   in B outside each part's columns.
+ *   workspace   : fp32 device scratch, overwritten, never NULL when M > 0: at
+ *                 least w4a16_gemm_lora_workspace_bytes, 16-byte aligned.
+ * Values of an adapter reach only the rows that name it: an infinity or NaN in
+ * another adapter, or in another row, leaves a row as it is. X . A[l]^T is
+ * held in fp32 and enters the second product as the sum of two bf16 values
+ * (relative error of each element at most 2^-16). No atomics are used: the
+ * result is bitwise reproducible for a given shape and split_k.
+ */
+size_t w4a16_gemm_lora_workspace_bytes(int64_t M, int64_t N, int64_t K,
+                                       int32_t group_size, int32_t L, int32_t R,
+                                       int32_t split_k);
+w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed,
+                             const uint16_t* scales, const uint16_t* a,
+                             const uint16_t* b, const int32_t* adapter_ids,
+                             const float* scaling, uint16_t* y,
+                             int64_t M, int64_t N, int64_t K, int32_t group_size,
+                             int32_t L, int32_t R, int32_t split_k,
+                             float* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rows of a mixture of experts around w4a16_gemm_grouped.
+ *
+ * T tokens choose k experts each: slot s = t * k + j holds expert ids[t, j].
+ * Slots whose id is outside [0, G) are dropped (padded tokens, experts of
+ * another device). T >= 0, k >= 1, T * k < 2^31, 1 <= G <= 4096. The bf16
+ * arrays here may be larger than 2^32 bytes; a row's width is any number >= 1
+ * below 2^31.
+ *
+ * w4a16_expert_sort: the slots in expert order, slot order within an expert.
+ *   ids     : [T, k] int32, device
+ *   order   : [T * k] int32, device, written: the slot at each sorted row; the
+ *             dropped slots follow the kept ones, in slot order
+ *   pos     : [T, k] int32, device, written: the sorted row of each slot, -1
+ *             for a dropped one
+ *   m_sizes : [G] int32, device, written: rows per expert (the m_sizes of
+ *             w4a16_gemm_grouped); all zero when T == 0
+ *   workspace: device scratch, overwritten, 16-byte aligned, at least
+ *             w4a16_expert_sort_workspace_bytes (0 when T == 0 or on invalid
+ *             arguments).
+ */
+size_t w4a16_expert_sort_workspace_bytes(int64_t T, int32_t k, int32_t G);
+w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,
+                               int32_t* m_sizes, int64_t T, int32_t k, int32_t G,
+                               void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/*
+ * The four calls below take `pos` of w4a16_expert_sort (4-byte aligned) and
+ * expert-ordered arrays of `rows` rows (T * k hold every slot; with fewer, a
+ * slot whose position is not below `rows` counts as dropped). Two slots of
+ * one call never share a position. The rows that no slot names (those behind
+ * the last kept one) are neither read nor written.
+ *
+ * w4a16_expert_gather: xs[pos[t, j]] = x[t].
+ *   x : [T, width] bf16, device;  xs : [rows, width] bf16, device, written
+ * w4a16_expert_gather_grad, its gradient: dx[t] = sum_j dxs[pos[t, j]], summed
+ * in fp32 in the order of j and rounded once; zero where every slot is dropped.
+ *   dxs : [rows, width] bf16, device;  dx : [T, width] bf16, device, written
+ */
+w4a16_status w4a16_expert_gather(const uint16_t* x, const int32_t* pos,
+                                 uint16_t* xs, int64_t T, int32_t k,
+                                 int64_t rows, int64_t width, void* stream);
+w4a16_status w4a16_expert_gather_grad(const uint16_t* dxs, const int32_t* pos,
+                                      uint16_t* dx, int64_t T, int32_t k,
+                                      int64_t rows, int64_t width, void* stream);
+
+/*
+ * w4a16_expert_combine: y[t] = sum_j weights[t, j] * z[pos[t, j]], summed in
+ * fp32 in the order of j and rounded once; zero where every slot is dropped.
+ *   z : [rows, width] bf16, device;  weights : [T, k] fp32, device (4-byte
+ *   aligned), or NULL (all 1);  y : [T, width] bf16, device, written
+ * w4a16_expert_combine_grad, its gradients from dy = dL/dy:
+ *   dz[pos[t, j]] = weights[t, j] * dy[t] (bf16, rounded once), and
+ *   dweights[t, j] = sum_n dy[t, n] * z[pos[t, j], n] (fp32; 0 for a dropped
+ *   slot).
+ *   dy : [T, width] bf16, device;  z, dz : [rows, width] bf16, device (dz
+ *   written);  weights, dweights : [T, k] fp32, device (dweights written)
+ * Written arrays must not overlap the read ones, except that dz may be z.
+ */
+w4a16_status w4a16_expert_combine(const uint16_t* z, const int32_t* pos,
+                                  const float* weights, uint16_t* y, int64_t T,
+                                  int32_t k, int64_t rows, int64_t width,
+                                  void* stream);
+w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z,
+                                       const int32_t* pos, const float* weights,
+                                       uint16_t* dz, float* dweights, int64_t T,
+                                       int32_t k, int64_t rows, int64_t width,
+                                       void* stream);
 
 #ifdef __cplusplus
 }

@@ -11,6 +11,7 @@
 
 #include "../../include/w4a16.h"
 #include "launch.hpp"
+#include "lora.hpp"
 #include "w4a16_internal.h"
 
 namespace {
@@ -346,30 +347,30 @@ w4a16_status plan_gemm(const uint16_t* x, const uint8_t* w, const uint16_t* s, u
 
 // Enqueues a planned GEMM; `partials` holds the [SK, M, N] fp32 slices when
 // p.sk > 1 (unused otherwise); `rowsums` (tile path, may be nullptr) the
-// pre-pass row sums.
+// pre-pass row sums; `la` per-row adapters.
 w4a16_status launch_plan(const Plan& p, const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y,
                          int64_t M, int64_t N, int64_t K, int32_t group_size, float* partials, float* rowsums,
-                         hipStream_t strm) {
+                         hipStream_t strm, const w4a16::LoraArgs* la = nullptr) {
   float* ws_split = p.sk > 1 ? partials : nullptr;
   const int iM = (int)M, iN = (int)N, iK = (int)K;
   hipError_t e = hipSuccess;
   switch (p.path) {
     case kPathGemv:
-      e = w4a16::launch_gemv_m1(x, w, s, y, ws_split, iN, iK, p.gps, p.sk, p.variant == 1, strm);
+      e = w4a16::launch_gemv_m1(x, w, s, y, ws_split, iN, iK, p.gps, p.sk, p.variant == 1, strm, la);
       break;
     case kPathSkinny:
       if (p.variant >= 3 && w4a16::skinny_lds_fits(iM, p.gps))
-        e = w4a16::launch_skinny_lds(x, w, s, y, ws_split, iM, iN, iK, p.gps, p.sk, p.variant - 3, strm);
+        e = w4a16::launch_skinny_lds(x, w, s, y, ws_split, iM, iN, iK, p.gps, p.sk, p.variant - 3, strm, la);
       else
         e = w4a16::launch_skinny(x, w, s, y, ws_split, iM, iN, iK, p.gps, p.sk, p.variant >= 3 ? 1 : p.variant,
-                                 kSkinnyWaves, strm);
+                                 kSkinnyWaves, strm, la);
       break;
     case kPathTile: {
       const int ld = (int)round_up((uint64_t)M, 4);
       if (rowsums != nullptr) e = w4a16::launch_rowsum_neg136(x, rowsums, iM, iK, ld, group_size, strm);
       if (e == hipSuccess)
         e = w4a16::launch_tile(x, w, s, rowsums, ld, y, ws_split, nullptr, 0, iM, iN, iK, 1, p.gps, p.sk, p.variant,
-                               group_size, strm);
+                               group_size, strm, la);
       break;
     }
     default:
@@ -481,10 +482,8 @@ void* scratch_ptr() {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 struct LoraPlan {
-  Plan base;
-  int32_t ks, kgps;   // K slices of x . A^T and their 128-groups
-  uint64_t ws_h;      // bytes of the [ks, M, R] fp32 parts of x . A^T
-  uint64_t ws_part;   // bytes of the projection's [SK, M, N] fp32 slices
+  Plan base;       // the projection
+  uint64_t ws_h;   // bytes of the [2, M, R] bf16 parts of x . A^T, ahead of the projection's workspace
 };
 
 w4a16_status make_lora_plan(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t L, int32_t R,
@@ -493,22 +492,24 @@ w4a16_status make_lora_plan(int64_t M, int64_t N, int64_t K, int32_t group_size,
   w4a16_status st = check_dims(M, N, K, group_size);
   if (st != W4A16_OK) return st;
   if (L < 1 || R < 8 || R > w4a16::kLoraMaxRank || R % 8 != 0) return W4A16_ERR_SHAPE;
-  if ((uint64_t)N * (uint64_t)R * 2u > kMaxBytes || (uint64_t)K * (uint64_t)R * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if ((uint64_t)N * (uint64_t)R * 2u > kMaxBytes || (uint64_t)K * (uint64_t)R * 2u > kMaxBytes ||
+      (uint64_t)M * (uint64_t)R * 4u > kMaxBytes)
+    return W4A16_ERR_SHAPE;
   if (M == 0) return W4A16_OK;
-  const bool small = group_size == kGroup && M <= w4a16::kSkinnyMaxRows;
-  const w4a16_config cfg = {small ? kPathSkinny : kPathTile, small ? 1 : -1};
-  st = make_plan(M, N, K, split_k, &cfg, group_size, &p->base);
+  st = make_plan(M, N, K, split_k, nullptr, group_size, &p->base);
   if (st != W4A16_OK) return st;
-  const int64_t Gk = K / kGroup, row_tiles = ceil_div(M, 16);
-  p->ks = (int32_t)std::min<int64_t>(std::min<int64_t>(8, ceil_div(Gk, 4)), std::max<int64_t>(1, 512 / row_tiles));
-  p->kgps = (int32_t)ceil_div(Gk, p->ks);
-  p->ws_h = round_up((uint64_t)p->ks * (uint64_t)M * (uint64_t)R * 4u, 256);
-  p->ws_part = round_up((uint64_t)p->base.sk * (uint64_t)M * (uint64_t)N * 4u, 256);
-  if ((uint64_t)p->base.sk * (uint64_t)M * (uint64_t)N * 4u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if (p->base.path == kPathGemv && !w4a16::gemv_mfma_fits(p->base.gps)) {
+    // a slice length of the half-wave GEMV, which takes no adapters
+    const w4a16_config cfg = {kPathSkinny, -1};
+    st = make_plan(M, N, K, split_k, &cfg, group_size, &p->base);
+    if (st != W4A16_OK) return st;
+  }
+  if (p->base.ws_split > kMaxBytes) return W4A16_ERR_SHAPE;
+  p->ws_h = round_up((uint64_t)M * (uint64_t)R * 4u, 256);
   return W4A16_OK;
 }
 
-uint64_t lora_bytes(const LoraPlan& p) { return p.ws_h + p.ws_part + p.base.ws_sx; }
+uint64_t lora_bytes(const LoraPlan& p) { return p.ws_h + plan_bytes(p.base); }
 
 // ---------------------------------------------------------------- rows of a mixture of experts
 bool expert_slots_ok(int64_t T, int32_t k) { return T >= 0 && k >= 1 && T <= kMaxDim / k; }
@@ -761,25 +762,16 @@ w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed, const u
   if (workspace == nullptr || workspace_bytes < lora_bytes(p)) return W4A16_ERR_WORKSPACE;
   if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
   hipStream_t strm = reinterpret_cast<hipStream_t>(stream);
-  uint8_t* base = reinterpret_cast<uint8_t*>(workspace);
-  float* h = workspace;
-  float* part = reinterpret_cast<float*>(base + p.ws_h);
-  float* rowsums = reinterpret_cast<float*>(base + p.ws_h + p.ws_part);
-  const int iM = (int)M, iN = (int)N, iK = (int)K;
-  hipError_t e = w4a16::launch_lora_shrink(x, a, adapter_ids, scaling, h, iM, iK, L, R, p.kgps, p.ks, strm);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws);
+  float* partials = reinterpret_cast<float*>(ws + p.ws_h);
+  float* rowsums =
+      p.base.ws_sx > 0 ? reinterpret_cast<float*>(ws + p.ws_h + round_up(p.base.ws_split, 256)) : nullptr;
+  const hipError_t e =
+      w4a16::launch_lora_shrink(x, a, adapter_ids, scaling, h, (int)M, (int)K, L, R, strm);
   if (e != hipSuccess) return W4A16_ERR_LAUNCH;
-  if (p.base.path == kPathSkinny) {
-    e = w4a16::launch_skinny(x, w_packed, scales, y, part, iM, iN, iK, p.base.gps, p.base.sk, p.base.variant,
-                             kSkinnyWaves, strm);
-  } else {
-    const int ld = (int)round_up((uint64_t)M, 4);
-    if (p.base.ws_sx > 0) e = w4a16::launch_rowsum_neg136(x, rowsums, iM, iK, ld, group_size, strm);
-    if (e == hipSuccess)
-      e = w4a16::launch_tile(x, w_packed, scales, p.base.ws_sx > 0 ? rowsums : nullptr, ld, y, part, nullptr, 0, iM,
-                             iN, iK, 1, p.base.gps, p.base.sk, p.base.variant, group_size, strm);
-  }
-  if (e != hipSuccess) return W4A16_ERR_LAUNCH;
-  return launched(w4a16::launch_lora_expand(part, h, b, adapter_ids, y, iM, iN, L, R, p.base.sk, p.ks, strm));
+  const w4a16::LoraArgs la = {h, b, adapter_ids, (int)M, (int)N, L, R};
+  return launch_plan(p.base, x, w_packed, scales, y, M, N, K, group_size, partials, rowsums, strm, &la);
 }
 
 size_t w4a16_expert_sort_workspace_bytes(int64_t T, int32_t k, int32_t G) {

@@ -24,6 +24,7 @@
 // [s * gps, min((s + 1) * gps, G)) and writes fp32 partials to ws[s, 0, :].
 #include "common.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 
 #include <algorithm>
 #include <atomic>
@@ -149,6 +150,85 @@ __device__ __forceinline__ void wave_reduce_rows(float (&acc)[R]) {
 
 constexpr int kMaxChunks = 256;   // 32-k chunks per row-slice (64 groups)
 
+// The adapter's part of a workgroup of the M = 1 GEMV, which owns columns
+// [lo, hi), at most kGemvLoraCols of them.
+constexpr int kGemvLoraCols = 256;
+
+template <int NTHR, bool ON>
+struct GemvLora {};
+
+template <int NTHR>
+struct GemvLora<NTHR, true> {
+  static constexpr int kItems = kGemvLoraCols * kLoraMaxRank / 8;   // 16-byte pieces of the columns' rows of B
+  struct Lds {
+    float sums[kGemvLoraCols];
+    float part[kItems];
+    float h[kLoraMaxRank];
+  };
+  Lds* s;
+  int lo, hi, l;
+  u32x4 first;            // this thread's first piece of B
+  uint16_t h_hi, h_lo;    // h of rank tid
+
+  __device__ __forceinline__ float& sum(int n) { return s->sums[n - lo]; }
+
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const LoraArgs& la) const {
+    return make_rsrc(la.b + ((size_t)l * la.N + lo) * la.R, (uint32_t)(hi - lo) * (uint32_t)la.R * 2u);
+  }
+
+  // Loads only (without an adapter past the extents, so that the number of
+  // loads in flight is the same); their results are used in end().
+  __device__ __forceinline__ void begin(const LoraArgs& la, int from, int to, int slice, int tid) {
+    __shared__ Lds lds;
+    s = &lds;
+    lo = from;
+    hi = to;
+    const int id = __builtin_amdgcn_readfirstlane(la.ids[0]);
+    const bool on = slice == 0 && (uint32_t)id < (uint32_t)la.L;
+    l = on ? id : 0;
+    first = ld128(rows(la), on ? 16u * (uint32_t)tid : 0xFFFFFFF0u);
+    const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 4u * (uint32_t)la.R);
+    const uint32_t off = on && tid < la.R ? 2u * (uint32_t)tid : 0xFFFFFFF0u;
+    h_hi = ld16(rh, off);
+    h_lo = ld16(rh, off, 2u * (uint32_t)la.R);
+    if (!on) l = -1;
+  }
+
+  // the products of piece i (8 ranks of one column)
+  __device__ __forceinline__ void dot(u32x4 v, int i, int oct) {
+    const float* h = s->h + 8 * (i % oct);
+    float d = bf16lo(v.x) * h[0];
+    d = fmaf(bf16hi(v.x), h[1], d);
+    d = fmaf(bf16lo(v.y), h[2], d);
+    d = fmaf(bf16hi(v.y), h[3], d);
+    d = fmaf(bf16lo(v.z), h[4], d);
+    d = fmaf(bf16hi(v.z), h[5], d);
+    d = fmaf(bf16lo(v.w), h[6], d);
+    s->part[i] = fmaf(bf16hi(v.w), h[7], d);
+  }
+
+  __device__ __forceinline__ void end(const LoraArgs& la, void* out, int slice, int tid) {
+    const int oct = la.R / 8, items = (hi - lo) * oct;
+    if (tid < la.R) s->h[tid] = bf16f(h_hi) + bf16f(h_lo);
+    __syncthreads();
+    if (l >= 0) {
+      if (tid < items) dot(first, tid, oct);
+      for (int i = tid + NTHR; i < items; i += NTHR) dot(ld128(rows(la), 16u * (uint32_t)i), i, oct);
+      __syncthreads();
+    }
+    for (int c = tid; c < hi - lo; c += NTHR) {
+      float v = s->sums[c];
+      if (l >= 0) {
+        float d = s->part[c * oct];
+        for (int o = 1; o < oct; ++o) d += s->part[c * oct + o];
+        v += d;
+      }
+      if (gridDim.y > 1) static_cast<float*>(out)[(size_t)slice * la.N + lo + c] = v;
+      else static_cast<uint16_t*>(out)[lo + c] = to_bf16(v);
+    }
+  }
+};
+
 // ---------------------------------------------------------------- MFMA layout
 // The default for M = 1. The lanes of a wave are laid over a block of R weight
 // rows (of this K-slice) so that every wave instruction reads one contiguous
@@ -166,12 +246,18 @@ constexpr int kMaxChunks = 256;   // 32-k chunks per row-slice (64 groups)
 // (group g, sub-chunk kb, dword j) in the pair order of the dequant, slot
 // (4 kb + j) XOR-swizzled by (g & 15) so that the 16 lanes of a B read (16
 // consecutive groups, same slot) hit 16 different bank groups.
-template <int R, int I, int D, int WAVES>
+// LA: nothing, or the LoraArgs of the row's adapter. The workgroup's columns
+// are one contiguous run, so their rows of B are one contiguous run too: its
+// first 16-byte pieces, one per thread, are requested behind the first weight
+// blocks, and the rest after the last one; the projection's sums wait in LDS
+// and are stored with the adapter's products added (K slice 0).
+template <int R, int I, int D, int WAVES, class... LA>
 __global__ __launch_bounds__(64 * WAVES) void gemv_mfma_kernel(const uint16_t* __restrict__ x,
                                                                const uint8_t* __restrict__ w,
                                                                const uint16_t* __restrict__ s,
                                                                void* __restrict__ out,
-                                                               int N, int K, int gps, int bper, int brem) {
+                                                               int N, int K, int gps, int bper, int brem,
+                                                               const LA... la) {
   // (13 dwords of arguments: all of them arrive preloaded in SGPRs where the
   // code object asks for kernel-argument preloading, so the first address
   // computations wait on no scalar load)
@@ -273,6 +359,9 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_mfma_kernel(const uint16_t* _
   // requests one more block (see the loop at the end)
 #pragma unroll
   for (int jb = 0; jb < (D > 1 ? D - 1 : 1); ++jb) issue(wbuf[jb], sbuf[jb], jb);
+
+  GemvLora<64 * WAVES, sizeof...(LA) != 0> adapter;
+  if constexpr (sizeof...(LA) > 0) (adapter.begin(la, b_lo * R, min(N, (b_lo + nbw) * R), slice, tid), ...);
 
   // ---- the rest of the per-lane mapping, needed only when a block is consumed
   uint32_t xaddr[I], sshift[I];
@@ -400,7 +489,8 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_mfma_kernel(const uint16_t* _
       for (int rr = 0; rr < R; ++rr) {
         const int n = (b_lo + wq + jb * WAVES) * R + rr;
         if (n < N) {
-          if (!partials) static_cast<uint16_t*>(out)[n] = to_bf16(acc[rr]);
+          if constexpr (sizeof...(LA) > 0) adapter.sum(n) = acc[rr];
+          else if (!partials) static_cast<uint16_t*>(out)[n] = to_bf16(acc[rr]);
           else static_cast<float*>(out)[(size_t)slice * N + n] = acc[rr];
         }
       }
@@ -430,6 +520,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemv_mfma_kernel(const uint16_t* _
       }
     }
   }
+  if constexpr (sizeof...(LA) > 0) (adapter.end(la, out, slice, tid), ...);
 }
 
 // MFMA-layout geometry: a block of R rows holds 16 * I groups (R <= 4, I <= 8)
@@ -459,24 +550,37 @@ static int cu_count() {
 // about one block per wave the ring only adds dead requests: 1 x 6144 x 2560
 // 4.78 -> 4.94 us) and a block is under 7 instructions (a second register
 // set of 7 spills).
-template <int R, int I>
-static hipError_t launch_mfma_ri(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
-                                 int N, int K, int gps, int sk, hipStream_t stream) {
+template <int R, int I, class... LA>
+static hipError_t launch_mfma_la(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
+                                 int N, int K, int gps, int sk, hipStream_t stream, LA... la) {
   constexpr int kWaves = 8;
   const int nblk = (N + R - 1) / R;
-  const int gx = std::max(1, std::min(cu_count(), (nblk + kWaves - 1) / kWaves));
+  int gx = std::max(1, std::min(cu_count(), (nblk + kWaves - 1) / kWaves));
+  if (sizeof...(LA) > 0) gx = std::max(gx, (nblk + kGemvLoraCols / R - 1) / (kGemvLoraCols / R));   // columns in LDS
   const int bper = nblk / gx, brem = nblk - bper * gx;
   void* out = sk > 1 ? static_cast<void*>(ws) : static_cast<void*>(y);
   if constexpr (I < 7) {
     if (bper >= 2 * kWaves) {
-      hipLaunchKernelGGL((gemv_mfma_kernel<R, I, 2, kWaves>), dim3(gx, sk), dim3(64 * kWaves), 0, stream, x, w, s,
-                         out, N, K, gps, bper, brem);
+      hipLaunchKernelGGL((gemv_mfma_kernel<R, I, 2, kWaves, LA...>), dim3(gx, sk), dim3(64 * kWaves), 0, stream, x, w,
+                         s, out, N, K, gps, bper, brem, la...);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((gemv_mfma_kernel<R, I, 1, kWaves>), dim3(gx, sk), dim3(64 * kWaves), 0, stream, x, w, s, out,
-                     N, K, gps, bper, brem);
+  hipLaunchKernelGGL((gemv_mfma_kernel<R, I, 1, kWaves, LA...>), dim3(gx, sk), dim3(64 * kWaves), 0, stream, x, w, s,
+                     out, N, K, gps, bper, brem, la...);
   return hipGetLastError();
+}
+
+template <int R, int I>
+static hipError_t launch_mfma_ri(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
+                                 int N, int K, int gps, int sk, hipStream_t stream, const LoraArgs* la) {
+  if (la != nullptr) return launch_mfma_la<R, I>(x, w, s, y, ws, N, K, gps, sk, stream, *la);
+  return launch_mfma_la<R, I>(x, w, s, y, ws, N, K, gps, sk, stream);
+}
+
+bool gemv_mfma_fits(int gps) {
+  int R, I;
+  return mfma_geometry(gps, &R, &I);
 }
 
 // Half-wave layout (slices with no MFMA geometry): two rows in flight per
@@ -493,11 +597,13 @@ static hipError_t launch_halfwave(const uint16_t* x, const uint8_t* w, const uin
 }
 
 hipError_t launch_gemv_m1(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws, int N,
-                          int K, int gps, int sk, bool force_halfwave, hipStream_t stream) {
+                          int K, int gps, int sk, bool force_halfwave, hipStream_t stream,
+                          const LoraArgs* la) {
   int R = 0, I = 0;
+  if (la != nullptr && (force_halfwave || !gemv_mfma_fits(gps))) return hipErrorInvalidValue;
   if (!force_halfwave && mfma_geometry(gps, &R, &I)) {
 #define W4A16_RI(RR, II) \
-  if (R == RR && I == II) return launch_mfma_ri<RR, II>(x, w, s, y, ws, N, K, gps, sk, stream);
+  if (R == RR && I == II) return launch_mfma_ri<RR, II>(x, w, s, y, ws, N, K, gps, sk, stream, la);
     W4A16_RI(1, 1) W4A16_RI(1, 2) W4A16_RI(1, 3) W4A16_RI(1, 4)
     W4A16_RI(2, 1) W4A16_RI(2, 3) W4A16_RI(2, 5) W4A16_RI(2, 7)
     W4A16_RI(4, 1) W4A16_RI(4, 3) W4A16_RI(4, 5) W4A16_RI(4, 7)

@@ -8,6 +8,8 @@
 
 namespace w4a16 {
 
+struct LoraArgs;   // lora.hpp: per-row adapters, which the projection's kernels add to their sums
+
 // Raises a kernel's dynamic-LDS limit to `bytes` on the current device, once
 // per device: `done` is the caller's per-kernel set of devices already set
 // (bit d = device d; a device index past 63 sets it on every call).
@@ -27,19 +29,24 @@ hipError_t launch_splitk_reduce(const float* ws, uint16_t* y, uint64_t mn, int s
 // M = 1 decode GEMV; gps = 128-groups per split-K slice (<= 64), sk slices;
 // ws == nullptr writes bf16 y, else fp32 partials ws[s, 0, :]. The MFMA layout
 // where the slice length has a tiling of 16 (row, group) pairs per
-// instruction, otherwise (or when forced) the half-wave layout.
+// instruction, otherwise (or when forced) the half-wave layout. la: the row's
+// adapter (MFMA layout only).
 hipError_t launch_gemv_m1(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
-                          int N, int K, int gps, int sk, bool force_halfwave, hipStream_t stream);
+                          int N, int K, int gps, int sk, bool force_halfwave, hipStream_t stream,
+                          const LoraArgs* la = nullptr);
+bool gemv_mfma_fits(int gps);   // the MFMA layout takes slices of gps groups
 
 // 1 <= M <= kSkinnyMaxRows decode on MFMA 16x16x32; nt column tiles of 16 per
 // wave (1 or 2), 8 waves per workgroup (past 32 rows only nt = 1).
 hipError_t launch_skinny(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
-                         int M, int N, int K, int gps, int sk, int nt, int waves, hipStream_t stream);
+                         int M, int N, int K, int gps, int sk, int nt, int waves, hipStream_t stream,
+                         const LoraArgs* la = nullptr);
 
 // 1 <= M <= 16 decode with X and the weights staged in LDS by DMA (skinny_lds.hip)
 bool skinny_lds_fits(int M, int gps);
 hipError_t launch_skinny_lds(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws, int M,
-                             int N, int K, int gps, int sk, int geometry, hipStream_t stream);
+                             int N, int K, int gps, int sk, int geometry, hipStream_t stream,
+                             const LoraArgs* la = nullptr);
 
 // slices of at most this many groups stage their scales in LDS (16 NT x gps x 2
 // bytes, at most 32 KiB)
@@ -57,23 +64,20 @@ hipError_t launch_rowsum_neg136(const uint16_t* x, float* out, int M, int K, int
 // (m_sizes == nullptr, m_uniform == 0, G == 1), grouped (rows per weight group
 // in m_sizes on the device) or batched (G weight groups of m_uniform rows
 // each). With ws != nullptr (plain and batched) slice s of gridDim.y = sk
-// writes fp32 partials ws[s, :, :]. sxn: the -136 * row sums [K/gsize, ld] of
+// writes fp32 partials ws[s, :, :]. la (plain): per-row adapters, added in
+// slice 0. sxn: the -136 * row sums [K/gsize, ld] of
 // launch_rowsum_neg136, or nullptr for the kernel to form them itself.
 hipError_t launch_tile(const uint16_t* x, const uint8_t* w, const uint16_t* s, const float* sxn, int ld, uint16_t* y,
                        float* ws, const int32_t* m_sizes, int m_uniform, int M_total, int N, int K, int G, int gps,
-                       int sk, int bm, int gsize, hipStream_t stream);
+                       int sk, int bm, int gsize, hipStream_t stream, const LoraArgs* la = nullptr);
 // whether the tile kernel is built for bm-row tiles at scale group gsize
 bool tile_rows_ok(int bm, int gsize);
 constexpr int kTileCols = 256;
 
 // ---- low-rank adapters beside the projection (lora.hip)
-constexpr int kLoraMaxRank = 128;
-// hp[s, m, r] = sc * partial sum of x[m, :] . A[ids[m], r, :] over K slice s of ks (gps 128-groups each)
+// h[2, M, R]: sc * x[m, :] . A[ids[m], r, :] as two bf16 parts (rows with an adapter only)
 hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
-                              float* hp, int M, int K, int L, int R, int gps, int ks, hipStream_t stream);
-// y = bf16(sum of the sk slices ws[s, m, n] + sum_r h[m, r] B[ids[m], n, r])
-hipError_t launch_lora_expand(const float* ws, const float* hp, const uint16_t* b, const int32_t* ids, uint16_t* y,
-                              int M, int N, int L, int R, int sk, int ks, hipStream_t stream);
+                              uint16_t* h, int M, int K, int L, int R, hipStream_t stream);
 
 // ---- rows of a mixture of experts (experts.hip)
 constexpr int kExpertMaxGroups = 4096;

@@ -1,0 +1,230 @@
+// The adapter term of a 16-row MFMA epilogue: acc += h . B[l]^T for the rows of
+// each adapter l, in the accumulators of a projection kernel, before its one
+// rounding (lora.hip states the operation and forms h).
+#pragma once
+
+#include "common.hpp"
+
+namespace w4a16 {
+
+constexpr int kLoraMaxRank = 128;
+
+struct LoraArgs {
+  const uint16_t* h;    // [2, M, R] bf16: h as the sum of its rounding and the rounding of what is left
+  const uint16_t* b;    // [L, N, R] bf16
+  const int32_t* ids;   // [M], outside [0, L): no adapter
+  int M, N, L, R;
+};
+
+// The adapters of the rows of a 16 MS-row tile, one after another: id[q] is the
+// adapter of row 64 q + lane (-1: none).
+template <int MS>
+struct LoraRows {
+  static constexpr int Q = (16 * MS + 63) / 64;
+  uint64_t todo[Q];
+  int turn = 0;
+  __device__ __forceinline__ explicit LoraRows(const int (&id)[Q]) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) todo[q] = __ballot(id[q] >= 0);
+  }
+  // The next adapter (in the order of their first row) whose turn is `part` of
+  // `nparts`: its id, or -1 when none is left, and its rows.
+  __device__ __forceinline__ int next(const int (&id)[Q], uint64_t (&rows)[Q], int part, int nparts) {
+    for (;;) {
+      int l = -1;
+#pragma unroll
+      for (int q = Q - 1; q >= 0; --q)
+        if (todo[q] != 0) l = __builtin_amdgcn_readlane(id[q], __builtin_ctzll(todo[q]));
+      if (l < 0) return -1;
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        rows[q] = __ballot(id[q] == l);
+        todo[q] &= ~rows[q];
+      }
+      const bool own = turn == part;
+      turn = turn + 1 == nparts ? 0 : turn + 1;
+      if (own) return l;
+    }
+  }
+};
+
+// B fragments of adapter l: column n0 + 16 ns + lane % 16, ranks 32 st + 8
+// (lane / 16) + 0..7; zeros past N and past R.
+template <int SN, int NS>
+__device__ __forceinline__ void lora_load_b(bf16x8 (&bf)[NS][SN], const LoraArgs& la, int l, int n0, int lane) {
+  const int m16 = lane & 15, kb = lane >> 4;
+  const __amdgpu_buffer_rsrc_t rbuf =
+      make_rsrc(la.b + (size_t)l * la.N * la.R, (uint32_t)la.N * (uint32_t)la.R * 2u);
+#pragma unroll
+  for (int st = 0; st < NS; ++st)
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) {
+      const int n = n0 + 16 * ns + m16, r = 32 * st + 8 * kb;
+      const uint32_t off = r < la.R && n < la.N ? ((uint32_t)n * (uint32_t)la.R + (uint32_t)r) * 2u : 0xFFFFFFF0u;
+      bf[st][ns] = __builtin_bit_cast(bf16x8, ld128(rbuf, off));
+    }
+}
+
+// acc += h . B^T for the rows `mine` (bit 4 (lane / 16) + i: the lane's row i).
+// The product is formed apart and selected by row, so that another adapter's
+// infinities or NaN reach no row.
+template <int SN, int NS>
+__device__ __forceinline__ void lora_mac(f32x4 (&acc)[SN], const u32x4 (&hi)[NS], const u32x4 (&lo)[NS],
+                                         const bf16x8 (&bf)[NS][SN], uint32_t mine, int kb) {
+  f32x4 d[SN];
+#pragma unroll
+  for (int ns = 0; ns < SN; ++ns) d[ns] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int st = 0; st < NS; ++st) {
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns)
+      d[ns] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, hi[st]), bf[st][ns], d[ns], 0, 0, 0);
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns)
+      d[ns] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lo[st]), bf[st][ns], d[ns], 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool own = (mine >> (4 * kb + i)) & 1;
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) acc[ns][i] += own ? d[ns][i] : 0.0f;
+  }
+}
+
+// ---- tile kernels: h of the tile's rows staged in LDS, read by every wave.
+// Row r holds the ranks up to 32 NS (zeros past R) and is 16 bytes longer, an
+// odd multiple of 16 bytes, so that the 16 rows of a fragment read spread over
+// the banks; the part that is left follows behind the rows' leading part, and
+// the rows' adapters behind both. The row length is a constant: every fragment
+// read is one base register and an immediate (with a row length from R the
+// addresses of all row tiles stayed live across the adapters and the 144-row
+// tile spilled).
+constexpr int lora_row_bytes(int NS) { return 64 * NS + 16; }
+constexpr int lora_lds_bytes(int rows) { return rows * (2 * lora_row_bytes(kLoraMaxRank / 32) + 4); }
+
+template <int MS, int SN, int NS, int NTHR>
+__device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds, const LoraArgs& la, int row0, int live,
+                                             int n0, int tid) {
+  constexpr int ROWS = 16 * MS, Q = LoraRows<MS>::Q, RB = lora_row_bytes(NS), OCT = 4 * NS;
+  int32_t* sid = reinterpret_cast<int32_t*>(lds + 2 * ROWS * RB);
+  for (int r = tid; r < ROWS; r += NTHR) {
+    const int id = r < live ? la.ids[row0 + r] : -1;
+    sid[r] = (uint32_t)id < (uint32_t)la.L ? id : -1;
+  }
+  // (rows without an adapter hold any bits and are never selected)
+  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
+  const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
+  constexpr int IT = (ROWS * OCT + NTHR - 1) / NTHR;
+  u32x4 a[IT], b[IT];
+#pragma unroll
+  for (int u = 0; u < IT; ++u) {
+    const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
+    const bool ok = r < live && 8 * o < la.R;
+    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)o) * 2u;
+    a[u] = ld128(rh, ok ? off : 0xFFFFFFF0u);
+    b[u] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
+  }
+#pragma unroll
+  for (int u = 0; u < IT; ++u) {
+    const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
+    if (ROWS * OCT % NTHR == 0 || r < ROWS) {
+      *reinterpret_cast<u32x4*>(lds + r * RB + 16 * o) = a[u];
+      *reinterpret_cast<u32x4*>(lds + (ROWS + r) * RB + 16 * o) = b[u];
+    }
+  }
+  __syncthreads();
+
+  const int lane = tid & 63, m16 = lane & 15, kb = lane >> 4;
+  int id[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) id[q] = 64 * q + lane < ROWS ? sid[64 * q + lane] : -1;
+  LoraRows<MS> adapters(id);
+  const uint8_t* base = lds + m16 * RB + 16 * kb;
+  for (;;) {
+    uint64_t rows[Q];
+    const int l = adapters.next(id, rows, 0, 1);
+    if (l < 0) break;
+    bf16x8 bf[NS][SN];
+    lora_load_b<SN, NS>(bf, la, l, n0, lane);
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms) {
+      const uint32_t mine = (uint32_t)(rows[ms / 4] >> (16 * (ms % 4))) & 0xFFFFu;
+      if (mine != 0) {
+        u32x4 hi[NS], lo[NS];
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+          hi[st] = *reinterpret_cast<const u32x4*>(base + 16 * ms * RB + 64 * st);
+          lo[st] = *reinterpret_cast<const u32x4*>(base + (ROWS + 16 * ms) * RB + 64 * st);
+        }
+        lora_mac<SN, NS>(acc[ms], hi, lo, bf, mine, kb);
+      }
+    }
+  }
+}
+
+template <int MS, int SN, int NTHR>
+__device__ __forceinline__ void lora_tile(f32x4 (&acc)[MS][SN], uint8_t* lds, const LoraArgs& la, int row0, int live,
+                                          int n0, int tid) {
+  if (la.R <= 32) lora_tile_ns<MS, SN, 1, NTHR>(acc, lds, la, row0, live, n0, tid);
+  else if (la.R <= 64) lora_tile_ns<MS, SN, 2, NTHR>(acc, lds, la, row0, live, n0, tid);
+  else lora_tile_ns<MS, SN, 4, NTHR>(acc, lds, la, row0, live, n0, tid);
+}
+
+// ---- small batch (M <= 16 MS rows): h read straight into the fragments by the
+// waves that hold an adapter, `part` of `nparts`; 4 / NS adapters' B fragments
+// are in flight at once, the first ones together with h.
+template <int MS, int SN, int NS>
+__device__ __forceinline__ void lora_rows_ns(f32x4 (&acc)[MS][SN], const LoraArgs& la, const int (&id)[1], int n0,
+                                             int lane, int part, int nparts) {
+  constexpr int NB = 4 / NS;
+  const int m16 = lane & 15, kb = lane >> 4;
+  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
+  const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
+  u32x4 hi[MS][NS], lo[MS][NS];
+  LoraRows<MS> adapters(id);
+  for (bool first = true;; first = false) {
+    int l[NB];
+    uint64_t rows[NB][1];
+    bf16x8 bf[NB][NS][SN];
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      l[k] = (k == 0 || l[k > 0 ? k - 1 : 0] >= 0) ? adapters.next(id, rows[k], part, nparts) : -1;
+      if (l[k] >= 0) lora_load_b<SN, NS>(bf[k], la, l[k], n0, lane);
+    }
+    if (l[0] < 0) return;
+    if (first) {
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+          const int r = 32 * st + 8 * kb, m = 16 * ms + m16;
+          const bool ok = m < la.M && r < la.R;
+          const uint32_t off = ((uint32_t)m * (uint32_t)la.R + (uint32_t)r) * 2u;
+          hi[ms][st] = ld128(rh, ok ? off : 0xFFFFFFF0u);
+          lo[ms][st] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (l[k] < 0) return;
+#pragma unroll
+      for (int ms = 0; ms < MS; ++ms) {
+        const uint32_t mine = (uint32_t)(rows[k][0] >> (16 * ms)) & 0xFFFFu;
+        if (mine != 0) lora_mac<SN, NS>(acc[ms], hi[ms], lo[ms], bf[k], mine, kb);
+      }
+    }
+  }
+}
+
+template <int MS, int SN>
+__device__ __forceinline__ void lora_rows(f32x4 (&acc)[MS][SN], const LoraArgs& la, int n0, int lane, int part,
+                                          int nparts) {
+  static_assert(MS <= 4, "one row per lane");
+  const int i = lane < la.M && lane < 16 * MS ? la.ids[lane] : -1;
+  const int id[1] = {(uint32_t)i < (uint32_t)la.L ? i : -1};
+  if (la.R <= 32) lora_rows_ns<MS, SN, 1>(acc, la, id, n0, lane, part, nparts);
+  else if (la.R <= 64) lora_rows_ns<MS, SN, 2>(acc, la, id, n0, lane, part, nparts);
+  else lora_rows_ns<MS, SN, 4>(acc, la, id, n0, lane, part, nparts);
+}
+
+}  // namespace w4a16

@@ -40,6 +40,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 #include "tilemap.hpp"
 
 namespace w4a16 {
@@ -90,8 +91,10 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds_dst
 
 }  // namespace
 
-template <int NSTAGE, int MS, int GS, bool RSK>
-__global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs args) {
+// LA: nothing, or the LoraArgs of per-row adapters, whose products join the
+// accumulators of K slice 0 before the epilogue (plain calls only).
+template <int NSTAGE, int MS, int GS, bool RSK, class... LA>
+__global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs args, const LA... la) {
   static_assert(NSTAGE == 3, "stages: the row sums of group j + 1 are formed while group j + 2 is in flight");
   static_assert(MS >= 2 && MS <= 16, "row tiles");
   static_assert(GS == 128 || GS == 32, "scale group");
@@ -480,6 +483,15 @@ __global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs arg
     }
   }
 
+  // ---- adapters (the stages are free once every wave is past its last group)
+  if constexpr (sizeof...(LA) > 0) {
+    static_assert(lora_lds_bytes(BM) <= NSTAGE * ST::kBytes, "staged rows fit the stages' LDS");
+    if (slice == 0) {
+      __syncthreads();
+      (lora_tile<MS, SN, 64 * kNW>(acc, lds, la, row0, rows, n0 + TN * wv, tid), ...);
+    }
+  }
+
   // ---- epilogue: lane holds rows 16 ms + 4 kb + i of column TN wv + 16 ns + m16
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(args.y + (size_t)row0 * args.N, (uint32_t)rows * (uint32_t)args.N * 2u);
   const __amdgpu_buffer_rsrc_t rws =
@@ -591,13 +603,13 @@ hipError_t launch_rowsum_neg136(const uint16_t* x, float* out, int M, int K, int
   return hipGetLastError();
 }
 
-template <int NSTAGE, int MS, int GS, bool RSK>
-static hipError_t launch_prefill_rsk(PrefillArgs a, int sk, hipStream_t stream) {
+template <int NSTAGE, int MS, int GS, bool RSK, class... LA>
+static hipError_t launch_prefill_rsk(PrefillArgs a, int sk, hipStream_t stream, LA... la) {
   constexpr int BM = Stage<MS, GS>::kRows;
   const int lds_bytes = NSTAGE * Stage<MS, GS>::kBytes;
   static std::atomic<uint64_t> lds_set{0};   // per instantiation and device
   const hipError_t ea =
-      ensure_dyn_lds(reinterpret_cast<const void*>(&prefill_kernel<NSTAGE, MS, GS, RSK>), lds_bytes, lds_set);
+      ensure_dyn_lds(reinterpret_cast<const void*>(&prefill_kernel<NSTAGE, MS, GS, RSK, LA...>), lds_bytes, lds_set);
   if (ea != hipSuccess) return ea;
   a.mtiles = a.m_uniform > 0 ? a.G * ((a.m_uniform + BM - 1) / BM)
                              : (a.M_total + BM - 1) / BM + (a.m_sizes != nullptr ? a.G : 0);
@@ -605,14 +617,18 @@ static hipError_t launch_prefill_rsk(PrefillArgs a, int sk, hipStream_t stream) 
   const long long blocks = (long long)a.mtiles * a.ntiles;
   if (blocks <= 0) return hipSuccess;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((prefill_kernel<NSTAGE, MS, GS, RSK>), dim3((unsigned)blocks, sk), dim3(64 * kNW), lds_bytes,
-                     stream, a);
+  hipLaunchKernelGGL((prefill_kernel<NSTAGE, MS, GS, RSK, LA...>), dim3((unsigned)blocks, sk), dim3(64 * kNW),
+                     lds_bytes, stream, a, la...);
   return hipGetLastError();
 }
 
 // row sums formed in the kernel (sxn == nullptr) or taken from the pre-pass
 template <int NSTAGE, int MS, int GS = 128>
-static hipError_t launch_prefill_t(PrefillArgs a, int sk, hipStream_t stream) {
+static hipError_t launch_prefill_t(PrefillArgs a, int sk, hipStream_t stream, const LoraArgs* la) {
+  if (la != nullptr) {
+    if (a.sxn == nullptr) return launch_prefill_rsk<NSTAGE, MS, GS, true>(a, sk, stream, *la);
+    return launch_prefill_rsk<NSTAGE, MS, GS, false>(a, sk, stream, *la);
+  }
   if (a.sxn == nullptr) return launch_prefill_rsk<NSTAGE, MS, GS, true>(a, sk, stream);
   return launch_prefill_rsk<NSTAGE, MS, GS, false>(a, sk, stream);
 }
@@ -630,7 +646,7 @@ bool tile_rows_ok(int bm, int gsize) {
 
 hipError_t launch_tile(const uint16_t* x, const uint8_t* w, const uint16_t* s, const float* sxn, int ld, uint16_t* y,
                        float* ws, const int32_t* m_sizes, int m_uniform, int M_total, int N, int K, int G, int gps,
-                       int sk, int bm, int gsize, hipStream_t stream) {
+                       int sk, int bm, int gsize, hipStream_t stream, const LoraArgs* la) {
   if (!tile_rows_ok(bm, gsize)) return hipErrorInvalidValue;
   PrefillArgs a;
   a.x = x; a.w = w; a.s = s; a.sxn = sxn; a.y = y; a.ws = ws; a.m_sizes = m_sizes; a.m_uniform = m_uniform;
@@ -638,21 +654,21 @@ hipError_t launch_tile(const uint16_t* x, const uint8_t* w, const uint16_t* s, c
   a.mtiles = 0; a.ntiles = 0;
   if (gsize == 32) {
     switch (bm / 16) {
-      case 8: return launch_prefill_t<3, 8, 32>(a, sk, stream);   // 3 x 50.5 KiB stages
-      case 7: return launch_prefill_t<3, 7, 32>(a, sk, stream);
-      case 6: return launch_prefill_t<3, 6, 32>(a, sk, stream);
-      case 5: return launch_prefill_t<3, 5, 32>(a, sk, stream);
+      case 8: return launch_prefill_t<3, 8, 32>(a, sk, stream, la);   // 3 x 50.5 KiB stages
+      case 7: return launch_prefill_t<3, 7, 32>(a, sk, stream, la);
+      case 6: return launch_prefill_t<3, 6, 32>(a, sk, stream, la);
+      case 5: return launch_prefill_t<3, 5, 32>(a, sk, stream, la);
       default: return hipErrorInvalidValue;
     }
   }
   switch (bm / 16) {
-    case 9: return launch_prefill_t<3, 9>(a, sk, stream);     // 144 x 256 tiles, 3 x 52.6 KiB stages
-    case 8: return launch_prefill_t<3, 8>(a, sk, stream);     // 128 x 256 tiles, 3 x 48.5 KiB stages
-    case 7: return launch_prefill_t<3, 7>(a, sk, stream);     // 112 x 256 tiles, 3 x 44.4 KiB stages
-    case 6: return launch_prefill_t<3, 6>(a, sk, stream);     // 96 x 256 tiles, 3 x 40.4 KiB stages
-    case 5: return launch_prefill_t<3, 5>(a, sk, stream);     // 80 x 256 tiles, 3 x 36.3 KiB stages
-    case 4: return launch_prefill_t<3, 4>(a, sk, stream);     // 64 x 256 tiles, 3 x 32.3 KiB stages
-    case 3: return launch_prefill_t<3, 3>(a, sk, stream);     // 48 x 256 tiles, 3 x 28.2 KiB stages
+    case 9: return launch_prefill_t<3, 9>(a, sk, stream, la);     // 144 x 256 tiles, 3 x 52.6 KiB stages
+    case 8: return launch_prefill_t<3, 8>(a, sk, stream, la);     // 128 x 256 tiles, 3 x 48.5 KiB stages
+    case 7: return launch_prefill_t<3, 7>(a, sk, stream, la);     // 112 x 256 tiles, 3 x 44.4 KiB stages
+    case 6: return launch_prefill_t<3, 6>(a, sk, stream, la);     // 96 x 256 tiles, 3 x 40.4 KiB stages
+    case 5: return launch_prefill_t<3, 5>(a, sk, stream, la);     // 80 x 256 tiles, 3 x 36.3 KiB stages
+    case 4: return launch_prefill_t<3, 4>(a, sk, stream, la);     // 64 x 256 tiles, 3 x 32.3 KiB stages
+    case 3: return launch_prefill_t<3, 3>(a, sk, stream, la);     // 48 x 256 tiles, 3 x 28.2 KiB stages
     default: return hipErrorInvalidValue;
   }
 }

@@ -30,6 +30,7 @@
 // to ws[s, :, :] with plain stores; an empty slice writes zeros).
 #include "common.hpp"
 #include "launch.hpp"
+#include "lora.hpp"
 
 namespace w4a16 {
 
@@ -89,12 +90,15 @@ __device__ __forceinline__ void wait_stages(int later) {
 
 }  // namespace
 
-template <int SG, int NS>
+// LA: nothing, or the LoraArgs of per-row adapters, whose products join the
+// accumulators of K slice 0: the four waves of a column tile take the adapters
+// in turn, before their sums are added up.
+template <int SG, int NS, class... LA>
 __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_t* __restrict__ x,
                                                                    const uint8_t* __restrict__ w,
                                                                    const uint16_t* __restrict__ s,
                                                                    void* __restrict__ out, int M, int N, int K,
-                                                                   int gps) {
+                                                                   int gps, const LA... la) {
   using ST = SLStage<SG>;
   static_assert(SG == 4 || SG == 8, "groups per stage");
   static_assert(NS >= 3, "stages");
@@ -163,7 +167,8 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   const bf16x8 bneg = __builtin_bit_cast(bf16x8, u32x4{neg136, neg136, neg136, neg136});
 
   const int ct = wv & 1;                       // the wave's column tile
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc1[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+  f32x4& acc = acc1[0][0];
 
   // unit (ct, gl) of the stage in buffer b: X rows in A, column tile ct in B
   auto unit = [&](const uint8_t* sb, int gl, int g) {
@@ -228,6 +233,10 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
     }
   }
 
+  if constexpr (sizeof...(LA) > 0) {
+    if (slice == 0) (lora_rows<1, 1>(acc1, la, n0 + 16 * ct, lane, wv >> 1, 4), ...);
+  }
+
   // ---- the four waves of a column tile: summed in wave order (waves ct,
   // ct + 2, ct + 4, ct + 6), through LDS (the stages are free now)
   __syncthreads();
@@ -261,27 +270,35 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
 
 bool skinny_lds_fits(int M, int gps) { return M >= 1 && M <= 16 && gps >= 1; }
 
-template <int SG, int NS>
-static hipError_t launch_sl(const uint16_t* x, const uint8_t* w, const uint16_t* s, void* out, int M, int N, int K,
-                            int gps, int sk, hipStream_t stream) {
+template <int SG, int NS, class... LA>
+static hipError_t launch_sl_la(const uint16_t* x, const uint8_t* w, const uint16_t* s, void* out, int M, int N, int K,
+                               int gps, int sk, hipStream_t stream, LA... la) {
   constexpr int lds = NS * SLStage<SG>::kBytes;
   static std::atomic<uint64_t> lds_set{0};
-  const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&skinny_lds_kernel<SG, NS>), lds, lds_set);
+  const hipError_t ea =
+      ensure_dyn_lds(reinterpret_cast<const void*>(&skinny_lds_kernel<SG, NS, LA...>), lds, lds_set);
   if (ea != hipSuccess) return ea;
-  hipLaunchKernelGGL((skinny_lds_kernel<SG, NS>), dim3((N + kSLCols - 1) / kSLCols, sk), dim3(64 * kSLWaves), lds,
-                     stream, x, w, s, out, M, N, K, gps);
+  hipLaunchKernelGGL((skinny_lds_kernel<SG, NS, LA...>), dim3((N + kSLCols - 1) / kSLCols, sk), dim3(64 * kSLWaves),
+                     lds, stream, x, w, s, out, M, N, K, gps, la...);
   return hipGetLastError();
 }
 
+template <int SG, int NS>
+static hipError_t launch_sl(const uint16_t* x, const uint8_t* w, const uint16_t* s, void* out, int M, int N, int K,
+                            int gps, int sk, hipStream_t stream, const LoraArgs* la) {
+  if (la != nullptr) return launch_sl_la<SG, NS>(x, w, s, out, M, N, K, gps, sk, stream, *la);
+  return launch_sl_la<SG, NS>(x, w, s, out, M, N, K, gps, sk, stream);
+}
+
 hipError_t launch_skinny_lds(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws, int M,
-                             int N, int K, int gps, int sk, int geometry, hipStream_t stream) {
+                             int N, int K, int gps, int sk, int geometry, hipStream_t stream, const LoraArgs* la) {
   if (!skinny_lds_fits(M, gps)) return hipErrorInvalidValue;
   void* out = sk > 1 ? static_cast<void*>(ws) : static_cast<void*>(y);
   switch (geometry) {
-    case 0: return launch_sl<8, 3>(x, w, s, out, M, N, K, gps, sk, stream);   // 3 x 49 KiB
-    case 1: return launch_sl<4, 6>(x, w, s, out, M, N, K, gps, sk, stream);   // 6 x 24.5 KiB
-    case 2: return launch_sl<4, 5>(x, w, s, out, M, N, K, gps, sk, stream);
-    case 3: return launch_sl<4, 4>(x, w, s, out, M, N, K, gps, sk, stream);
+    case 0: return launch_sl<8, 3>(x, w, s, out, M, N, K, gps, sk, stream, la);   // 3 x 49 KiB
+    case 1: return launch_sl<4, 6>(x, w, s, out, M, N, K, gps, sk, stream, la);   // 6 x 24.5 KiB
+    case 2: return launch_sl<4, 5>(x, w, s, out, M, N, K, gps, sk, stream, la);
+    case 3: return launch_sl<4, 4>(x, w, s, out, M, N, K, gps, sk, stream, la);
     default: return hipErrorInvalidValue;
   }
 }

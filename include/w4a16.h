@@ -281,8 +281,8 @@ w4a16_status w4a16_splitk_reduce(const float* workspace, uint16_t* y,
  *                 any value outside [0, L) means none.
  *   scaling     : [L] fp32, device, 4-byte aligned, or NULL (all 1)
  *   L >= 1; R a multiple of 8, 8 <= R <= 128 (pad an adapter of another rank
- *   with zeros: W4A16_ERR_SHAPE otherwise); N * R * 2 < 2^32 bytes. a and b may
- *   be larger than 2^32 bytes. Adapters of the parts of a fused projection
+ *   with zeros: W4A16_ERR_SHAPE otherwise); N * R * 2 and M * R * 4 < 2^32
+ *   bytes. a and b may be larger than 2^32 bytes. Adapters of the parts of a fused projection
  *   (gate and up, or q, k and v) are one adapter of the ranks' sum, with zeros
  *   in B outside each part's columns.
  *   workspace   : fp32 device scratch, overwritten, never NULL when M > 0: at

@@ -3,18 +3,34 @@
 // rounding (lora.hip states the operation and forms h).
 #pragma once
 
+#include <utility>
+
 #include "common.hpp"
 
 namespace w4a16 {
 
 constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxSlices = 4;   // K slices of h (tile kernel)
 
 struct LoraArgs {
-  const uint16_t* h;    // [2, M, R] bf16: h as the sum of its rounding and the rounding of what is left
+  const void* h;        // decode kernels: [2, M, R] bf16, h as the sum of two bf16 values (its rounding and
+                        //   the rounding of what is left); tile kernel: [ks, M, R] fp32 slices of h over K
   const uint16_t* b;    // [L, N, R] bf16
   const int32_t* ids;   // [M], outside [0, L): no adapter
-  int M, N, L, R;
+  int M, N, L, R, ks;
 };
+
+// f(0) ... f(N - 1) with constant indices, whatever the size of the body (the
+// compiler left the loop over the row tiles rolled in some instances, their
+// accumulators indexed at run time)
+template <class F, int... I>
+__device__ __forceinline__ void static_for_each(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+  static_for_each(std::make_integer_sequence<int, N>{}, f);
+}
 
 // The adapters of the rows of a 16 MS-row tile, one after another: id[q] is the
 // adapter of row 64 q + lane (-1: none).
@@ -111,25 +127,39 @@ __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds,
     const int id = r < live ? la.ids[row0 + r] : -1;
     sid[r] = (uint32_t)id < (uint32_t)la.L ? id : -1;
   }
-  // (rows without an adapter hold any bits and are never selected)
-  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
-  const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
+  // the slices of h summed in order, then split into two bf16 values (rows
+  // without an adapter hold any bits and are never selected)
+  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 4u;
   constexpr int IT = (ROWS * OCT + NTHR - 1) / NTHR;
-  u32x4 a[IT], b[IT];
 #pragma unroll
   for (int u = 0; u < IT; ++u) {
     const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
     const bool ok = r < live && 8 * o < la.R;
-    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)o) * 2u;
-    a[u] = ld128(rh, ok ? off : 0xFFFFFFF0u);
-    b[u] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
-  }
+    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)o) * 4u;
+    float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    u32x4 a[kLoraMaxSlices], b[kLoraMaxSlices];
 #pragma unroll
-  for (int u = 0; u < IT; ++u) {
-    const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
+    for (int s = 0; s < kLoraMaxSlices; ++s) {   // slices past the last read zeros
+      const __amdgpu_buffer_rsrc_t rh =
+          make_rsrc(static_cast<const float*>(la.h) + (size_t)s * la.M * la.R, s < la.ks ? plane : 0u);
+      a[s] = ld128(rh, ok ? off : 0xFFFFFFE0u);
+      b[s] = ld128(rh, ok ? off + 16u : 0xFFFFFFF0u);
+    }
+#pragma unroll
+    for (int s = 0; s < kLoraMaxSlices; ++s) {
+      const uint32_t w[8] = {a[s].x, a[s].y, a[s].z, a[s].w, b[s].x, b[s].y, b[s].z, b[s].w};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) h[q] += __uint_as_float(w[q]);
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      hi[q] = pack_bf16x2(h[2 * q], h[2 * q + 1]);
+      lo[q] = pack_bf16x2(h[2 * q] - bf16lo(hi[q]), h[2 * q + 1] - bf16hi(hi[q]));
+    }
     if (ROWS * OCT % NTHR == 0 || r < ROWS) {
-      *reinterpret_cast<u32x4*>(lds + r * RB + 16 * o) = a[u];
-      *reinterpret_cast<u32x4*>(lds + (ROWS + r) * RB + 16 * o) = b[u];
+      *reinterpret_cast<u32x4*>(lds + r * RB + 16 * o) = u32x4{hi[0], hi[1], hi[2], hi[3]};
+      *reinterpret_cast<u32x4*>(lds + (ROWS + r) * RB + 16 * o) = u32x4{lo[0], lo[1], lo[2], lo[3]};
     }
   }
   __syncthreads();
@@ -140,24 +170,32 @@ __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds,
   for (int q = 0; q < Q; ++q) id[q] = 64 * q + lane < ROWS ? sid[64 * q + lane] : -1;
   LoraRows<MS> adapters(id);
   const uint8_t* base = lds + m16 * RB + 16 * kb;
+  constexpr int NB = 4 / NS;   // adapters whose B fragments are in flight at once
   for (;;) {
-    uint64_t rows[Q];
-    const int l = adapters.next(id, rows, 0, 1);
-    if (l < 0) break;
-    bf16x8 bf[NS][SN];
-    lora_load_b<SN, NS>(bf, la, l, n0, lane);
+    int l[NB];
+    uint64_t rows[NB][Q];
+    bf16x8 bf[NB][NS][SN];
 #pragma unroll
-    for (int ms = 0; ms < MS; ++ms) {
-      const uint32_t mine = (uint32_t)(rows[ms / 4] >> (16 * (ms % 4))) & 0xFFFFu;
-      if (mine != 0) {
-        u32x4 hi[NS], lo[NS];
+    for (int k = 0; k < NB; ++k) {
+      l[k] = (k == 0 || l[k > 0 ? k - 1 : 0] >= 0) ? adapters.next(id, rows[k], 0, 1) : -1;
+      if (l[k] >= 0) lora_load_b<SN, NS>(bf[k], la, l[k], n0, lane);
+    }
 #pragma unroll
-        for (int st = 0; st < NS; ++st) {
-          hi[st] = *reinterpret_cast<const u32x4*>(base + 16 * ms * RB + 64 * st);
-          lo[st] = *reinterpret_cast<const u32x4*>(base + (ROWS + 16 * ms) * RB + 64 * st);
+    for (int k = 0; k < NB; ++k) {
+      if (l[k] < 0) return;
+      static_for<MS>([&](auto i) {
+        constexpr int ms = decltype(i)::value;
+        const uint32_t mine = (uint32_t)(rows[k][ms / 4] >> (16 * (ms % 4))) & 0xFFFFu;
+        if (mine != 0) {
+          u32x4 hi[NS], lo[NS];
+#pragma unroll
+          for (int st = 0; st < NS; ++st) {
+            hi[st] = *reinterpret_cast<const u32x4*>(base + 16 * ms * RB + 64 * st);
+            lo[st] = *reinterpret_cast<const u32x4*>(base + (ROWS + 16 * ms) * RB + 64 * st);
+          }
+          lora_mac<SN, NS>(acc[ms], hi, lo, bf[k], mine, kb);
         }
-        lora_mac<SN, NS>(acc[ms], hi, lo, bf, mine, kb);
-      }
+      });
     }
   }
 }

@@ -94,6 +94,11 @@ CASES = [
     (257, 513, 256, 32, 120, 6, "rand", 1),
     (300, 64, 128, 128, 16, 2, "none", 0),
     (1000, 40, 256, 128, 88, 3, "holes", 0),
+    (4500, 48, 256, 128, 16, 5, "holes", 1),     # more rows than one grouping block
+    (9000, 16, 128, 128, 8, 700, "rand", 0),
+    (300, 64, 256, 128, 24, 9000, "holes", 0),   # more adapters than the grouping counts
+    (70, 40, 640, 32, 8, 8193, "each", 0),
+    (8, 520, 1024, 32, 128, 8, "each", 4),
 ]
 
 

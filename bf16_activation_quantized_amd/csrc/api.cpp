@@ -483,8 +483,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 struct LoraPlan {
   Plan base;       // the projection
-  int32_t ks;      // K slices of x . A^T (1 for the decode kernels)
-  uint64_t ws_h;   // its bytes, ahead of the projection's workspace
+  uint64_t ws_h;   // bytes of the [2, M, R] bf16 parts of x . A^T, ahead of the projection's workspace
 };
 
 w4a16_status make_lora_plan(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t L, int32_t R,
@@ -506,8 +505,7 @@ w4a16_status make_lora_plan(int64_t M, int64_t N, int64_t K, int32_t group_size,
     if (st != W4A16_OK) return st;
   }
   if (p->base.ws_split > kMaxBytes) return W4A16_ERR_SHAPE;
-  p->ks = p->base.path == kPathTile ? w4a16::lora_shrink_slices((int)M, (int)K, L, R) : 1;
-  p->ws_h = round_up((uint64_t)p->ks * (uint64_t)M * (uint64_t)R * 4u, 256);
+  p->ws_h = round_up((uint64_t)M * (uint64_t)R * 4u, 256);
   return W4A16_OK;
 }
 
@@ -768,14 +766,10 @@ w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed, const u
   float* partials = reinterpret_cast<float*>(ws + p.ws_h);
   float* rowsums =
       p.base.ws_sx > 0 ? reinterpret_cast<float*>(ws + p.ws_h + round_up(p.base.ws_split, 256)) : nullptr;
-  const int iM = (int)M, iK = (int)K;
-  const hipError_t e =
-      p.base.path == kPathTile
-          ? w4a16::launch_lora_shrink_units(x, a, adapter_ids, scaling, workspace, iM, iK, L, R, p.ks, strm)
-          : w4a16::launch_lora_shrink_rows(x, a, adapter_ids, scaling, reinterpret_cast<uint16_t*>(ws), iM, iK, L, R,
-                                           strm);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws);
+  const hipError_t e = w4a16::launch_lora_shrink(x, a, adapter_ids, scaling, h, (int)M, (int)K, L, R, strm);
   if (e != hipSuccess) return W4A16_ERR_LAUNCH;
-  const w4a16::LoraArgs la = {ws, b, adapter_ids, iM, (int)N, L, R, p.ks};
+  const w4a16::LoraArgs la = {h, b, adapter_ids, (int)M, (int)N, L, R};
   return launch_plan(p.base, x, w_packed, scales, y, M, N, K, group_size, partials, rowsums, strm, &la);
 }
 

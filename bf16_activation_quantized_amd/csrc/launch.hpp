@@ -75,13 +75,9 @@ bool tile_rows_ok(int bm, int gsize);
 constexpr int kTileCols = 256;
 
 // ---- low-rank adapters beside the projection (lora.hip)
-// x . A^T for the decode kernels (few rows) and for the tile kernel, in ks
-// slices of K (layouts: LoraArgs)
-hipError_t launch_lora_shrink_rows(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
-                                   uint16_t* h, int M, int K, int L, int R, hipStream_t stream);
-int lora_shrink_slices(int M, int K, int L, int R);
-hipError_t launch_lora_shrink_units(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
-                                    float* hp, int M, int K, int L, int R, int ks, hipStream_t stream);
+// h = sc * x . A^T as two bf16 parts [2, M, R] (rows with an adapter only)
+hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
+                              uint16_t* h, int M, int K, int L, int R, hipStream_t stream);
 
 // ---- rows of a mixture of experts (experts.hip)
 constexpr int kExpertMaxGroups = 4096;

@@ -10,14 +10,12 @@
 namespace w4a16 {
 
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraMaxSlices = 4;   // K slices of h (tile kernel)
 
 struct LoraArgs {
-  const void* h;        // decode kernels: [2, M, R] bf16, h as the sum of two bf16 values (its rounding and
-                        //   the rounding of what is left); tile kernel: [ks, M, R] fp32 slices of h over K
+  const uint16_t* h;    // [2, M, R] bf16: h as its rounding and the rounding of what is left
   const uint16_t* b;    // [L, N, R] bf16
   const int32_t* ids;   // [M], outside [0, L): no adapter
-  int M, N, L, R, ks;
+  int M, N, L, R;
 };
 
 // f(0) ... f(N - 1) with constant indices, whatever the size of the body (the
@@ -107,7 +105,8 @@ __device__ __forceinline__ void lora_mac(f32x4 (&acc)[SN], const u32x4 (&hi)[NS]
   }
 }
 
-// ---- tile kernels: h of the tile's rows staged in LDS, read by every wave.
+// ---- tile kernels: h of the tile's rows staged in LDS, read by every wave;
+// part = K slice of nparts, so that the slices share the adapters.
 // Row r holds the ranks up to 32 NS (zeros past R) and is 16 bytes longer, an
 // odd multiple of 16 bytes, so that the 16 rows of a fragment read spread over
 // the banks; the part that is left follows behind the rows' leading part, and
@@ -120,46 +119,32 @@ constexpr int lora_lds_bytes(int rows) { return rows * (2 * lora_row_bytes(kLora
 
 template <int MS, int SN, int NS, int NTHR>
 __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds, const LoraArgs& la, int row0, int live,
-                                             int n0, int tid) {
+                                             int n0, int tid, int part, int nparts) {
   constexpr int ROWS = 16 * MS, Q = LoraRows<MS>::Q, RB = lora_row_bytes(NS), OCT = 4 * NS;
   int32_t* sid = reinterpret_cast<int32_t*>(lds + 2 * ROWS * RB);
   for (int r = tid; r < ROWS; r += NTHR) {
     const int id = r < live ? la.ids[row0 + r] : -1;
     sid[r] = (uint32_t)id < (uint32_t)la.L ? id : -1;
   }
-  // the slices of h summed in order, then split into two bf16 values (rows
-  // without an adapter hold any bits and are never selected)
-  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 4u;
+  // (rows without an adapter hold any bits and are never selected)
+  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
+  const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
   constexpr int IT = (ROWS * OCT + NTHR - 1) / NTHR;
+  u32x4 a[IT], b[IT];
 #pragma unroll
   for (int u = 0; u < IT; ++u) {
     const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
     const bool ok = r < live && 8 * o < la.R;
-    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)o) * 4u;
-    float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    u32x4 a[kLoraMaxSlices], b[kLoraMaxSlices];
+    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)o) * 2u;
+    a[u] = ld128(rh, ok ? off : 0xFFFFFFF0u);
+    b[u] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
+  }
 #pragma unroll
-    for (int s = 0; s < kLoraMaxSlices; ++s) {   // slices past the last read zeros
-      const __amdgpu_buffer_rsrc_t rh =
-          make_rsrc(static_cast<const float*>(la.h) + (size_t)s * la.M * la.R, s < la.ks ? plane : 0u);
-      a[s] = ld128(rh, ok ? off : 0xFFFFFFE0u);
-      b[s] = ld128(rh, ok ? off + 16u : 0xFFFFFFF0u);
-    }
-#pragma unroll
-    for (int s = 0; s < kLoraMaxSlices; ++s) {
-      const uint32_t w[8] = {a[s].x, a[s].y, a[s].z, a[s].w, b[s].x, b[s].y, b[s].z, b[s].w};
-#pragma unroll
-      for (int q = 0; q < 8; ++q) h[q] += __uint_as_float(w[q]);
-    }
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      hi[q] = pack_bf16x2(h[2 * q], h[2 * q + 1]);
-      lo[q] = pack_bf16x2(h[2 * q] - bf16lo(hi[q]), h[2 * q + 1] - bf16hi(hi[q]));
-    }
+  for (int u = 0; u < IT; ++u) {
+    const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
     if (ROWS * OCT % NTHR == 0 || r < ROWS) {
-      *reinterpret_cast<u32x4*>(lds + r * RB + 16 * o) = u32x4{hi[0], hi[1], hi[2], hi[3]};
-      *reinterpret_cast<u32x4*>(lds + (ROWS + r) * RB + 16 * o) = u32x4{lo[0], lo[1], lo[2], lo[3]};
+      *reinterpret_cast<u32x4*>(lds + r * RB + 16 * o) = a[u];
+      *reinterpret_cast<u32x4*>(lds + (ROWS + r) * RB + 16 * o) = b[u];
     }
   }
   __syncthreads();
@@ -170,14 +155,16 @@ __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds,
   for (int q = 0; q < Q; ++q) id[q] = 64 * q + lane < ROWS ? sid[64 * q + lane] : -1;
   LoraRows<MS> adapters(id);
   const uint8_t* base = lds + m16 * RB + 16 * kb;
-  constexpr int NB = 4 / NS;   // adapters whose B fragments are in flight at once
+  // adapters whose B fragments are in flight at once (in the registers that the
+  // accumulators of a short tile leave)
+  constexpr int NB = (MS <= 5 ? 8 : 4) / NS;
   for (;;) {
     int l[NB];
     uint64_t rows[NB][Q];
     bf16x8 bf[NB][NS][SN];
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
-      l[k] = (k == 0 || l[k > 0 ? k - 1 : 0] >= 0) ? adapters.next(id, rows[k], 0, 1) : -1;
+      l[k] = (k == 0 || l[k > 0 ? k - 1 : 0] >= 0) ? adapters.next(id, rows[k], part, nparts) : -1;
       if (l[k] >= 0) lora_load_b<SN, NS>(bf[k], la, l[k], n0, lane);
     }
 #pragma unroll
@@ -202,10 +189,10 @@ __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds,
 
 template <int MS, int SN, int NTHR>
 __device__ __forceinline__ void lora_tile(f32x4 (&acc)[MS][SN], uint8_t* lds, const LoraArgs& la, int row0, int live,
-                                          int n0, int tid) {
-  if (la.R <= 32) lora_tile_ns<MS, SN, 1, NTHR>(acc, lds, la, row0, live, n0, tid);
-  else if (la.R <= 64) lora_tile_ns<MS, SN, 2, NTHR>(acc, lds, la, row0, live, n0, tid);
-  else lora_tile_ns<MS, SN, 4, NTHR>(acc, lds, la, row0, live, n0, tid);
+                                          int n0, int tid, int part, int nparts) {
+  if (la.R <= 32) lora_tile_ns<MS, SN, 1, NTHR>(acc, lds, la, row0, live, n0, tid, part, nparts);
+  else if (la.R <= 64) lora_tile_ns<MS, SN, 2, NTHR>(acc, lds, la, row0, live, n0, tid, part, nparts);
+  else lora_tile_ns<MS, SN, 4, NTHR>(acc, lds, la, row0, live, n0, tid, part, nparts);
 }
 
 // ---- small batch (M <= 16 MS rows): h read straight into the fragments by the
@@ -254,12 +241,14 @@ __device__ __forceinline__ void lora_rows_ns(f32x4 (&acc)[MS][SN], const LoraArg
   }
 }
 
+// the adapter of row `lane`: a load at the kernel's start, used at its end
+__device__ __forceinline__ int lora_id(const LoraArgs& la, int lane) { return lane < la.M ? la.ids[lane] : -1; }
+
 template <int MS, int SN>
-__device__ __forceinline__ void lora_rows(f32x4 (&acc)[MS][SN], const LoraArgs& la, int n0, int lane, int part,
-                                          int nparts) {
+__device__ __forceinline__ void lora_rows(f32x4 (&acc)[MS][SN], const LoraArgs& la, int row_id, int n0, int lane,
+                                          int part, int nparts) {
   static_assert(MS <= 4, "one row per lane");
-  const int i = lane < la.M && lane < 16 * MS ? la.ids[lane] : -1;
-  const int id[1] = {(uint32_t)i < (uint32_t)la.L ? i : -1};
+  const int id[1] = {lane < 16 * MS && (uint32_t)row_id < (uint32_t)la.L ? row_id : -1};
   if (la.R <= 32) lora_rows_ns<MS, SN, 1>(acc, la, id, n0, lane, part, nparts);
   else if (la.R <= 64) lora_rows_ns<MS, SN, 2>(acc, la, id, n0, lane, part, nparts);
   else lora_rows_ns<MS, SN, 4>(acc, la, id, n0, lane, part, nparts);

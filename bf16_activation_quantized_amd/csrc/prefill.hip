@@ -92,7 +92,9 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds_dst
 }  // namespace
 
 // LA: nothing, or the LoraArgs of per-row adapters, whose products join the
-// accumulators of K slice 0 before the epilogue (plain calls only).
+// accumulators before the epilogue, dealt out over the K slices (plain calls
+// only; 64 x 8192 x 8192 with 64 adapters of rank 16, SK 8: 49 us with all of
+// them in slice 0).
 template <int NSTAGE, int MS, int GS, bool RSK, class... LA>
 __global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs args, const LA... la) {
   static_assert(NSTAGE == 3, "stages: the row sums of group j + 1 are formed while group j + 2 is in flight");
@@ -486,10 +488,8 @@ __global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs arg
   // ---- adapters (the stages are free once every wave is past its last group)
   if constexpr (sizeof...(LA) > 0) {
     static_assert(lora_lds_bytes(BM) <= NSTAGE * ST::kBytes, "staged rows fit the stages' LDS");
-    if (slice == 0) {
-      __syncthreads();
-      (lora_tile<MS, SN, 64 * kNW>(acc, lds, la, row0, rows, n0 + TN * wv, tid), ...);
-    }
+    __syncthreads();
+    (lora_tile<MS, SN, 64 * kNW>(acc, lds, la, row0, rows, n0 + TN * wv, tid, slice, (int)gridDim.y), ...);
   }
 
   // ---- epilogue: lane holds rows 16 ms + 4 kb + i of column TN wv + 16 ns + m16

@@ -44,8 +44,8 @@ __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, 
 // (M <= 4 XR <= 16 MT). The A-operand rows past them are never written in
 // the staging tile; they feed only output rows >= M, which are not stored.
 // LA: nothing, or the LoraArgs of per-row adapters, whose products join the
-// accumulators of K slice 0: the waves take the adapters in turn, before their
-// sums are added up.
+// accumulators: the waves of all K slices take the adapters in turn, before
+// their sums are added up.
 template <int NT, int WAVES, bool SLDS, int XR, int MT, class... LA>
 __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __restrict__ x,
                                                             const uint8_t* __restrict__ w,
@@ -66,6 +66,8 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __re
 
   const int wave = threadIdx.x >> 6;
   const int lane = threadIdx.x & 63;
+  int row_id = -1;
+  if constexpr (sizeof...(LA) > 0) ((row_id = lora_id(la, lane)), ...);
   const int col = lane & 15;
   const int kb = lane >> 4;
   const int G = K / kGroup;
@@ -258,7 +260,9 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __re
   }
 
   if constexpr (sizeof...(LA) > 0) {
-    if (slice == 0) (lora_rows<MT, NT>(acc, la, nb, lane, __builtin_amdgcn_readfirstlane(wave), WAVES), ...);
+    (lora_rows<MT, NT>(acc, la, row_id, nb, lane, __builtin_amdgcn_readfirstlane(wave) + WAVES * slice,
+                       WAVES * (int)gridDim.y),
+     ...);
   }
 
   // cross-wave reduction: waves 1.. park their tiles in LDS, wave 0 sums

@@ -91,8 +91,8 @@ __device__ __forceinline__ void wait_stages(int later) {
 }  // namespace
 
 // LA: nothing, or the LoraArgs of per-row adapters, whose products join the
-// accumulators of K slice 0: the four waves of a column tile take the adapters
-// in turn, before their sums are added up.
+// accumulators: the four waves of a column tile, in all K slices, take the
+// adapters in turn, before their sums are added up.
 template <int SG, int NS, class... LA>
 __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_t* __restrict__ x,
                                                                    const uint8_t* __restrict__ w,
@@ -106,6 +106,8 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int row_id = -1;
+  if constexpr (sizeof...(LA) > 0) ((row_id = lora_id(la, lane)), ...);
   const int m16 = lane & 15, kb = lane >> 4;
   const uint32_t xs = xswz(m16);   // this lane's row swizzle in both operands
   const int G = K / kGroup;
@@ -234,7 +236,7 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   }
 
   if constexpr (sizeof...(LA) > 0) {
-    if (slice == 0) (lora_rows<1, 1>(acc1, la, n0 + 16 * ct, lane, wv >> 1, 4), ...);
+    (lora_rows<1, 1>(acc1, la, row_id, n0 + 16 * ct, lane, (wv >> 1) + 4 * slice, 4 * (int)gridDim.y), ...);
   }
 
   // ---- the four waves of a column tile: summed in wave order (waves ct,

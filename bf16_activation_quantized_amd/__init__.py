@@ -307,31 +307,55 @@ def w4a16_splitk_reduce(workspace: torch.Tensor, y: Optional[torch.Tensor] = Non
 
 
 # ------------------------------------------------------------------ low-rank adapters, rows of a mixture of experts
+# These calls are short (a few us on the GPU), so their checks are one pass
+# over each tensor's own attributes.
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
+def _in(t, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this type and shape on device
+    `dev`; raises what `_check` raises, or ValueError for another device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _check(t, name, dtype, shape)
+    raise ValueError(f"{name} is on device {t.get_device()}, the first argument on device {dev}")
+
+
+def _rank(t, name: str, dtype, dims: int):
+    """Shape of a tensor of `dims` dimensions (its other checks: `_in`)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        _check(t, name, dtype)
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """torch.empty from the memory pool of the stream that will write it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
-            torch.cuda.default_stream(device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else \
+            torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _call(name: str, tensors, stream, *args) -> None:
-    """Calls a C entry point with the tensors' device current (they all have to
-    be on one device), on `stream` or that device's current stream."""
-    device = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: tensors on {device} and {t.device}")
-    f = getattr(_lib(), name)
-    if device.index == torch.cuda.current_device():
-        _raise(f(*args, _stream(stream)), name)
+# the current stream of a device as an address, without building a Stream object
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _run(name: str, dev: int, stream, *args) -> None:
+    """Calls a C entry point with device `dev` current, on `stream` or that
+    device's current stream."""
+    f = getattr(_lib_handle or _lib(), name)
+    raw = _current_raw_stream(dev) if stream is None else _stream(stream)
+    if dev == torch.cuda.current_device():
+        status = f(*args, raw)
     else:
-        with torch.cuda.device(device):
-            _raise(f(*args, _stream(stream)), name)
+        with torch.cuda.device(dev):
+            status = f(*args, raw)
+    if status != 0:
+        raise W4A16Error(status, name)
 
 
 def w4a16_gemm_lora_workspace_bytes(M: int, N: int, K: int, L: int, R: int, split_k: int = 0,
@@ -348,29 +372,32 @@ def w4a16_gemm_lora(x: torch.Tensor, w_packed: torch.Tensor, scales: torch.Tenso
     rounding: Y[m] = X[m] . dequant(W)^T + scaling[l] (X[m] . A[l]^T) . B[l]^T,
     l = adapter_ids[m] (int32 [M]; outside [0, L): no adapter), a [L, R, K],
     b [L, N, R], scaling fp32 [L] or None (all 1)."""
-    _check(x, "x", torch.bfloat16)
-    M, K = x.shape
-    N = w_packed.shape[0]
-    _check(w_packed, "w_packed", torch.uint8, (N, K // 2))
-    _check(scales, "scales", torch.bfloat16, (N, K // group_size))
-    _check(a, "a", torch.bfloat16)
-    L, R = a.shape[0], a.shape[1]
-    _check(a, "a", torch.bfloat16, (L, R, K))
-    _check(b, "b", torch.bfloat16, (L, N, R))
-    _check(adapter_ids, "adapter_ids", torch.int32, (M,))
-    if scaling is not None:
-        _check(scaling, "scaling", torch.float32, (L,))
+    bf16 = torch.bfloat16
+    M, K = _rank(x, "x", bf16, 2)
+    N = _rank(w_packed, "w_packed", torch.uint8, 2)[0]
+    L, R, _ = _rank(a, "a", bf16, 3)
+    dev = x.get_device()
+    px = _in(x, "x", bf16, (M, K), dev)
+    pw = _in(w_packed, "w_packed", torch.uint8, (N, K // 2), dev)
+    ps = _in(scales, "scales", bf16, (N, K // group_size), dev)
+    pa = _in(a, "a", bf16, (L, R, K), dev)
+    pb = _in(b, "b", bf16, (L, N, R), dev)
+    pi = _in(adapter_ids, "adapter_ids", torch.int32, (M,), dev)
+    pc = None if scaling is None else _in(scaling, "scaling", torch.float32, (L,), dev)
     if y is None:
-        y = _empty((M, N), torch.bfloat16, x.device, stream)
-    _check(y, "y", torch.bfloat16, (M, N))
+        y = _empty((M, N), bf16, x, stream)
+    py = _in(y, "y", bf16, (M, N), dev)
     if workspace is None:
         need = _lib().w4a16_gemm_lora_workspace_bytes(M, N, K, group_size, L, R, split_k)
-        workspace = _empty((need // 4,), torch.float32, x.device, stream)
-    _check(workspace, "workspace", torch.float32)
-    _call("w4a16_gemm_lora", (x, w_packed, scales, a, b, adapter_ids, scaling, y, workspace), stream, _ptr(x),
-          _ptr(w_packed), _ptr(scales), _ptr(a), _ptr(b), _ptr(adapter_ids), _ptr(scaling), _ptr(y), M, N, K,
-          group_size, L, R, split_k, _ptr(workspace), workspace.numel() * 4)
+        workspace = _empty((need // 4,), torch.float32, x, stream)
+    pws, nws = _in(workspace, "workspace", torch.float32, workspace.shape, dev), workspace.numel()
+    _run("w4a16_gemm_lora", dev, stream, px, pw, ps, pa, pb, pi, pc, py, M, N, K, group_size, L, R, split_k, pws,
+         nws * 4)
     return y
+
+
+def w4a16_expert_sort_workspace_bytes(T: int, k: int, G: int) -> int:
+    return int(_lib().w4a16_expert_sort_workspace_bytes(T, k, G))
 
 
 def w4a16_expert_sort(ids: torch.Tensor, G: int, order: Optional[torch.Tensor] = None,
@@ -379,74 +406,74 @@ def w4a16_expert_sort(ids: torch.Tensor, G: int, order: Optional[torch.Tensor] =
     """Slots of ids [T, k] (int32; outside [0, G): dropped) in expert order:
     (order [T k], pos [T, k], m_sizes [G]), all int32. m_sizes is the argument
     of w4a16_gemm_grouped, pos that of the gather and combine calls."""
-    _check(ids, "ids", torch.int32)
-    T, k = ids.shape
+    i32 = torch.int32
+    T, k = _rank(ids, "ids", i32, 2)
+    dev = ids.get_device()
+    pi = _in(ids, "ids", i32, (T, k), dev)
     if order is None:
-        order = _empty((T * k,), torch.int32, ids.device, stream)
+        order = _empty((T * k,), i32, ids, stream)
     if pos is None:
-        pos = _empty((T, k), torch.int32, ids.device, stream)
+        pos = _empty((T, k), i32, ids, stream)
     if m_sizes is None:
-        m_sizes = _empty((G,), torch.int32, ids.device, stream)
-    _check(order, "order", torch.int32, (T * k,))
-    _check(pos, "pos", torch.int32, (T, k))
-    _check(m_sizes, "m_sizes", torch.int32, (G,))
+        m_sizes = _empty((G,), i32, ids, stream)
+    po = _in(order, "order", i32, (T * k,), dev)
+    pp = _in(pos, "pos", i32, (T, k), dev)
+    pm = _in(m_sizes, "m_sizes", i32, (G,), dev)
     if workspace is None:
         need = _lib().w4a16_expert_sort_workspace_bytes(T, k, G)
-        workspace = _empty((need // 4,), torch.int32, ids.device, stream)
-    _check(workspace, "workspace", torch.int32)
-    _call("w4a16_expert_sort", (ids, order, pos, m_sizes, workspace), stream, _ptr(ids), _ptr(order), _ptr(pos),
-          _ptr(m_sizes), T, k, G, _ptr(workspace), workspace.numel() * 4)
+        if need > 0:
+            workspace = _empty((need // 4,), i32, ids, stream)
+    pws, nws = None, 0
+    if workspace is not None:
+        pws, nws = _in(workspace, "workspace", i32, workspace.shape, dev), workspace.numel()
+    _run("w4a16_expert_sort", dev, stream, pi, po, pp, pm, T, k, G, pws, nws * 4)
     return order, pos, m_sizes
-
-
-def w4a16_expert_sort_workspace_bytes(T: int, k: int, G: int) -> int:
-    return int(_lib().w4a16_expert_sort_workspace_bytes(T, k, G))
 
 
 def w4a16_expert_gather(x: torch.Tensor, pos: torch.Tensor, xs: Optional[torch.Tensor] = None,
                         stream=None) -> torch.Tensor:
     """xs[pos[t, j]] = x[t] (rows that no slot names are left as they were)."""
-    _check(x, "x", torch.bfloat16)
-    _check(pos, "pos", torch.int32)
-    T, k = pos.shape
-    width = x.shape[1]
-    _check(x, "x", torch.bfloat16, (T, width))
+    bf16 = torch.bfloat16
+    T, k = _rank(pos, "pos", torch.int32, 2)
+    width = _rank(x, "x", bf16, 2)[1]
+    dev = x.get_device()
+    px = _in(x, "x", bf16, (T, width), dev)
+    pp = _in(pos, "pos", torch.int32, (T, k), dev)
     if xs is None:
-        xs = _empty((T * k, width), torch.bfloat16, x.device, stream)
-    rows = xs.shape[0]
-    _check(xs, "xs", torch.bfloat16, (rows, width))
-    _call("w4a16_expert_gather", (x, pos, xs), stream, _ptr(x), _ptr(pos), _ptr(xs), T, k, rows, width)
+        xs = _empty((T * k, width), bf16, x, stream)
+    rows = _rank(xs, "xs", bf16, 2)[0]
+    _run("w4a16_expert_gather", dev, stream, px, pp, _in(xs, "xs", bf16, (rows, width), dev), T, k, rows, width)
     return xs
 
 
 def w4a16_expert_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, dx: Optional[torch.Tensor] = None,
                              stream=None) -> torch.Tensor:
     """dx[t] = sum_j dxs[pos[t, j]]: the gradient of w4a16_expert_gather."""
-    _check(dxs, "dxs", torch.bfloat16)
-    _check(pos, "pos", torch.int32)
-    T, k = pos.shape
-    rows, width = dxs.shape
+    bf16 = torch.bfloat16
+    T, k = _rank(pos, "pos", torch.int32, 2)
+    rows, width = _rank(dxs, "dxs", bf16, 2)
+    dev = dxs.get_device()
+    pd = _in(dxs, "dxs", bf16, (rows, width), dev)
+    pp = _in(pos, "pos", torch.int32, (T, k), dev)
     if dx is None:
-        dx = _empty((T, width), torch.bfloat16, dxs.device, stream)
-    _check(dx, "dx", torch.bfloat16, (T, width))
-    _call("w4a16_expert_gather_grad", (dxs, pos, dx), stream, _ptr(dxs), _ptr(pos), _ptr(dx), T, k, rows, width)
+        dx = _empty((T, width), bf16, dxs, stream)
+    _run("w4a16_expert_gather_grad", dev, stream, pd, pp, _in(dx, "dx", bf16, (T, width), dev), T, k, rows, width)
     return dx
 
 
 def w4a16_expert_combine(z: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
                          y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[t] = sum_j weights[t, j] z[pos[t, j]] (weights fp32 [T, k], or None: all 1)."""
-    _check(z, "z", torch.bfloat16)
-    _check(pos, "pos", torch.int32)
-    T, k = pos.shape
-    rows, width = z.shape
-    if weights is not None:
-        _check(weights, "weights", torch.float32, (T, k))
+    bf16 = torch.bfloat16
+    T, k = _rank(pos, "pos", torch.int32, 2)
+    rows, width = _rank(z, "z", bf16, 2)
+    dev = z.get_device()
+    pz = _in(z, "z", bf16, (rows, width), dev)
+    pp = _in(pos, "pos", torch.int32, (T, k), dev)
+    pw = None if weights is None else _in(weights, "weights", torch.float32, (T, k), dev)
     if y is None:
-        y = _empty((T, width), torch.bfloat16, z.device, stream)
-    _check(y, "y", torch.bfloat16, (T, width))
-    _call("w4a16_expert_combine", (z, pos, weights, y), stream, _ptr(z), _ptr(pos), _ptr(weights), _ptr(y), T, k,
-          rows, width)
+        y = _empty((T, width), bf16, z, stream)
+    _run("w4a16_expert_combine", dev, stream, pz, pp, pw, _in(y, "y", bf16, (T, width), dev), T, k, rows, width)
     return y
 
 
@@ -455,19 +482,19 @@ def w4a16_expert_combine_grad(dy: torch.Tensor, z: torch.Tensor, pos: torch.Tens
                               stream=None) -> tuple:
     """Gradients of w4a16_expert_combine: (dz, dweights). Rows of dz that no
     slot names are left as they were."""
-    _check(dy, "dy", torch.bfloat16)
-    _check(z, "z", torch.bfloat16)
-    _check(pos, "pos", torch.int32)
-    T, k = pos.shape
-    rows, width = z.shape
-    _check(dy, "dy", torch.bfloat16, (T, width))
-    _check(weights, "weights", torch.float32, (T, k))
+    bf16, f32 = torch.bfloat16, torch.float32
+    T, k = _rank(pos, "pos", torch.int32, 2)
+    rows, width = _rank(z, "z", bf16, 2)
+    dev = dy.get_device() if isinstance(dy, torch.Tensor) else -1
+    pd = _in(dy, "dy", bf16, (T, width), dev)
+    pz = _in(z, "z", bf16, (rows, width), dev)
+    pp = _in(pos, "pos", torch.int32, (T, k), dev)
+    pw = _in(weights, "weights", f32, (T, k), dev)
     if dz is None:
-        dz = _empty((rows, width), torch.bfloat16, z.device, stream)
+        dz = _empty((rows, width), bf16, z, stream)
     if dweights is None:
-        dweights = _empty((T, k), torch.float32, z.device, stream)
-    _check(dz, "dz", torch.bfloat16, (rows, width))
-    _check(dweights, "dweights", torch.float32, (T, k))
-    _call("w4a16_expert_combine_grad", (dy, z, pos, weights, dz, dweights), stream, _ptr(dy), _ptr(z), _ptr(pos),
-          _ptr(weights), _ptr(dz), _ptr(dweights), T, k, rows, width)
+        dweights = _empty((T, k), f32, z, stream)
+    pdz = _in(dz, "dz", bf16, (rows, width), dev)
+    pdw = _in(dweights, "dweights", f32, (T, k), dev)
+    _run("w4a16_expert_combine_grad", dev, stream, pd, pz, pp, pw, pdz, pdw, T, k, rows, width)
     return dz, dweights

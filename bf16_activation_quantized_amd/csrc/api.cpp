@@ -515,7 +515,8 @@ uint64_t lora_bytes(const LoraPlan& p) { return p.ws_h + plan_bytes(p.base); }
 bool expert_slots_ok(int64_t T, int32_t k) { return T >= 0 && k >= 1 && T <= kMaxDim / k; }
 
 uint64_t expert_sort_bytes(int64_t T, int32_t k, int32_t G) {
-  return round_up((uint64_t)w4a16::expert_sort_blocks(T * k) * (uint64_t)(G + 1) * 4u, 256);
+  const int blocks = w4a16::expert_sort_blocks(T * k, G);
+  return blocks > 1 ? round_up((uint64_t)blocks * (uint64_t)(G + 1) * 4u, 256) : 0u;
 }
 
 // Checks of the calls on rows; *empty: nothing to enqueue.
@@ -784,7 +785,7 @@ w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,
   if (m_sizes == nullptr) return W4A16_ERR_NULL;
   if (T > 0 && (ids == nullptr || order == nullptr || pos == nullptr)) return W4A16_ERR_NULL;
   if (!aligned4(ids) || !aligned4(order) || !aligned4(pos) || !aligned4(m_sizes)) return W4A16_ERR_ALIGN;
-  if (T > 0) {
+  if (T > 0 && expert_sort_bytes(T, k, G) > 0) {
     if (workspace == nullptr || workspace_bytes < expert_sort_bytes(T, k, G)) return W4A16_ERR_WORKSPACE;
     if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
   }

@@ -47,102 +47,167 @@ __device__ __forceinline__ u32x4 pack8f(const float (&a)[8]) {
   return u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7])};
 }
 
-constexpr int kSortThreads = 256;
-constexpr int kSortWaves = kSortThreads / 64;
+// Sort: a block of 16 waves (8 where G needs the LDS) takes tiles of 256 slots
+// per wave in turn.
+constexpr int kSortPer = 4;                 // slots per lane and tile
+constexpr int kSortMaxBlocks = 256;
+constexpr int kSortSingle = 8192;           // slots that one block takes alone
 
-__device__ __forceinline__ int bin_of(const int32_t* ids, int64_t s, int G) {
-  const int e = ids[s];
+__device__ __forceinline__ int bin_of(int e, int G) {
   return (uint32_t)e < (uint32_t)G ? e : G;   // bin G: dropped
+}
+
+// Counts the bins of slots [lo, hi) into cnt (LDS, zeroed). The lanes that
+// share the first lane's bin are counted at once (a popular expert would
+// otherwise be up to 64 additions to one address), the others one by one.
+__device__ __forceinline__ void count_bins(int32_t* cnt, const int32_t* ids, int64_t lo, int64_t hi, int G, int tid,
+                                           int nthr) {
+  for (int64_t s0 = lo; s0 < hi; s0 += kSortPer * nthr) {
+    int e[kSortPer];
+#pragma unroll
+    for (int i = 0; i < kSortPer; ++i) {
+      const int64_t s = s0 + (int64_t)i * nthr + tid;
+      e[i] = s < hi ? bin_of(ids[s], G) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kSortPer; ++i) {
+      const uint64_t live = __ballot(e[i] >= 0);
+      if (live == 0) continue;
+      const int first = __builtin_ctzll(live);
+      const uint64_t same = __ballot(e[i] == __builtin_amdgcn_readlane(e[i], first));
+      if ((tid & 63) == first) atomicAdd(&cnt[e[i]], (int)__popcll(same));
+      else if (e[i] >= 0 && !((same >> (tid & 63)) & 1)) atomicAdd(&cnt[e[i]], 1);
+    }
+  }
 }
 
 }  // namespace
 
 // ---------------------------------------------------------------- sort
-// Pass 1: block b counts the bins of its chunk of slots, hist[b][0 .. G].
-__global__ __launch_bounds__(kSortThreads) void expert_hist_kernel(const int32_t* __restrict__ ids,
-                                                                   int32_t* __restrict__ hist, int S, int G,
-                                                                   int chunk) {
+// Pass 1 (more than one block): block b counts the bins of its slots,
+// hist[b][0 .. G].
+template <int W>
+__global__ __launch_bounds__(64 * W) void expert_hist_kernel(const int32_t* __restrict__ ids,
+                                                             int32_t* __restrict__ hist, int64_t S, int G,
+                                                             int64_t chunk) {
   extern __shared__ __attribute__((aligned(16))) int32_t cnt[];
-  for (int g = threadIdx.x; g <= G; g += kSortThreads) cnt[g] = 0;
+  for (int g = threadIdx.x; g <= G; g += 64 * W) cnt[g] = 0;
   __syncthreads();
-  const int64_t lo = (int64_t)blockIdx.x * chunk;
-  const int64_t hi = min((int64_t)S, lo + chunk);
-  for (int64_t s = lo + threadIdx.x; s < hi; s += kSortThreads) atomicAdd(&cnt[bin_of(ids, s, G)], 1);
+  const int64_t lo = (int64_t)blockIdx.x * chunk, hi = lo + chunk < S ? lo + chunk : S;
+  count_bins(cnt, ids, lo, hi, G, threadIdx.x, 64 * W);
   __syncthreads();
-  for (int g = threadIdx.x; g <= G; g += kSortThreads) hist[(int64_t)blockIdx.x * (G + 1) + g] = cnt[g];
+  for (int g = threadIdx.x; g <= G; g += 64 * W) hist[(int64_t)blockIdx.x * (G + 1) + g] = cnt[g];
 }
 
-// Pass 2: every block forms the start of each bin for its own chunk (all bins
-// before it, plus the same bin in the chunks before it), splits it over its
-// waves' sub-chunks, and each wave ranks its slots 64 at a time: the lanes of
-// equal bin are found with one ballot per bin bit, a lane's rank is the number
-// of equal lanes below it, and the last lane of a bin moves the bin's running
-// count on. Slots keep their order, so the sort is stable.
-__global__ __launch_bounds__(kSortThreads) void expert_scatter_kernel(
+// Pass 2: the start of each bin for the block's slots (all bins before it,
+// plus the same bin in the blocks before), then tile by tile: each wave ranks
+// its slots 64 at a time (the lanes of equal bin are found with one ballot per
+// bin bit; the last of them moves the wave's count of the bin on), the waves'
+// counts become their starts, and every slot is written. Slots keep their
+// order within a bin: the sort is stable, and exact whatever the scheduling.
+template <int W>
+__global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
     const int32_t* __restrict__ ids, const int32_t* __restrict__ hist, int32_t* __restrict__ order,
-    int32_t* __restrict__ pos, int32_t* __restrict__ m_sizes, int S, int G, int chunk, int blocks, int bits) {
+    int32_t* __restrict__ pos, int32_t* __restrict__ m_sizes, int64_t S, int G, int64_t chunk, int blocks, int bits) {
+  constexpr int NTHR = 64 * W;
   extern __shared__ __attribute__((aligned(16))) int32_t lds[];
   const int nb = G + 1;
-  int32_t* start = lds;              // [nb] start of each bin for this chunk
-  int32_t* run = lds + nb;           // [waves][nb] counts, then running starts of each wave's sub-chunk
-  __shared__ int32_t part[kSortThreads];
+  int32_t* at = lds;             // [nb] where the block's next slot of each bin goes
+  int32_t* total = lds + nb;     // [nb] slots of each bin: aliased by the waves' counts below
+  int32_t* run = lds + nb;       // [W][nb]
+  __shared__ int32_t wave_sum[W];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t lo = (int64_t)blockIdx.x * chunk, hi = lo + chunk < S ? lo + chunk : S;
 
-  // bins of this thread: a contiguous run, so that the scan over bins is one
-  // scan over the threads
-  const int per = (nb + kSortThreads - 1) / kSortThreads;
+  for (int g = tid; g < 2 * nb; g += NTHR) lds[g] = 0;
+  __syncthreads();
+  if (blocks == 1) {
+    count_bins(total, ids, lo, hi, G, tid, NTHR);
+  } else {
+    const int me = (int)blockIdx.x * nb, all = blocks * nb;   // blocks <= 256, nb <= 4097
+    const int step = NTHR % nb;
+    int g = tid % nb;
+    for (int i0 = tid; i0 < all; i0 += 8 * NTHR) {
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = i0 + u * NTHR < all ? hist[i0 + u * NTHR] : 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (v[u] != 0) {
+          atomicAdd(&total[g], v[u]);
+          if (i0 + u * NTHR < me) atomicAdd(&at[g], v[u]);
+        }
+        g += step;
+        g = g >= nb ? g - nb : g;
+      }
+    }
+  }
+  __syncthreads();
+  // exclusive sum over the bins: a contiguous run of bins per thread
+  const int per = (nb + NTHR - 1) / NTHR;
   const int g0 = min(nb, tid * per), g1 = min(nb, g0 + per);
   int mine = 0;
+  for (int g = g0; g < g1; ++g) mine += total[g];
+  int in = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(in, d);
+    if (lane >= d) in += o;
+  }
+  if (lane == 63) wave_sum[wv] = in;
+  __syncthreads();
+  int below = in - mine;
+#pragma unroll
+  for (int w = 0; w < W; ++w) below += w < wv ? wave_sum[w] : 0;
   for (int g = g0; g < g1; ++g) {
-    int tot = 0, before = 0;
-    for (int b = 0; b < blocks; ++b) {
-      const int v = hist[(int64_t)b * nb + g];
-      tot += v;
-      before += b < (int)blockIdx.x ? v : 0;
-    }
-    if (blockIdx.x == 0 && g < G) m_sizes[g] = tot;
-    start[g] = mine + before;
-    mine += tot;
+    const int n = total[g];
+    if (blockIdx.x == 0 && g < G) m_sizes[g] = n;
+    at[g] += below;
+    below += n;
   }
-  part[tid] = mine;
-  for (int i = tid; i < kSortWaves * nb; i += kSortThreads) run[i] = 0;
-  __syncthreads();
-  int below = 0;
-  for (int t = 0; t < tid; ++t) below += part[t];
-  for (int g = g0; g < g1; ++g) start[g] += below;
 
-  const int sub = chunk / kSortWaves;
-  const int64_t lo = min((int64_t)S, (int64_t)blockIdx.x * chunk + (int64_t)wv * sub);
-  const int64_t hi = min((int64_t)S, lo + sub);
-  for (int64_t s = lo + lane; s < hi; s += 64) atomicAdd(&run[wv * nb + bin_of(ids, s, G)], 1);
-  __syncthreads();
-  for (int g = tid; g < nb; g += kSortThreads) {
-    int at = start[g];
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = run[w * nb + g];
-      run[w * nb + g] = at;
-      at += c;
-    }
-  }
-  __syncthreads();
   int32_t* r = run + wv * nb;
-  for (int64_t s0 = lo; s0 < hi; s0 += 64) {
-    const int64_t s = s0 + lane;
-    const bool live = s < hi;
-    const int e = live ? bin_of(ids, s, G) : G;
-    uint64_t same = __ballot(live);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t v = __ballot((e >> b) & 1);
-      same &= ((e >> b) & 1) ? v : ~v;
+  for (int64_t t0 = lo; t0 < hi; t0 += kSortPer * NTHR) {
+    const int64_t s0 = t0 + (int64_t)wv * (64 * kSortPer) + lane;
+    int e[kSortPer], rank[kSortPer];
+#pragma unroll
+    for (int i = 0; i < kSortPer; ++i) e[i] = s0 + 64 * i < hi ? bin_of(ids[s0 + 64 * i], G) : -1;
+    __syncthreads();   // the tile before (or the totals) is done with the counts
+    for (int i = tid; i < W * nb; i += NTHR) run[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSortPer; ++i) {
+      uint64_t same = __ballot(e[i] >= 0);
+      if (same == 0) break;   // the waves past the last slot
+      for (int b = 0; b < bits; ++b) {
+        const bool one = (e[i] >> b) & 1;
+        const uint64_t v = __ballot(one);
+        same &= one ? v : ~v;
+      }
+      wave_lds_exchange();   // after the last step's counts
+      if (e[i] >= 0) rank[i] = r[e[i]] + (int)__popcll(same & ((1ull << lane) - 1));
+      wave_lds_exchange();   // every lane has read before the counts move on
+      if (e[i] >= 0 && (same >> lane) == 1ull) r[e[i]] = rank[i] + 1;
     }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    wave_lds_exchange();   // after the last step's writes
-    const int p = r[e] + rank;
-    wave_lds_exchange();   // every lane has read before the counts move on
-    if (live && (same >> lane) == 1ull) r[e] = p + 1;
-    if (live) {
-      order[p] = (int32_t)s;
-      pos[s] = e < G ? p : -1;
+    __syncthreads();
+    for (int g = tid; g < nb; g += NTHR) {
+      int a = at[g];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const int c = run[w * nb + g];
+        run[w * nb + g] = a;
+        a += c;
+      }
+      at[g] = a;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSortPer; ++i) {
+      if (e[i] >= 0) {
+        const int p = r[e[i]] + rank[i];
+        order[p] = (int32_t)(s0 + 64 * i);
+        pos[s0 + 64 * i] = e[i] < G ? p : -1;
+      }
     }
   }
 }
@@ -254,16 +319,40 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t
 }
 
 // ---------------------------------------------------------------- launchers
-// Slots per block of the sort: whole sub-chunks of 64 slots per wave, at most
-// about 256 blocks.
-int expert_sort_chunk(int64_t S) {
-  const int64_t per = (S + 255) / 256;
-  const int64_t c = (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-  return (int)(c < 1024 ? 1024 : c);
+// One block up to kSortSingle slots (one launch), else whole tiles per block,
+// at most kSortMaxBlocks blocks (each reads all blocks' counts).
+static int sort_waves(int G) { return G < 2048 ? 16 : 8; }
+static int64_t sort_chunk(int64_t S, int G) {
+  const int64_t tile = 64 * kSortPer * sort_waves(G);
+  if (S <= kSortSingle) return kSortSingle;
+  const int64_t tiles = (S + tile - 1) / tile;
+  return (tiles + kSortMaxBlocks - 1) / kSortMaxBlocks * tile;
 }
-int expert_sort_blocks(int64_t S) {
-  const int c = expert_sort_chunk(S);
+int expert_sort_blocks(int64_t S, int G) {
+  const int64_t c = sort_chunk(S, G);
   return (int)((S + c - 1) / c);
+}
+
+template <int W>
+static hipError_t launch_sort_w(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t S, int G,
+                                int32_t* ws, hipStream_t stream) {
+  const int64_t chunk = sort_chunk(S, G);
+  const int blocks = expert_sort_blocks(S, G);
+  int bits = 1;
+  while ((1 << bits) <= G) ++bits;
+  const int lds1 = (G + 1) * 4, lds2 = (G + 1) * 4 * (1 + W);
+  static std::atomic<uint64_t> set{0};
+  const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&expert_scatter_kernel<W>),
+                                       ((W == 16 ? 2047 : kExpertMaxGroups) + 1) * 4 * (1 + W), set);
+  if (ea != hipSuccess) return ea;
+  if (blocks > 1) {
+    hipLaunchKernelGGL(expert_hist_kernel<W>, dim3(blocks), dim3(64 * W), lds1, stream, ids, ws, S, G, chunk);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(expert_scatter_kernel<W>, dim3(blocks), dim3(64 * W), lds2, stream, ids, ws, order, pos, m_sizes,
+                     S, G, chunk, blocks, bits);
+  return hipGetLastError();
 }
 
 hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t S, int G,
@@ -272,20 +361,8 @@ hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, 
     hipLaunchKernelGGL(expert_zero_kernel, dim3(1), dim3(256), 0, stream, m_sizes, G);
     return hipGetLastError();
   }
-  const int chunk = expert_sort_chunk(S), blocks = expert_sort_blocks(S);
-  int bits = 1;
-  while ((1 << bits) <= G) ++bits;
-  const size_t lds1 = (size_t)(G + 1) * 4, lds2 = (size_t)(G + 1) * 4 * (1 + kSortWaves);
-  static std::atomic<uint64_t> lds_set{0};
-  const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&expert_scatter_kernel),
-                                       (kExpertMaxGroups + 1) * 4 * (1 + kSortWaves), lds_set);
-  if (ea != hipSuccess) return ea;
-  hipLaunchKernelGGL(expert_hist_kernel, dim3(blocks), dim3(kSortThreads), lds1, stream, ids, ws, (int)S, G, chunk);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(expert_scatter_kernel, dim3(blocks), dim3(kSortThreads), lds2, stream, ids, ws, order, pos,
-                     m_sizes, (int)S, G, chunk, blocks, bits);
-  return hipGetLastError();
+  return sort_waves(G) == 16 ? launch_sort_w<16>(ids, order, pos, m_sizes, S, G, ws, stream)
+                             : launch_sort_w<8>(ids, order, pos, m_sizes, S, G, ws, stream);
 }
 
 static unsigned row_grid(int64_t T) { return (unsigned)(T < (1 << 20) ? T : (1 << 20)); }

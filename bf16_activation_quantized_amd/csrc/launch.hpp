@@ -81,8 +81,7 @@ hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_
 
 // ---- rows of a mixture of experts (experts.hip)
 constexpr int kExpertMaxGroups = 4096;
-int expert_sort_chunk(int64_t S);    // slots per block
-int expert_sort_blocks(int64_t S);   // blocks, one row of G + 1 counts of workspace each
+int expert_sort_blocks(int64_t S, int G);   // past one, each has a row of G + 1 counts of workspace
 hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t S, int G,
                               int32_t* ws, hipStream_t stream);
 hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int k, int64_t rows,

@@ -323,8 +323,8 @@ w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed,
  *   m_sizes : [G] int32, device, written: rows per expert (the m_sizes of
  *             w4a16_gemm_grouped); all zero when T == 0
  *   workspace: device scratch, overwritten, 16-byte aligned, at least
- *             w4a16_expert_sort_workspace_bytes (0 when T == 0 or on invalid
- *             arguments).
+ *             w4a16_expert_sort_workspace_bytes (0, and NULL allowed, up to
+ *             8192 slots, which take one kernel; 0 on invalid arguments).
  */
 size_t w4a16_expert_sort_workspace_bytes(int64_t T, int32_t k, int32_t G);
 w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,

@@ -41,7 +41,8 @@ SORT_CASES = [
     (64, 1, 64, "rand"), (65, 1, 65, "holes"), (255, 4, 128, "one"), (256, 4, 128, "rand"), (257, 4, 31, "skew"),
     (1000, 6, 160, "holes"), (512, 8, 256, "none"), (4097, 8, 127, "rand"), (2048, 2, 4096, "holes"),
     (40000, 8, 128, "skew"), (33333, 7, 255, "holes"), (300000, 1, 16, "one"), (270001, 2, 1000, "rand"),
-    (20000, 8, 4096, "holes"),
+    (20000, 8, 4096, "holes"), (8192, 1, 2047, "rand"), (8193, 1, 2048, "holes"), (4096, 2, 4096, "one"),
+    (1100000, 2, 60, "skew"), (700001, 3, 4095, "holes"),
 ]
 
 

@@ -73,7 +73,7 @@ def test_lora_workspace_of_invalid_sizes_is_zero():
     assert f(4, 64, 256, 0, 16) == 0 and f(4, 64, 256, 3, 16, 3) == 0
 
 
-def sort(lib, ids=A, order=A, pos=A, ms=A, T=4, k=2, G=8, ws=A, wsb=1 << 30):
+def sort(lib, ids=A, order=A, pos=A, ms=A, T=8192, k=2, G=8, ws=A, wsb=1 << 30):
     return lib.w4a16_expert_sort(ids, order, pos, ms, T, k, G, ws, wsb, None)
 
 
@@ -92,7 +92,9 @@ def test_sort_refusals(lib, kw, want):
 def test_sort_workspace(lib):
     f = w4.w4a16_expert_sort_workspace_bytes
     assert f(0, 2, 8) == 0 and f(4, 0, 8) == 0 and f(4, 2, 0) == 0 and f(4, 2, 4097) == 0 and f(1 << 30, 2, 8) == 0
-    for T, k, G in ((1, 1, 1), (16, 4, 8), (65536, 8, 128), (1 << 20, 8, 4096)):
+    for T, k, G in ((1, 1, 1), (16, 4, 8), (8192, 1, 4096)):   # one kernel
+        assert f(T, k, G) == 0
+    for T, k, G in ((8193, 1, 1), (65536, 8, 128), (1 << 20, 8, 4096), (1 << 28, 7, 300)):
         assert 0 < f(T, k, G) < 1 << 30
         assert sort(lib, T=T, k=k, G=G, wsb=f(T, k, G) - 1) == ERR_WS
 

@@ -12,6 +12,8 @@
 //                 dw[t, j] = sum_n dy[t, n] z[pos[t, j], n] in fp32
 // The gradient of gather is combine without weights. No atomics on results:
 // every result is bitwise reproducible.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -22,15 +24,25 @@ namespace {
 // 16 bytes of a row whose start is only 2-byte aligned (odd widths)
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 
+// Expert rows are read once and written once, at sizes beyond the caches: the
+// non-temporal hint on both sides took combine at 16384 x 8 x 4096 from 237.7
+// to 206.8 us and its gradient at 8192 x 8 x 4096 from 229.6 to 210.1 (loads
+// alone 219.7 / 232.2, stores alone 221.6 / 226.1); gather's rows 159.3 to
+// 155.8 us with it on the stores (on its loads too 159.2).
 template <bool ALIGNED>
 __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
   if constexpr (ALIGNED) return *reinterpret_cast<const u32x4*>(p);
   else return *reinterpret_cast<const u32x4_a2*>(p);
 }
 template <bool ALIGNED>
-__device__ __forceinline__ void store8(uint16_t* p, u32x4 v) {
-  if constexpr (ALIGNED) *reinterpret_cast<u32x4*>(p) = v;
-  else *reinterpret_cast<u32x4_a2*>(p) = v;
+__device__ __forceinline__ u32x4 load8_nt(const uint16_t* p) {
+  if constexpr (ALIGNED) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  else return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
+}
+template <bool ALIGNED>
+__device__ __forceinline__ void store8_nt(uint16_t* p, u32x4 v) {
+  if constexpr (ALIGNED) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
 }
 
 __device__ __forceinline__ void fma8(float (&a)[8], float w, u32x4 v) {
@@ -46,6 +58,19 @@ __device__ __forceinline__ void fma8(float (&a)[8], float w, u32x4 v) {
 __device__ __forceinline__ u32x4 pack8f(const float (&a)[8]) {
   return u32x4{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7])};
 }
+
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float c) {
+  c = fmaf(bf16lo(a.x), bf16lo(b.x), c);
+  c = fmaf(bf16hi(a.x), bf16hi(b.x), c);
+  c = fmaf(bf16lo(a.y), bf16lo(b.y), c);
+  c = fmaf(bf16hi(a.y), bf16hi(b.y), c);
+  c = fmaf(bf16lo(a.z), bf16lo(b.z), c);
+  c = fmaf(bf16hi(a.z), bf16hi(b.z), c);
+  c = fmaf(bf16lo(a.w), bf16lo(b.w), c);
+  return fmaf(bf16hi(a.w), bf16hi(b.w), c);
+}
+
+constexpr int kBatch = 4;   // slots of a token whose rows are in flight together
 
 // Sort: a block of 16 waves (8 where G needs the LDS) takes tiles of 256 slots
 // per wave in turn.
@@ -216,25 +241,41 @@ __global__ void expert_zero_kernel(int32_t* __restrict__ m_sizes, int G) {
   for (int g = threadIdx.x; g < G; g += blockDim.x) m_sizes[g] = 0;
 }
 
+// ---------------------------------------------------------------- rows
+// TPT threads (32 to 256) hold a token, 8 columns each, so that narrow rows
+// leave no lanes idle (30000 x 4 x 256 gradient: 65 us with a workgroup per
+// token). From 64 on the token is the same in a whole wave, and saying so
+// keeps its positions and weights in scalar registers.
+template <int TPT>
+__device__ __forceinline__ int token_in_block() {
+  const int s = (int)threadIdx.x / TPT;
+  return TPT >= 64 ? __builtin_amdgcn_readfirstlane(s) : s;
+}
+
 // ---------------------------------------------------------------- gather
-template <bool ALIGNED>
+template <bool ALIGNED, int TPT>
 __global__ __launch_bounds__(256) void expert_gather_kernel(const uint16_t* __restrict__ x,
                                                             const int32_t* __restrict__ pos,
                                                             uint16_t* __restrict__ xs, int64_t T, int k, int64_t rows,
                                                             int width) {
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+  constexpr int TOK = 256 / TPT;
+  const int in = (int)threadIdx.x % TPT;
+  for (int64_t t = (int64_t)blockIdx.x * TOK + token_in_block<TPT>(); t < T; t += (int64_t)gridDim.x * TOK) {
     const uint16_t* src = x + t * width;
-    for (int c = 8 * threadIdx.x; c < width; c += 8 * 256) {
-      const bool full = c + 8 <= width;
-      u32x4 v;
-      if (full) v = load8<ALIGNED>(src + c);
-      for (int j = 0; j < k; ++j) {
-        const int64_t p = pos[t * k + j];
-        if (p < 0 || p >= rows) continue;
-        uint16_t* dst = xs + p * width + c;
-        if (full) store8<ALIGNED>(dst, v);
-        else
-          for (int i = 0; c + i < width; ++i) dst[i] = src[c + i];
+    const int32_t* pt = pos + t * k;
+    for (int64_t c = 8 * ((int64_t)blockIdx.y * TPT + in); c < width; c += 8 * (int64_t)gridDim.y * TPT) {
+      if (c + 8 <= width) {
+        const u32x4 v = load8<ALIGNED>(src + c);
+        for (int j = 0; j < k; ++j) {
+          const int64_t p = pt[j];
+          if (p >= 0 && p < rows) store8_nt<ALIGNED>(xs + p * width + c, v);
+        }
+      } else {
+        for (int j = 0; j < k; ++j) {
+          const int64_t p = pt[j];
+          if (p >= 0 && p < rows)
+            for (int64_t i = c; i < width; ++i) xs[p * width + i] = src[i];
+        }
       }
     }
   }
@@ -242,78 +283,136 @@ __global__ __launch_bounds__(256) void expert_gather_kernel(const uint16_t* __re
 
 // ---------------------------------------------------------------- combine
 // w == nullptr: all weights 1 (the gradient of gather)
-template <bool ALIGNED>
+template <bool ALIGNED, int TPT>
 __global__ __launch_bounds__(256) void expert_combine_kernel(const uint16_t* __restrict__ z,
                                                              const int32_t* __restrict__ pos,
                                                              const float* __restrict__ w, uint16_t* __restrict__ y,
                                                              int64_t T, int k, int64_t rows, int width) {
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    for (int c = 8 * threadIdx.x; c < width; c += 8 * 256) {
-      const int n = min(8, width - c);
+  constexpr int TOK = 256 / TPT;
+  const int in = (int)threadIdx.x % TPT;
+  for (int64_t t = (int64_t)blockIdx.x * TOK + token_in_block<TPT>(); t < T; t += (int64_t)gridDim.x * TOK) {
+    for (int64_t c = 8 * ((int64_t)blockIdx.y * TPT + in); c < width; c += 8 * (int64_t)gridDim.y * TPT) {
+      const int n = width - c < 8 ? (int)(width - c) : 8;
       float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int j = 0; j < k; ++j) {
-        const int64_t p = pos[t * k + j];
-        if (p < 0 || p >= rows) continue;
-        const float wj = w != nullptr ? w[t * k + j] : 1.0f;
-        const uint16_t* src = z + p * width + c;
-        if (n == 8) fma8(a, wj, load8<ALIGNED>(src));
-        else
-          for (int i = 0; i < n; ++i) a[i] = fmaf(wj, bf16f(src[i]), a[i]);
+      for (int j0 = 0; j0 < k; j0 += kBatch) {
+        int64_t p[kBatch];
+        float wj[kBatch];
+        u32x4 v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          p[u] = j0 + u < k ? pos[t * k + j0 + u] : -1;
+          if (p[u] >= rows) p[u] = -1;
+          wj[u] = p[u] >= 0 && w != nullptr ? w[t * k + j0 + u] : 1.0f;
+        }
+        if (n == 8) {
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0) v[u] = load8_nt<ALIGNED>(z + p[u] * width + c);
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0) fma8(a, wj[u], v[u]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0)
+#pragma unroll
+              for (int i = 0; i < 7; ++i)
+                if (i < n) a[i] = fmaf(wj[u], bf16f(z[p[u] * width + c + i]), a[i]);
+        }
       }
       uint16_t* dst = y + t * width + c;
-      if (n == 8) store8<ALIGNED>(dst, pack8f(a));
-      else
-        for (int i = 0; i < n; ++i) dst[i] = to_bf16(a[i]);
+      if (n == 8) {
+        store8_nt<ALIGNED>(dst, pack8f(a));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i < n) dst[i] = to_bf16(a[i]);
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------- combine's gradient
-template <bool ALIGNED>
+// A token's dots need its whole width in one workgroup: its threads go over the
+// columns in turn, kBatch slots at a time (dy is read again from the caches
+// for every further batch), and are summed over the wave's lanes, then over
+// the token's waves through LDS. Each element of z is read by the thread that
+// writes that element of dz, before it does: dz may be z.
+template <bool ALIGNED, int TPT>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t* __restrict__ dy,
-                                                                  const uint16_t* __restrict__ z,
+                                                                  const uint16_t* z,
                                                                   const int32_t* __restrict__ pos,
-                                                                  const float* __restrict__ w,
-                                                                  uint16_t* __restrict__ dz, float* __restrict__ dw,
-                                                                  int64_t T, int k, int64_t rows, int width) {
-  __shared__ float red[4];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    for (int j = 0; j < k; ++j) {
-      const int64_t p = pos[t * k + j];
-      if (p < 0 || p >= rows) {
-        if (threadIdx.x == 0) dw[t * k + j] = 0.0f;
-        continue;
+                                                                  const float* __restrict__ w, uint16_t* dz,
+                                                                  float* __restrict__ dw, int64_t T, int k,
+                                                                  int64_t rows, int width) {
+  constexpr int TOK = 256 / TPT, WPT = TPT >= 64 ? TPT / 64 : 1;
+  __shared__ float red[2][4][kBatch];
+  const int in = (int)threadIdx.x % TPT, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int sub = token_in_block<TPT>();
+  int turn = 0;
+  // (every thread of a workgroup makes the same trips: the barriers are met by all)
+  for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < T; t0 += (int64_t)gridDim.x * TOK) {
+    const int64_t t = t0 + sub;
+    const bool live = t < T;
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+      int64_t p[kBatch];
+      float wj[kBatch], dot[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        p[u] = live && j0 + u < k ? pos[t * k + j0 + u] : -1;
+        if (p[u] >= rows) p[u] = -1;
+        wj[u] = p[u] >= 0 ? w[t * k + j0 + u] : 0.0f;
+        dot[u] = 0.0f;
       }
-      const float wj = w[t * k + j];
-      float dot = 0.0f;
-      for (int c = 8 * threadIdx.x; c < width; c += 8 * 256) {
-        const int n = min(8, width - c);
+      for (int64_t c = 8 * in; c < width && live; c += 8 * TPT) {
+        const int n = width - c < 8 ? (int)(width - c) : 8;
         const uint16_t* d = dy + t * width + c;
-        const uint16_t* zr = z + p * width + c;
-        uint16_t* o = dz + p * width + c;
         if (n == 8) {
-          const u32x4 dv = load8<ALIGNED>(d), zv = load8<ALIGNED>(zr);
-          float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          fma8(a, wj, dv);
-          store8<ALIGNED>(o, pack8f(a));
-          const uint32_t dd[4] = {dv.x, dv.y, dv.z, dv.w}, zz[4] = {zv.x, zv.y, zv.z, zv.w};
-          for (int i = 0; i < 4; ++i) {
-            dot = fmaf(bf16lo(dd[i]), bf16lo(zz[i]), dot);
-            dot = fmaf(bf16hi(dd[i]), bf16hi(zz[i]), dot);
-          }
+          const u32x4 dv = load8<ALIGNED>(d);
+          u32x4 zv[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0) zv[u] = load8_nt<ALIGNED>(z + p[u] * width + c);
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0) {
+              float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              fma8(a, wj[u], dv);
+              store8_nt<ALIGNED>(dz + p[u] * width + c, pack8f(a));
+              dot[u] = dot8(dv, zv[u], dot[u]);
+            }
         } else {
-          for (int i = 0; i < n; ++i) {
-            o[i] = to_bf16(wj * bf16f(d[i]));
-            dot = fmaf(bf16f(d[i]), bf16f(zr[i]), dot);
-          }
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0)
+              for (int i = 0; i < n; ++i) {
+                const float di = bf16f(d[i]);
+                dot[u] = fmaf(di, bf16f(z[p[u] * width + c + i]), dot[u]);
+                dz[p[u] * width + c + i] = to_bf16(wj[u] * di);
+              }
         }
       }
-      dot = wave64_sum(dot);
-      if (lane == 63) red[wv] = dot;
-      __syncthreads();
-      if (threadIdx.x == 0) dw[t * k + j] = (red[0] + red[1]) + (red[2] + red[3]);
-      __syncthreads();
+      if constexpr (TPT <= 64) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float s = TPT == 64 ? wave64_sum(dot[u]) : half32_sum(dot[u]);
+          if (in == TPT - 1 && live && j0 + u < k) dw[t * k + j0 + u] = s;
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float s = wave64_sum(dot[u]);
+          if (lane == 63) red[turn][wv][u] = s;
+        }
+        __syncthreads();
+        if (in < kBatch && live && j0 + in < k) {
+          float s = red[turn][sub * WPT][in];
+#pragma unroll
+          for (int q = 1; q < WPT; ++q) s += red[turn][sub * WPT + q][in];
+          dw[t * k + j0 + in] = s;
+        }
+        turn ^= 1;   // the next sums go elsewhere: one barrier per batch
+      }
     }
   }
 }
@@ -365,40 +464,55 @@ hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, 
                              : launch_sort_w<8>(ids, order, pos, m_sizes, S, G, ws, stream);
 }
 
-static unsigned row_grid(int64_t T) { return (unsigned)(T < (1 << 20) ? T : (1 << 20)); }
+// Threads per token: the power of two that holds the row, 32 to 256.
+template <class F>
+static hipError_t by_width(int width, F launch) {
+  const bool al = width % 8 == 0;
+  const int chunks = width / 8 + (width % 8 != 0 ? 1 : 0);
+  const auto go = [&](auto aligned) {
+    if (chunks <= 32) launch(aligned, std::integral_constant<int, 32>{});
+    else if (chunks <= 64) launch(aligned, std::integral_constant<int, 64>{});
+    else if (chunks <= 128) launch(aligned, std::integral_constant<int, 128>{});
+    else launch(aligned, std::integral_constant<int, 256>{});
+  };
+  if (al) go(std::true_type{});
+  else go(std::false_type{});
+  return hipGetLastError();
+}
+
+// x: tokens, 256 / tpt per workgroup (the kernels stride over what is beyond
+// the grid); y: 8 tpt columns each where `split`
+static dim3 row_grid(int64_t T, int width, int tpt, bool split) {
+  const int64_t x = (T + 256 / tpt - 1) / (256 / tpt), y = split ? ((int64_t)width + 8 * tpt - 1) / (8 * tpt) : 1;
+  return dim3((unsigned)(x < (1 << 20) ? x : 1 << 20), (unsigned)(y < 64 ? y : 64));
+}
 
 hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int k, int64_t rows,
                                 int width, hipStream_t stream) {
-  if (width % 8 == 0)
-    hipLaunchKernelGGL(expert_gather_kernel<true>, dim3(row_grid(T)), dim3(256), 0, stream, x, pos, xs, T, k, rows,
+  return by_width(width, [&](auto al, auto tpt) {
+    hipLaunchKernelGGL((expert_gather_kernel<decltype(al)::value, decltype(tpt)::value>),
+                       row_grid(T, width, decltype(tpt)::value, true), dim3(256), 0, stream, x, pos, xs, T, k, rows,
                        width);
-  else
-    hipLaunchKernelGGL(expert_gather_kernel<false>, dim3(row_grid(T)), dim3(256), 0, stream, x, pos, xs, T, k, rows,
-                       width);
-  return hipGetLastError();
+  });
 }
 
 hipError_t launch_expert_combine(const uint16_t* z, const int32_t* pos, const float* w, uint16_t* y, int64_t T, int k,
                                  int64_t rows, int width, hipStream_t stream) {
-  if (width % 8 == 0)
-    hipLaunchKernelGGL(expert_combine_kernel<true>, dim3(row_grid(T)), dim3(256), 0, stream, z, pos, w, y, T, k, rows,
+  return by_width(width, [&](auto al, auto tpt) {
+    hipLaunchKernelGGL((expert_combine_kernel<decltype(al)::value, decltype(tpt)::value>),
+                       row_grid(T, width, decltype(tpt)::value, true), dim3(256), 0, stream, z, pos, w, y, T, k, rows,
                        width);
-  else
-    hipLaunchKernelGGL(expert_combine_kernel<false>, dim3(row_grid(T)), dim3(256), 0, stream, z, pos, w, y, T, k,
-                       rows, width);
-  return hipGetLastError();
+  });
 }
 
 hipError_t launch_expert_combine_grad(const uint16_t* dy, const uint16_t* z, const int32_t* pos, const float* w,
                                       uint16_t* dz, float* dw, int64_t T, int k, int64_t rows, int width,
                                       hipStream_t stream) {
-  if (width % 8 == 0)
-    hipLaunchKernelGGL(expert_combine_grad_kernel<true>, dim3(row_grid(T)), dim3(256), 0, stream, dy, z, pos, w, dz,
-                       dw, T, k, rows, width);
-  else
-    hipLaunchKernelGGL(expert_combine_grad_kernel<false>, dim3(row_grid(T)), dim3(256), 0, stream, dy, z, pos, w, dz,
-                       dw, T, k, rows, width);
-  return hipGetLastError();
+  return by_width(width, [&](auto al, auto tpt) {
+    hipLaunchKernelGGL((expert_combine_grad_kernel<decltype(al)::value, decltype(tpt)::value>),
+                       row_grid(T, width, decltype(tpt)::value, false), dim3(256), 0, stream, dy, z, pos, w, dz, dw, T,
+                       k, rows, width);
+  });
 }
 
 }  // namespace w4a16

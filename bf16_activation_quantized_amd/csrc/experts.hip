@@ -24,25 +24,19 @@ namespace {
 // 16 bytes of a row whose start is only 2-byte aligned (odd widths)
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 
-// Expert rows are read once and written once, at sizes beyond the caches: the
-// non-temporal hint on both sides took combine at 16384 x 8 x 4096 from 237.7
-// to 206.8 us and its gradient at 8192 x 8 x 4096 from 229.6 to 210.1 (loads
-// alone 219.7 / 232.2, stores alone 221.6 / 226.1); gather's rows 159.3 to
-// 155.8 us with it on the stores (on its loads too 159.2).
-template <bool ALIGNED>
+template <bool ALIGNED, bool NT = false>
 __device__ __forceinline__ u32x4 load8(const uint16_t* p) {
-  if constexpr (ALIGNED) return *reinterpret_cast<const u32x4*>(p);
+  if constexpr (ALIGNED && NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  else if constexpr (ALIGNED) return *reinterpret_cast<const u32x4*>(p);
+  else if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
   else return *reinterpret_cast<const u32x4_a2*>(p);
 }
-template <bool ALIGNED>
-__device__ __forceinline__ u32x4 load8_nt(const uint16_t* p) {
-  if constexpr (ALIGNED) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-  else return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p));
-}
-template <bool ALIGNED>
-__device__ __forceinline__ void store8_nt(uint16_t* p, u32x4 v) {
-  if constexpr (ALIGNED) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-  else __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
+template <bool ALIGNED, bool NT>
+__device__ __forceinline__ void store8(uint16_t* p, u32x4 v) {
+  if constexpr (ALIGNED && NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else if constexpr (ALIGNED) *reinterpret_cast<u32x4*>(p) = v;
+  else if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a2*>(p));
+  else *reinterpret_cast<u32x4_a2*>(p) = v;
 }
 
 __device__ __forceinline__ void fma8(float (&a)[8], float w, u32x4 v) {
@@ -253,7 +247,7 @@ __device__ __forceinline__ int token_in_block() {
 }
 
 // ---------------------------------------------------------------- gather
-template <bool ALIGNED, int TPT>
+template <bool ALIGNED, int TPT, bool NT>
 __global__ __launch_bounds__(256) void expert_gather_kernel(const uint16_t* __restrict__ x,
                                                             const int32_t* __restrict__ pos,
                                                             uint16_t* __restrict__ xs, int64_t T, int k, int64_t rows,
@@ -268,7 +262,7 @@ __global__ __launch_bounds__(256) void expert_gather_kernel(const uint16_t* __re
         const u32x4 v = load8<ALIGNED>(src + c);
         for (int j = 0; j < k; ++j) {
           const int64_t p = pt[j];
-          if (p >= 0 && p < rows) store8_nt<ALIGNED>(xs + p * width + c, v);
+          if (p >= 0 && p < rows) store8<ALIGNED, NT>(xs + p * width + c, v);
         }
       } else {
         for (int j = 0; j < k; ++j) {
@@ -283,7 +277,7 @@ __global__ __launch_bounds__(256) void expert_gather_kernel(const uint16_t* __re
 
 // ---------------------------------------------------------------- combine
 // w == nullptr: all weights 1 (the gradient of gather)
-template <bool ALIGNED, int TPT>
+template <bool ALIGNED, int TPT, bool NT>
 __global__ __launch_bounds__(256) void expert_combine_kernel(const uint16_t* __restrict__ z,
                                                              const int32_t* __restrict__ pos,
                                                              const float* __restrict__ w, uint16_t* __restrict__ y,
@@ -307,7 +301,7 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const uint16_t* __r
         if (n == 8) {
 #pragma unroll
           for (int u = 0; u < kBatch; ++u)
-            if (p[u] >= 0) v[u] = load8_nt<ALIGNED>(z + p[u] * width + c);
+            if (p[u] >= 0) v[u] = load8<ALIGNED, NT>(z + p[u] * width + c);
 #pragma unroll
           for (int u = 0; u < kBatch; ++u)
             if (p[u] >= 0) fma8(a, wj[u], v[u]);
@@ -322,7 +316,7 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const uint16_t* __r
       }
       uint16_t* dst = y + t * width + c;
       if (n == 8) {
-        store8_nt<ALIGNED>(dst, pack8f(a));
+        store8<ALIGNED, NT>(dst, pack8f(a));
       } else {
 #pragma unroll
         for (int i = 0; i < 7; ++i)
@@ -338,7 +332,7 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const uint16_t* __r
 // for every further batch), and are summed over the wave's lanes, then over
 // the token's waves through LDS. Each element of z is read by the thread that
 // writes that element of dz, before it does: dz may be z.
-template <bool ALIGNED, int TPT>
+template <bool ALIGNED, int TPT, bool NT>
 __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t* __restrict__ dy,
                                                                   const uint16_t* z,
                                                                   const int32_t* __restrict__ pos,
@@ -372,13 +366,13 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t
           u32x4 zv[kBatch];
 #pragma unroll
           for (int u = 0; u < kBatch; ++u)
-            if (p[u] >= 0) zv[u] = load8_nt<ALIGNED>(z + p[u] * width + c);
+            if (p[u] >= 0) zv[u] = load8<ALIGNED, NT>(z + p[u] * width + c);
 #pragma unroll
           for (int u = 0; u < kBatch; ++u)
             if (p[u] >= 0) {
               float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
               fma8(a, wj[u], dv);
-              store8_nt<ALIGNED>(dz + p[u] * width + c, pack8f(a));
+              store8<ALIGNED, NT>(dz + p[u] * width + c, pack8f(a));
               dot[u] = dot8(dv, zv[u], dot[u]);
             }
         } else {
@@ -464,19 +458,27 @@ hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, 
                              : launch_sort_w<8>(ids, order, pos, m_sizes, S, G, ws, stream);
 }
 
-// Threads per token: the power of two that holds the row, 32 to 256.
+// The variant by the rows: threads per token, the power of two that holds the
+// row, 32 to 256; and the non-temporal hint on the expert rows where they are
+// larger than the last-level cache (256 MB), so that their reader or writer
+// could not meet them there anyway: combine at 16384 x 8 x 4096 (1.1 GB) 237.7
+// -> 206.8 us, its gradient at 8192 x 8 x 4096 229.6 -> 210.1, gather at 16384
+// x 4 x 5120 159.3 -> 155.8; but gather, grouped GEMM and combine of 1024 x 2
+// tokens, K 4096, N 2048 (25 MB) one after the other 72.8 -> 76.5 us with it.
 template <class F>
-static hipError_t by_width(int width, F launch) {
-  const bool al = width % 8 == 0;
+static hipError_t by_rows(int64_t rows, int width, F launch) {
   const int chunks = width / 8 + (width % 8 != 0 ? 1 : 0);
-  const auto go = [&](auto aligned) {
-    if (chunks <= 32) launch(aligned, std::integral_constant<int, 32>{});
-    else if (chunks <= 64) launch(aligned, std::integral_constant<int, 64>{});
-    else if (chunks <= 128) launch(aligned, std::integral_constant<int, 128>{});
-    else launch(aligned, std::integral_constant<int, 256>{});
+  const auto go = [&](auto aligned, auto nt) {
+    if (chunks <= 32) launch(aligned, std::integral_constant<int, 32>{}, nt);
+    else if (chunks <= 64) launch(aligned, std::integral_constant<int, 64>{}, nt);
+    else if (chunks <= 128) launch(aligned, std::integral_constant<int, 128>{}, nt);
+    else launch(aligned, std::integral_constant<int, 256>{}, nt);
   };
-  if (al) go(std::true_type{});
-  else go(std::false_type{});
+  const bool nt = rows * width * 2 > ((int64_t)256 << 20);
+  if (width % 8 == 0 && nt) go(std::true_type{}, std::true_type{});
+  else if (width % 8 == 0) go(std::true_type{}, std::false_type{});
+  else if (nt) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 
@@ -489,8 +491,8 @@ static dim3 row_grid(int64_t T, int width, int tpt, bool split) {
 
 hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int k, int64_t rows,
                                 int width, hipStream_t stream) {
-  return by_width(width, [&](auto al, auto tpt) {
-    hipLaunchKernelGGL((expert_gather_kernel<decltype(al)::value, decltype(tpt)::value>),
+  return by_rows(rows, width, [&](auto al, auto tpt, auto nt) {
+    hipLaunchKernelGGL((expert_gather_kernel<decltype(al)::value, decltype(tpt)::value, decltype(nt)::value>),
                        row_grid(T, width, decltype(tpt)::value, true), dim3(256), 0, stream, x, pos, xs, T, k, rows,
                        width);
   });
@@ -498,8 +500,8 @@ hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t*
 
 hipError_t launch_expert_combine(const uint16_t* z, const int32_t* pos, const float* w, uint16_t* y, int64_t T, int k,
                                  int64_t rows, int width, hipStream_t stream) {
-  return by_width(width, [&](auto al, auto tpt) {
-    hipLaunchKernelGGL((expert_combine_kernel<decltype(al)::value, decltype(tpt)::value>),
+  return by_rows(rows, width, [&](auto al, auto tpt, auto nt) {
+    hipLaunchKernelGGL((expert_combine_kernel<decltype(al)::value, decltype(tpt)::value, decltype(nt)::value>),
                        row_grid(T, width, decltype(tpt)::value, true), dim3(256), 0, stream, z, pos, w, y, T, k, rows,
                        width);
   });
@@ -508,8 +510,8 @@ hipError_t launch_expert_combine(const uint16_t* z, const int32_t* pos, const fl
 hipError_t launch_expert_combine_grad(const uint16_t* dy, const uint16_t* z, const int32_t* pos, const float* w,
                                       uint16_t* dz, float* dw, int64_t T, int k, int64_t rows, int width,
                                       hipStream_t stream) {
-  return by_width(width, [&](auto al, auto tpt) {
-    hipLaunchKernelGGL((expert_combine_grad_kernel<decltype(al)::value, decltype(tpt)::value>),
+  return by_rows(rows, width, [&](auto al, auto tpt, auto nt) {
+    hipLaunchKernelGGL((expert_combine_grad_kernel<decltype(al)::value, decltype(tpt)::value, decltype(nt)::value>),
                        row_grid(T, width, decltype(tpt)::value, false), dim3(256), 0, stream, dy, z, pos, w, dz, dw, T,
                        k, rows, width);
   });

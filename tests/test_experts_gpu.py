@@ -286,3 +286,37 @@ def test_side_stream_and_graph_replays():
         assert all(torch.equal(a, b) for a, b in zip(want, cap))
         all_calls()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,k,width", [(9000, 8, 2056), (45000, 3, 1003), (400000, 2, 176)])
+def test_rows_beyond_the_caches(T, k, width):
+    """More than 256 MB of expert rows: each call against the same call on a
+    few of its tokens, with guard rows behind."""
+    G = 16
+    rng = np.random.default_rng(T)
+    ids = _ids(rng, T, k, G, "holes")
+    pos = sort_ref(ids, G)[1].astype(np.int32)
+    kept = int((pos >= 0).sum())
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, width, generator=gen, device=dev()).bfloat16()
+    z = torch.randn(T * k, width, generator=gen, device=dev()).bfloat16()
+    w = torch.rand(T, k, generator=gen, device=dev())
+    dpos = torch.from_numpy(pos).to(dev())
+    xs = w4.w4a16_expert_gather(x, dpos, xs=torch.full_like(z, 7.0))
+    y = w4.w4a16_expert_combine(z, dpos, w)
+    dz, dw = w4.w4a16_expert_combine_grad(x, z, dpos, w, dz=torch.full_like(z, 7.0))
+    dx = w4.w4a16_expert_gather_grad(z, dpos)
+    assert (xs[kept:] == 7.0).all() and (dz[kept:] == 7.0).all()
+    tok = np.unique(np.concatenate([[0, 1, T // 2, T - 2, T - 1], rng.integers(0, T, 60)]))
+    rows = np.concatenate([pos[t][pos[t] >= 0] for t in tok]).astype(np.int64)
+    small = {int(r): i for i, r in enumerate(rows)}     # the named rows of these tokens, renumbered
+    sp = np.array([[small[int(p)] if p >= 0 else -1 for p in pos[t]] for t in tok])
+    pick = torch.from_numpy(rows).to(dev())
+    tt = torch.from_numpy(tok).to(dev())
+    xn, zn, wn = f64(x[tt]), f64(z[pick]), f64(w[tt])
+    assert np.array_equal(f64(xs[pick]), gather_ref(xn, sp, np.zeros((len(rows), width))))
+    within(f64(y[tt]), *combine_ref(zn, sp, wn), "combine")
+    within(f64(dx[tt]), *combine_ref(zn, sp, None), "gather_grad")
+    rz, bz, rw, bw = combine_grad_ref(xn, zn, sp, wn, np.zeros((len(rows), width)))
+    within(f64(dz[pick]), rz, bz, "dz")
+    within(f64(dw[tt]), rw, bw, "dweights")

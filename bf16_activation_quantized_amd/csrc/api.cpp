@@ -347,7 +347,7 @@ w4a16_status plan_gemm(const uint16_t* x, const uint8_t* w, const uint16_t* s, u
 
 // Enqueues a planned GEMM; `partials` holds the [SK, M, N] fp32 slices when
 // p.sk > 1 (unused otherwise); `rowsums` (tile path, may be nullptr) the
-// pre-pass row sums; `la` per-row adapters.
+// pre-pass row sums; `la` per-row adapters (the row sums are there already).
 w4a16_status launch_plan(const Plan& p, const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y,
                          int64_t M, int64_t N, int64_t K, int32_t group_size, float* partials, float* rowsums,
                          hipStream_t strm, const w4a16::LoraArgs* la = nullptr) {
@@ -367,7 +367,9 @@ w4a16_status launch_plan(const Plan& p, const uint16_t* x, const uint8_t* w, con
       break;
     case kPathTile: {
       const int ld = (int)round_up((uint64_t)M, 4);
-      if (rowsums != nullptr) e = w4a16::launch_rowsum_neg136(x, rowsums, iM, iK, ld, group_size, strm);
+      // with adapters they came with x . A^T
+      if (rowsums != nullptr && la == nullptr)
+        e = w4a16::launch_rowsum_neg136(x, rowsums, iM, iK, ld, group_size, strm);
       if (e == hipSuccess)
         e = w4a16::launch_tile(x, w, s, rowsums, ld, y, ws_split, nullptr, 0, iM, iN, iK, 1, p.gps, p.sk, p.variant,
                                group_size, strm, la);
@@ -768,7 +770,8 @@ w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed, const u
   float* rowsums =
       p.base.ws_sx > 0 ? reinterpret_cast<float*>(ws + p.ws_h + round_up(p.base.ws_split, 256)) : nullptr;
   uint16_t* h = reinterpret_cast<uint16_t*>(ws);
-  const hipError_t e = w4a16::launch_lora_shrink(x, a, adapter_ids, scaling, h, (int)M, (int)K, L, R, strm);
+  const hipError_t e = w4a16::launch_lora_shrink(x, a, adapter_ids, scaling, h, (int)M, (int)K, L, R,
+                                                 rowsums, (int)round_up((uint64_t)M, 4), group_size, strm);
   if (e != hipSuccess) return W4A16_ERR_LAUNCH;
   const w4a16::LoraArgs la = {h, b, adapter_ids, (int)M, (int)N, L, R};
   return launch_plan(p.base, x, w_packed, scales, y, M, N, K, group_size, partials, rowsums, strm, &la);

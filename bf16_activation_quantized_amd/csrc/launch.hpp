@@ -75,9 +75,11 @@ bool tile_rows_ok(int bm, int gsize);
 constexpr int kTileCols = 256;
 
 // ---- low-rank adapters beside the projection (lora.hip)
-// h = sc * x . A^T as two bf16 parts [2, M, R] (rows with an adapter only)
+// h = sc * x . A^T as two bf16 parts [2, M, R] (rows with an adapter only);
+// with rowsums != nullptr launch_rowsum_neg136's work too
 hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
-                              uint16_t* h, int M, int K, int L, int R, hipStream_t stream);
+                              uint16_t* h, int M, int K, int L, int R, float* rowsums, int ld, int gsize,
+                              hipStream_t stream);
 
 // ---- rows of a mixture of experts (experts.hip)
 constexpr int kExpertMaxGroups = 4096;

@@ -11,12 +11,15 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "lora.hpp"
+#include "rowsum.hpp"
 
 namespace w4a16 {
 
 namespace {
 
 __device__ __forceinline__ bf16x8 frag(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+constexpr int kWaves = 8;   // per workgroup, in every kernel here
 
 constexpr uint32_t kOutside = 0xFFFFFFF0u;   // a buffer offset past every extent: the load returns zeros
 
@@ -29,23 +32,20 @@ __device__ __forceinline__ void store_h(uint16_t* h, size_t plane, size_t e, flo
 }  // namespace
 
 // ---------------------------------------------------------------- few rows
-// Block (row, RP ranks): dot products on the VALU. The 8 waves take 512-k
+// Workgroup (row, RP ranks): dot products on the VALU. The 8 waves take 512-k
 // pieces in turn (one contiguous 1 KiB run of x and of each rank's row of A
 // per wave instruction), two pieces in flight, and are summed through LDS in
 // wave order.
-constexpr int kRowWaves = 8;
+constexpr int kRowWaves = kWaves;
 
 template <int RP>
-__global__ __launch_bounds__(64 * kRowWaves) void lora_shrink_row_kernel(const uint16_t* __restrict__ x,
-                                                                         const uint16_t* __restrict__ a,
-                                                                         const int32_t* __restrict__ ids,
-                                                                         const float* __restrict__ scaling,
-                                                                         uint16_t* __restrict__ h, int M, int K, int L,
-                                                                         int R) {
+__device__ __forceinline__ void shrink_row(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
+                                           const int32_t* __restrict__ ids, const float* __restrict__ scaling,
+                                           uint16_t* __restrict__ h, int M, int K, int L, int R, int block) {
   __shared__ float red[kRowWaves][RP];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m = blockIdx.x, r0 = blockIdx.y * RP;
+  const int per_row = R / RP, m = block / per_row, r0 = (block - m * per_row) * RP;
   const int l = __builtin_amdgcn_readfirstlane(ids[m]);
   if ((uint32_t)l >= (uint32_t)L) return;
   const uint32_t KB = (uint32_t)K * 2u;
@@ -98,8 +98,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void lora_shrink_row_kernel(const u
 }
 
 // ---------------------------------------------------------------- many rows
-// Workgroup (row tile of 16, rank tile of 16, turn): MFMA 16x16x32 over the
-// whole K range, for every gridDim.z-th adapter of the row tile in the order
+// Workgroup (turn, row tile of 16, rank tile of 16): MFMA 16x16x32 over the
+// whole K range, for every turns-th adapter of the row tile in the order
 // of their first row (one, where the rows of a request lie together). The 8
 // waves take the 128-k groups in turn; a group of x (only the rows of the
 // turn's adapters) and of A is fetched in whole lines (4 rows x 256 bytes per
@@ -108,17 +108,19 @@ __global__ __launch_bounds__(64 * kRowWaves) void lora_shrink_row_kernel(const u
 // another, and each product is added to the rows of its adapter only (one
 // accumulator: a row has one adapter). The waves are summed through LDS in
 // wave order.
-constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
+constexpr int kTileWaves = kWaves;
 
-__global__ __launch_bounds__(kTileThreads, 4) void lora_shrink_tile_kernel(
-    const uint16_t* __restrict__ x, const uint16_t* __restrict__ a, const int32_t* __restrict__ ids,
-    const float* __restrict__ scaling, uint16_t* __restrict__ h, int M, int K, int L, int R) {
+__device__ __forceinline__ void shrink_tile(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
+                                            const int32_t* __restrict__ ids, const float* __restrict__ scaling,
+                                            uint16_t* __restrict__ h, int M, int K, int L, int R, int block,
+                                            int turns) {
   __shared__ u32x4 tile[kTileWaves][16 * 16];   // [row][piece p of a group in slot p ^ row]
   __shared__ f32x4 red[kTileWaves][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m16 = lane & 15, kb = lane >> 4;
-  const int m0 = blockIdx.x * 16, r0 = blockIdx.y * 16;
+  const int rt = (R + 15) / 16, mt = (M + 15) / 16;
+  const int r0 = block % rt * 16, m0 = block / rt % mt * 16, me = block / rt / mt;
   const int Gk = K / kGroup;
   const uint32_t KB = (uint32_t)K * 2u;
   int id = m0 + m16 < M ? ids[m0 + m16] : -1;
@@ -128,10 +130,10 @@ __global__ __launch_bounds__(kTileThreads, 4) void lora_shrink_tile_kernel(
   uint32_t lead = 0, own = 0;
   {
     uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-    for (int turn = 0; todo != 0; turn = turn + 1 == (int)gridDim.z ? 0 : turn + 1) {
+    for (int turn = 0; todo != 0; turn = turn + 1 == turns ? 0 : turn + 1) {
       const int first = __builtin_ctz(todo);
       const uint32_t rows = (uint32_t)__ballot(id == __builtin_amdgcn_readlane(id, first)) & 0xFFFFu;
-      if (turn == (int)blockIdx.z) {
+      if (turn == me) {
         lead |= 1u << first;
         own |= rows;
       }
@@ -231,6 +233,44 @@ __global__ __launch_bounds__(kTileThreads, 4) void lora_shrink_tile_kernel(
   }
 }
 
+// ---------------------------------------------------------------- launch
+// The first workgroups form the tile kernel's row sums of X where it wants
+// them from ahead (8 rows each; GS = 0: none): both passes read x and neither
+// waits for the other (two launches cost about 4 us more).
+struct ShrinkArgs {
+  const uint16_t* x;
+  const uint16_t* a;
+  const int32_t* ids;
+  const float* scaling;
+  uint16_t* h;
+  float* rowsums;
+  int M, K, L, R, ld, rowsum_blocks, turns;
+};
+
+template <int GS>
+__device__ __forceinline__ bool rowsum_block(const ShrinkArgs& p) {
+  if constexpr (GS != 0) {
+    if ((int)blockIdx.x < p.rowsum_blocks) {
+      rowsum_neg136_row<GS>(p.x, p.rowsums, blockIdx.x * kWaves + (threadIdx.x >> 6), p.M, p.K, p.ld,
+                            threadIdx.x & 63);
+      return true;
+    }
+  }
+  return false;
+}
+
+template <int RP, int GS>
+__global__ __launch_bounds__(64 * kWaves) void lora_shrink_row_kernel(const ShrinkArgs p) {
+  if (rowsum_block<GS>(p)) return;
+  shrink_row<RP>(p.x, p.a, p.ids, p.scaling, p.h, p.M, p.K, p.L, p.R, (int)blockIdx.x - p.rowsum_blocks);
+}
+
+template <int GS>
+__global__ __launch_bounds__(64 * kWaves, 4) void lora_shrink_tile_kernel(const ShrinkArgs p) {
+  if (rowsum_block<GS>(p)) return;
+  shrink_tile(p.x, p.a, p.ids, p.scaling, p.h, p.M, p.K, p.L, p.R, (int)blockIdx.x - p.rowsum_blocks, p.turns);
+}
+
 // Few rows one by one, more in row tiles: the row kernel reads A once per row,
 // the tile kernel once per adapter of 16 rows, but through fewer workgroups
 // and in shorter runs. The whole call, row against tile kernel: 64 x 8192 x
@@ -240,25 +280,39 @@ __global__ __launch_bounds__(kTileThreads, 4) void lora_shrink_tile_kernel(
 // 4096 x 4096, rank 16, one after the other, 99.0 / 80.2. Turns: about a
 // thousand workgroups, for row tiles of many adapters; one that finds no
 // adapter left to it ends at once.
-hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
-                              uint16_t* h, int M, int K, int L, int R, hipStream_t stream) {
-  if ((int64_t)M * R <= 8192) {
-#define W4A16_ROW(RP)                                                                                         \
-  hipLaunchKernelGGL(lora_shrink_row_kernel<RP>, dim3(M, R / RP), dim3(64 * kRowWaves), 0, stream, x, a, ids, \
-                     scaling, h, M, K, L, R)
-    if (M * R >= 2048) W4A16_ROW(8);
-    else if (M * R >= 1024) W4A16_ROW(4);
-    else if (M * R >= 512) W4A16_ROW(2);
+template <int GS>
+static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
+  p.rowsum_blocks = GS != 0 ? (p.M + kWaves - 1) / kWaves : 0;
+  p.turns = 1;
+  const int64_t MR = (int64_t)p.M * p.R;
+  const dim3 threads(64 * kWaves);
+  if (MR <= 8192) {
+#define W4A16_ROW(RP) \
+  hipLaunchKernelGGL((lora_shrink_row_kernel<RP, GS>), dim3(p.rowsum_blocks + p.M * (p.R / RP)), threads, 0, stream, p)
+    // ranks per workgroup: x is read once for all of them, but a few hundred
+    // workgroups should be there
+    if (MR >= 2048) W4A16_ROW(8);
+    else if (MR >= 1024) W4A16_ROW(4);
+    else if (MR >= 512) W4A16_ROW(2);
     else W4A16_ROW(1);
 #undef W4A16_ROW
     return hipGetLastError();
   }
-  const int mt = (M + 15) / 16, rt = (R + 15) / 16;
-  int z = 1;
-  while (z < 16 && 2 * z <= L && (int64_t)mt * rt * 2 * z <= 1024) z *= 2;
-  hipLaunchKernelGGL(lora_shrink_tile_kernel, dim3(mt, rt, z), dim3(kTileThreads), 0, stream, x, a, ids, scaling, h,
-                     M, K, L, R);
+  const int64_t tiles = (int64_t)((p.M + 15) / 16) * ((p.R + 15) / 16);
+  while (p.turns < 16 && 2 * p.turns <= p.L && tiles * 2 * p.turns <= 1024) p.turns *= 2;
+  hipLaunchKernelGGL((lora_shrink_tile_kernel<GS>), dim3((unsigned)(p.rowsum_blocks + tiles * p.turns)), threads, 0,
+                     stream, p);
   return hipGetLastError();
+}
+
+hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
+                              uint16_t* h, int M, int K, int L, int R, float* rowsums, int ld, int gsize,
+                              hipStream_t stream) {
+  const ShrinkArgs p = {x, a, ids, scaling, h, rowsums, M, K, L, R, ld, 0, 1};
+  if (rowsums == nullptr) return launch_shrink_gs<0>(p, stream);
+  if (gsize == 128) return launch_shrink_gs<128>(p, stream);
+  if (gsize == 32) return launch_shrink_gs<32>(p, stream);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace w4a16

@@ -197,61 +197,70 @@ __device__ __forceinline__ void lora_tile(f32x4 (&acc)[MS][SN], uint8_t* lds, co
 
 // ---- small batch (M <= 16 MS rows): h read straight into the fragments by the
 // waves that hold an adapter, `part` of `nparts`; 4 / NS adapters' B fragments
-// are in flight at once, the first ones together with h.
+// are in flight at once, the first ones together with h. start() requests
+// them; add() uses them, and goes on with the adapters that are left.
+
+// the adapter of row `lane`: a load at the kernel's start, used at its end
+__device__ __forceinline__ int lora_id(const LoraArgs& la, int lane) { return lane < la.M ? la.ids[lane] : -1; }
+
 template <int MS, int SN, int NS>
-__device__ __forceinline__ void lora_rows_ns(f32x4 (&acc)[MS][SN], const LoraArgs& la, const int (&id)[1], int n0,
-                                             int lane, int part, int nparts) {
-  constexpr int NB = 4 / NS;
-  const int m16 = lane & 15, kb = lane >> 4;
-  const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
-  const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
+struct LoraSmall {
+  static_assert(MS <= 4, "one row per lane");
+  static constexpr int NB = 4 / NS;
+  int id[1];
+  LoraRows<MS> adapters;
+  int l[NB];
+  uint64_t rows[NB][1];
+  bf16x8 bf[NB][NS][SN];
   u32x4 hi[MS][NS], lo[MS][NS];
-  LoraRows<MS> adapters(id);
-  for (bool first = true;; first = false) {
-    int l[NB];
-    uint64_t rows[NB][1];
-    bf16x8 bf[NB][NS][SN];
+
+  __device__ __forceinline__ LoraSmall(const LoraArgs& la, int row_id, int lane)
+      : id{lane < 16 * MS && (uint32_t)row_id < (uint32_t)la.L ? row_id : -1}, adapters(id) {}
+
+  __device__ __forceinline__ void batch(const LoraArgs& la, int n0, int lane, int part, int nparts) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       l[k] = (k == 0 || l[k > 0 ? k - 1 : 0] >= 0) ? adapters.next(id, rows[k], part, nparts) : -1;
       if (l[k] >= 0) lora_load_b<SN, NS>(bf[k], la, l[k], n0, lane);
     }
+  }
+
+  __device__ __forceinline__ void start(const LoraArgs& la, int n0, int lane, int part, int nparts) {
+    batch(la, n0, lane, part, nparts);
     if (l[0] < 0) return;
-    if (first) {
+    const int m16 = lane & 15, kb = lane >> 4;
+    const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
+    const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
 #pragma unroll
-      for (int ms = 0; ms < MS; ++ms)
+    for (int ms = 0; ms < MS; ++ms)
 #pragma unroll
-        for (int st = 0; st < NS; ++st) {
-          const int r = 32 * st + 8 * kb, m = 16 * ms + m16;
-          const bool ok = m < la.M && r < la.R;
-          const uint32_t off = ((uint32_t)m * (uint32_t)la.R + (uint32_t)r) * 2u;
-          hi[ms][st] = ld128(rh, ok ? off : 0xFFFFFFF0u);
-          lo[ms][st] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      if (l[k] < 0) return;
-#pragma unroll
-      for (int ms = 0; ms < MS; ++ms) {
-        const uint32_t mine = (uint32_t)(rows[k][0] >> (16 * ms)) & 0xFFFFu;
-        if (mine != 0) lora_mac<SN, NS>(acc[ms], hi[ms], lo[ms], bf[k], mine, kb);
+      for (int st = 0; st < NS; ++st) {
+        const int r = 32 * st + 8 * kb, m = 16 * ms + m16;
+        const bool ok = m < la.M && r < la.R;
+        const uint32_t off = ((uint32_t)m * (uint32_t)la.R + (uint32_t)r) * 2u;
+        hi[ms][st] = ld128(rh, ok ? off : 0xFFFFFFF0u);
+        lo[ms][st] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
       }
+  }
+
+  __device__ __forceinline__ void add(f32x4 (&acc)[MS][SN], const LoraArgs& la, int n0, int lane, int part,
+                                      int nparts) {
+    while (l[0] >= 0) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (l[k] < 0) return;
+        static_for<MS>([&](auto i) {
+          constexpr int ms = decltype(i)::value;
+          const uint32_t mine = (uint32_t)(rows[k][0] >> (16 * ms)) & 0xFFFFu;
+          if (mine != 0) lora_mac<SN, NS>(acc[ms], hi[ms], lo[ms], bf[k], mine, lane >> 4);
+        });
+      }
+      batch(la, n0, lane, part, nparts);
     }
   }
-}
+};
 
-// the adapter of row `lane`: a load at the kernel's start, used at its end
-__device__ __forceinline__ int lora_id(const LoraArgs& la, int lane) { return lane < la.M ? la.ids[lane] : -1; }
-
-template <int MS, int SN>
-__device__ __forceinline__ void lora_rows(f32x4 (&acc)[MS][SN], const LoraArgs& la, int row_id, int n0, int lane,
-                                          int part, int nparts) {
-  static_assert(MS <= 4, "one row per lane");
-  const int id[1] = {lane < 16 * MS && (uint32_t)row_id < (uint32_t)la.L ? row_id : -1};
-  if (la.R <= 32) lora_rows_ns<MS, SN, 1>(acc, la, id, n0, lane, part, nparts);
-  else if (la.R <= 64) lora_rows_ns<MS, SN, 2>(acc, la, id, n0, lane, part, nparts);
-  else lora_rows_ns<MS, SN, 4>(acc, la, id, n0, lane, part, nparts);
-}
+// fragment steps of a rank
+inline int lora_steps(int R) { return R <= 32 ? 1 : R <= 64 ? 2 : 4; }
 
 }  // namespace w4a16

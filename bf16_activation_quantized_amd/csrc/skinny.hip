@@ -43,10 +43,10 @@ __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, 
 // MT: row tiles of 16 (M <= 16 MT); XR: row quads of X loaded per group
 // (M <= 4 XR <= 16 MT). The A-operand rows past them are never written in
 // the staging tile; they feed only output rows >= M, which are not stored.
-// LA: nothing, or the LoraArgs of per-row adapters, whose products join the
-// accumulators: the waves of all K slices take the adapters in turn, before
-// their sums are added up.
-template <int NT, int WAVES, bool SLDS, int XR, int MT, class... LA>
+// LA: nothing, or the LoraArgs of per-row adapters (ranks up to 32 LNS), whose
+// products join the accumulators: the waves of all K slices take the adapters
+// in turn, before their sums are added up.
+template <int NT, int WAVES, bool SLDS, int XR, int MT, int LNS, class... LA>
 __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __restrict__ x,
                                                             const uint8_t* __restrict__ w,
                                                             const uint16_t* __restrict__ s,
@@ -260,9 +260,10 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __re
   }
 
   if constexpr (sizeof...(LA) > 0) {
-    (lora_rows<MT, NT>(acc, la, row_id, nb, lane, __builtin_amdgcn_readfirstlane(wave) + WAVES * slice,
-                       WAVES * (int)gridDim.y),
-     ...);
+    const int part = __builtin_amdgcn_readfirstlane(wave) + WAVES * slice, nparts = WAVES * (int)gridDim.y;
+    LoraSmall<MT, NT, LNS> adapters(la..., row_id, lane);
+    (adapters.start(la, nb, lane, part, nparts), ...);
+    (adapters.add(acc, la, nb, lane, part, nparts), ...);
   }
 
   // cross-wave reduction: waves 1.. park their tiles in LDS, wave 0 sums
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __re
     }
 }
 
-template <int NT, int WV, int XR, int MT, class... LA>
+template <int NT, int WV, int XR, int MT, int LNS, class... LA>
 static hipError_t launch_skinny_la(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
                                    int M, int N, int K, int gps, int sk, hipStream_t stream, LA... la) {
   dim3 grid((N + 16 * NT - 1) / (16 * NT), sk);
@@ -316,13 +317,13 @@ static hipError_t launch_skinny_la(const uint16_t* x, const uint8_t* w, const ui
   if (gps <= kSkinnyMaxScaleGroups) {
     const size_t dyn = ((size_t)16 * NT * gps * 2 + 15) & ~(size_t)15;
     static std::atomic<uint64_t> lds_set{0};   // per instantiation and device
-    const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&skinny_kernel<NT, WV, true, XR, MT, LA...>),
+    const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&skinny_kernel<NT, WV, true, XR, MT, LNS, LA...>),
                                          16 * NT * kSkinnyMaxScaleGroups * 2, lds_set);
     if (ea != hipSuccess) return ea;
-    hipLaunchKernelGGL((skinny_kernel<NT, WV, true, XR, MT, LA...>), grid, dim3(64 * WV), dyn, stream, x, w, s, y,
+    hipLaunchKernelGGL((skinny_kernel<NT, WV, true, XR, MT, LNS, LA...>), grid, dim3(64 * WV), dyn, stream, x, w, s, y,
                        ws, M, N, K, gps, la...);
   } else {
-    hipLaunchKernelGGL((skinny_kernel<NT, WV, false, XR, MT, LA...>), grid, dim3(64 * WV), 0, stream, x, w, s, y, ws,
+    hipLaunchKernelGGL((skinny_kernel<NT, WV, false, XR, MT, LNS, LA...>), grid, dim3(64 * WV), 0, stream, x, w, s, y, ws,
                        M, N, K, gps, la...);
   }
   return hipGetLastError();
@@ -330,33 +331,55 @@ static hipError_t launch_skinny_la(const uint16_t* x, const uint8_t* w, const ui
 
 template <int NT, int WV, int XR, int MT = 1>
 static hipError_t launch_skinny_t(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
-                                  int M, int N, int K, int gps, int sk, hipStream_t stream, const LoraArgs* la) {
-  if (la != nullptr) return launch_skinny_la<NT, WV, XR, MT>(x, w, s, y, ws, M, N, K, gps, sk, stream, *la);
-  return launch_skinny_la<NT, WV, XR, MT>(x, w, s, y, ws, M, N, K, gps, sk, stream);
+                                  int M, int N, int K, int gps, int sk, hipStream_t stream) {
+  return launch_skinny_la<NT, WV, XR, MT, 0>(x, w, s, y, ws, M, N, K, gps, sk, stream);
+}
+
+// with adapters: the automatic choices only (M <= 8 and M > 32 one column tile
+// per wave, 17 <= M <= 32 two)
+template <int LNS>
+static hipError_t launch_skinny_lora(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
+                                     int M, int N, int K, int gps, int sk, int nt, hipStream_t stream,
+                                     const LoraArgs& la) {
+  if (nt != (M <= 8 || M > 32 ? 1 : 2) || (M > 8 && M <= 16)) return hipErrorInvalidValue;
+  if (M <= 4) return launch_skinny_la<1, 8, 1, 1, LNS>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);
+  if (M <= 8) return launch_skinny_la<1, 8, 2, 1, LNS>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);
+  if (M <= 24) return launch_skinny_la<2, 8, 6, 2, LNS>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);
+  if (M <= 32) return launch_skinny_la<2, 8, 8, 2, LNS>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);
+  if (M <= 40) return launch_skinny_la<1, 8, 10, 3, LNS>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);
+  return launch_skinny_la<1, 8, 12, 3, LNS>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);
 }
 
 hipError_t launch_skinny(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws,
                          int M, int N, int K, int gps, int sk, int nt, int waves, hipStream_t stream,
                          const LoraArgs* la) {
   if (M < 1 || M > kSkinnyMaxRows) return hipErrorInvalidValue;
+  if (la != nullptr) {
+    if (waves != 8) return hipErrorInvalidValue;
+    switch (lora_steps(la->R)) {
+      case 1: return launch_skinny_lora<1>(x, w, s, y, ws, M, N, K, gps, sk, nt, stream, *la);
+      case 2: return launch_skinny_lora<2>(x, w, s, y, ws, M, N, K, gps, sk, nt, stream, *la);
+      default: return launch_skinny_lora<4>(x, w, s, y, ws, M, N, K, gps, sk, nt, stream, *la);
+    }
+  }
   // only the row quads of X that hold rows < M are loaded; two row tiles of
   // 16 past 16 rows (8 waves of 1 or 2 column tiles), three past 32 rows (8
   // waves of 1 column tile)
-#define W4A16_SKINNY(NTT, WV)                                                                              \
-  if (nt == NTT && waves == WV) {                                                                          \
-    if (M <= 4) return launch_skinny_t<NTT, WV, 1>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);          \
-    if (M <= 8) return launch_skinny_t<NTT, WV, 2>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);          \
-    if (M <= 12) return launch_skinny_t<NTT, WV, 3>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);         \
-    if (M <= 16) return launch_skinny_t<NTT, WV, 4>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);         \
-    if constexpr (WV == 8 && NTT <= 2) {                                                                   \
-      if (M <= 24) return launch_skinny_t<NTT, WV, 6, 2>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);    \
-      if (M <= 32) return launch_skinny_t<NTT, WV, 8, 2>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);    \
-      if constexpr (NTT == 1) { /* three row tiles: one column tile fits the registers */                  \
-        if (M <= 40) return launch_skinny_t<NTT, WV, 10, 3>(x, w, s, y, ws, M, N, K, gps, sk, stream, la); \
-        return launch_skinny_t<NTT, WV, 12, 3>(x, w, s, y, ws, M, N, K, gps, sk, stream, la);              \
-      }                                                                                                    \
-    }                                                                                                      \
-    return hipErrorInvalidValue;                                                                           \
+#define W4A16_SKINNY(NTT, WV)                                                                           \
+  if (nt == NTT && waves == WV) {                                                                       \
+    if (M <= 4) return launch_skinny_t<NTT, WV, 1>(x, w, s, y, ws, M, N, K, gps, sk, stream);           \
+    if (M <= 8) return launch_skinny_t<NTT, WV, 2>(x, w, s, y, ws, M, N, K, gps, sk, stream);           \
+    if (M <= 12) return launch_skinny_t<NTT, WV, 3>(x, w, s, y, ws, M, N, K, gps, sk, stream);          \
+    if (M <= 16) return launch_skinny_t<NTT, WV, 4>(x, w, s, y, ws, M, N, K, gps, sk, stream);          \
+    if constexpr (WV == 8 && NTT <= 2) {                                                                \
+      if (M <= 24) return launch_skinny_t<NTT, WV, 6, 2>(x, w, s, y, ws, M, N, K, gps, sk, stream);     \
+      if (M <= 32) return launch_skinny_t<NTT, WV, 8, 2>(x, w, s, y, ws, M, N, K, gps, sk, stream);     \
+      if constexpr (NTT == 1) { /* three row tiles: one column tile fits the registers */               \
+        if (M <= 40) return launch_skinny_t<NTT, WV, 10, 3>(x, w, s, y, ws, M, N, K, gps, sk, stream);  \
+        return launch_skinny_t<NTT, WV, 12, 3>(x, w, s, y, ws, M, N, K, gps, sk, stream);               \
+      }                                                                                                 \
+    }                                                                                                   \
+    return hipErrorInvalidValue;                                                                        \
   }
   W4A16_SKINNY(1, 8)
   W4A16_SKINNY(2, 8)

@@ -90,10 +90,12 @@ __device__ __forceinline__ void wait_stages(int later) {
 
 }  // namespace
 
-// LA: nothing, or the LoraArgs of per-row adapters, whose products join the
-// accumulators: the four waves of a column tile, in all K slices, take the
-// adapters in turn, before their sums are added up.
-template <int SG, int NS, class... LA>
+// LA: nothing, or the LoraArgs of per-row adapters (ranks up to 32 LNS), whose
+// products join the accumulators: the four waves of a column tile, in all K
+// slices, take the adapters in turn, before their sums are added up. What they
+// need is requested with the last DMA, so that it arrives while the last
+// stages are computed (the waits for those then cover it too).
+template <int SG, int NS, int LNS, class... LA>
 __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_t* __restrict__ x,
                                                                    const uint8_t* __restrict__ w,
                                                                    const uint16_t* __restrict__ s,
@@ -169,6 +171,11 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   const bf16x8 bneg = __builtin_bit_cast(bf16x8, u32x4{neg136, neg136, neg136, neg136});
 
   const int ct = wv & 1;                       // the wave's column tile
+  [[maybe_unused]] const int part = (wv >> 1) + 4 * slice, nparts = 4 * (int)gridDim.y;
+  auto adapters = [&] {
+    if constexpr (sizeof...(LA) > 0) return LoraSmall<1, 1, LNS>(la..., row_id, lane);
+    else return 0;
+  }();
   f32x4 acc1[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
   f32x4& acc = acc1[0][0];
 
@@ -217,6 +224,9 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   for (int j = 0; j < nst; ++j) {
     const bool ahead = j + NS - 1 < nst;
     if (ahead) issue(j + NS - 1, (j + NS - 1) % NS);
+    if constexpr (sizeof...(LA) > 0) {
+      if (j == max(0, nst - NS)) (adapters.start(la, n0 + 16 * ct, lane, part, nparts), ...);
+    }
     const uint8_t* sb = lds + (j % NS) * ST::kBytes;
 #pragma unroll
     for (int u = 0; u < SG / 4; ++u) {
@@ -236,7 +246,8 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   }
 
   if constexpr (sizeof...(LA) > 0) {
-    (lora_rows<1, 1>(acc1, la, row_id, n0 + 16 * ct, lane, (wv >> 1) + 4 * slice, 4 * (int)gridDim.y), ...);
+    if (nst == 0) (adapters.start(la, n0 + 16 * ct, lane, part, nparts), ...);
+    (adapters.add(acc1, la, n0 + 16 * ct, lane, part, nparts), ...);
   }
 
   // ---- the four waves of a column tile: summed in wave order (waves ct,
@@ -272,35 +283,42 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
 
 bool skinny_lds_fits(int M, int gps) { return M >= 1 && M <= 16 && gps >= 1; }
 
-template <int SG, int NS, class... LA>
+template <int SG, int NS, int LNS, class... LA>
 static hipError_t launch_sl_la(const uint16_t* x, const uint8_t* w, const uint16_t* s, void* out, int M, int N, int K,
                                int gps, int sk, hipStream_t stream, LA... la) {
   constexpr int lds = NS * SLStage<SG>::kBytes;
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t ea =
-      ensure_dyn_lds(reinterpret_cast<const void*>(&skinny_lds_kernel<SG, NS, LA...>), lds, lds_set);
+      ensure_dyn_lds(reinterpret_cast<const void*>(&skinny_lds_kernel<SG, NS, LNS, LA...>), lds, lds_set);
   if (ea != hipSuccess) return ea;
-  hipLaunchKernelGGL((skinny_lds_kernel<SG, NS, LA...>), dim3((N + kSLCols - 1) / kSLCols, sk), dim3(64 * kSLWaves),
+  hipLaunchKernelGGL((skinny_lds_kernel<SG, NS, LNS, LA...>), dim3((N + kSLCols - 1) / kSLCols, sk), dim3(64 * kSLWaves),
                      lds, stream, x, w, s, out, M, N, K, gps, la...);
   return hipGetLastError();
 }
 
 template <int SG, int NS>
 static hipError_t launch_sl(const uint16_t* x, const uint8_t* w, const uint16_t* s, void* out, int M, int N, int K,
-                            int gps, int sk, hipStream_t stream, const LoraArgs* la) {
-  if (la != nullptr) return launch_sl_la<SG, NS>(x, w, s, out, M, N, K, gps, sk, stream, *la);
-  return launch_sl_la<SG, NS>(x, w, s, out, M, N, K, gps, sk, stream);
+                            int gps, int sk, hipStream_t stream) {
+  return launch_sl_la<SG, NS, 0>(x, w, s, out, M, N, K, gps, sk, stream);
 }
 
 hipError_t launch_skinny_lds(const uint16_t* x, const uint8_t* w, const uint16_t* s, uint16_t* y, float* ws, int M,
                              int N, int K, int gps, int sk, int geometry, hipStream_t stream, const LoraArgs* la) {
   if (!skinny_lds_fits(M, gps)) return hipErrorInvalidValue;
   void* out = sk > 1 ? static_cast<void*>(ws) : static_cast<void*>(y);
+  if (la != nullptr) {   // the automatic geometry only
+    if (geometry != 3) return hipErrorInvalidValue;
+    switch (lora_steps(la->R)) {
+      case 1: return launch_sl_la<4, 4, 1>(x, w, s, out, M, N, K, gps, sk, stream, *la);
+      case 2: return launch_sl_la<4, 4, 2>(x, w, s, out, M, N, K, gps, sk, stream, *la);
+      default: return launch_sl_la<4, 4, 4>(x, w, s, out, M, N, K, gps, sk, stream, *la);
+    }
+  }
   switch (geometry) {
-    case 0: return launch_sl<8, 3>(x, w, s, out, M, N, K, gps, sk, stream, la);   // 3 x 49 KiB
-    case 1: return launch_sl<4, 6>(x, w, s, out, M, N, K, gps, sk, stream, la);   // 6 x 24.5 KiB
-    case 2: return launch_sl<4, 5>(x, w, s, out, M, N, K, gps, sk, stream, la);
-    case 3: return launch_sl<4, 4>(x, w, s, out, M, N, K, gps, sk, stream, la);
+    case 0: return launch_sl<8, 3>(x, w, s, out, M, N, K, gps, sk, stream);   // 3 x 49 KiB
+    case 1: return launch_sl<4, 6>(x, w, s, out, M, N, K, gps, sk, stream);   // 6 x 24.5 KiB
+    case 2: return launch_sl<4, 5>(x, w, s, out, M, N, K, gps, sk, stream);
+    case 3: return launch_sl<4, 4>(x, w, s, out, M, N, K, gps, sk, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -105,59 +105,60 @@ __device__ __forceinline__ void lora_mac(f32x4 (&acc)[SN], const u32x4 (&hi)[NS]
   }
 }
 
-// ---- tile kernels: h of the tile's rows staged in LDS, read by every wave;
-// part = K slice of nparts, so that the slices share the adapters.
-// Row r holds the ranks up to 32 NS (zeros past R) and is 16 bytes longer, an
-// odd multiple of 16 bytes, so that the 16 rows of a fragment read spread over
-// the banks; the part that is left follows behind the rows' leading part, and
-// the rows' adapters behind both. The row length is a constant: every fragment
-// read is one base register and an immediate (with a row length from R the
-// addresses of all row tiles stayed live across the adapters and the 144-row
-// tile spilled).
-constexpr int lora_row_bytes(int NS) { return 64 * NS + 16; }
-constexpr int lora_lds_bytes(int rows) { return rows * (2 * lora_row_bytes(kLoraMaxRank / 32) + 4); }
+// ---- tile kernels: h of the tile's rows in LDS, read by every wave. The two
+// parts lie in two of the pipeline's stages, which are free while the last
+// group is computed; the DMA that fills them is issued ahead of that group, so
+// that its flight is covered (h staged through registers behind the last
+// barrier: three tile rounds of 1322 x 19456 x 2560, rank 64, 2-3 us longer).
+// Row r holds the ranks up to 32 NS (zeros past R) in 16-byte chunks, chunk c
+// in slot c ^ lora_swz(r): the 16 rows of a fragment read (chunks 4 st + 0..3)
+// then cover all banks evenly.
+__device__ __forceinline__ int lora_swz(int r, int lg) {   // NS = 1 << lg
+  return lg == 0 ? 0 : lg == 1 ? 4 * ((r >> 1) & 1) : 4 * (r & 3);
+}
+__device__ __forceinline__ int lora_lg(int R) { return R <= 32 ? 0 : R <= 64 ? 1 : 2; }
+// a part of h, then (behind the first part) the rows' adapters
+constexpr int lora_plane_bytes(int rows) { return rows * 2 * kLoraMaxRank + (rows + 63) / 64 * 256; }
 
-template <int MS, int SN, int NS, int NTHR>
-__device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds, const LoraArgs& la, int row0, int live,
-                                             int n0, int tid, int part, int nparts) {
-  constexpr int ROWS = 16 * MS, Q = LoraRows<MS>::Q, RB = lora_row_bytes(NS), OCT = 4 * NS;
-  int32_t* sid = reinterpret_cast<int32_t*>(lds + 2 * ROWS * RB);
-  for (int r = tid; r < ROWS; r += NTHR) {
-    const int id = r < live ? la.ids[row0 + r] : -1;
-    sid[r] = (uint32_t)id < (uint32_t)la.L ? id : -1;
-  }
-  // (rows without an adapter hold any bits and are never selected)
+// 1 KiB DMA instructions, dealt out over NW waves; rows past `live` and ranks
+// past R are zeros (past the extent).
+template <int MS, int NW>
+__device__ __forceinline__ void lora_tile_fetch(uint8_t* hi, uint8_t* lo, const LoraArgs& la, int row0, int live,
+                                                int lane, int wv) {
+  const int lg = lora_lg(la.R);
   const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
   const __amdgpu_buffer_rsrc_t rh = make_rsrc(la.h, 2u * plane);
-  constexpr int IT = (ROWS * OCT + NTHR - 1) / NTHR;
-  u32x4 a[IT], b[IT];
-#pragma unroll
-  for (int u = 0; u < IT; ++u) {
-    const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
-    const bool ok = r < live && 8 * o < la.R;
-    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)o) * 2u;
-    a[u] = ld128(rh, ok ? off : 0xFFFFFFF0u);
-    b[u] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
+  for (int q = wv; q < MS << lg; q += NW) {
+    const int i = 64 * q + lane, r = i >> (2 + lg), c = (i & ((4 << lg) - 1)) ^ lora_swz(r, lg);
+    const bool ok = r < live && 8 * c < la.R;
+    const uint32_t off = ((uint32_t)(row0 + r) * (uint32_t)la.R + 8u * (uint32_t)c) * 2u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rh, (__attribute__((address_space(3))) void*)(hi + 1024 * q), 16,
+                                             ok ? off : 0xFFFFFFF0u, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rh, (__attribute__((address_space(3))) void*)(lo + 1024 * q), 16,
+                                             ok ? plane + off : 0xFFFFFFF0u, 0, 0, 0);
   }
-#pragma unroll
-  for (int u = 0; u < IT; ++u) {
-    const int i = tid + u * NTHR, r = i / OCT, o = i % OCT;
-    if (ROWS * OCT % NTHR == 0 || r < ROWS) {
-      *reinterpret_cast<u32x4*>(lds + r * RB + 16 * o) = a[u];
-      *reinterpret_cast<u32x4*>(lds + (ROWS + r) * RB + 16 * o) = b[u];
-    }
-  }
-  __syncthreads();
+  // rows past M: zeros, which lora_tile_add does not look at
+  if (wv < LoraRows<MS>::Q)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(la.ids, (uint32_t)la.M * 4u),
+                                             (__attribute__((address_space(3))) void*)(hi + 4096 * MS + 256 * wv), 4,
+                                             4u * (uint32_t)(row0 + 64 * wv + lane), 0, 0, 0);
+}
 
-  const int lane = tid & 63, m16 = lane & 15, kb = lane >> 4;
-  int id[Q];
-#pragma unroll
-  for (int q = 0; q < Q; ++q) id[q] = 64 * q + lane < ROWS ? sid[64 * q + lane] : -1;
-  LoraRows<MS> adapters(id);
-  const uint8_t* base = lds + m16 * RB + 16 * kb;
+template <int MS, int SN, int NS>
+__device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], const uint8_t* hi, const uint8_t* lo,
+                                             const int (&id)[LoraRows<MS>::Q], const LoraArgs& la, int n0, int lane,
+                                             int part, int nparts) {
   // adapters whose B fragments are in flight at once (in the registers that the
   // accumulators of a short tile leave)
-  constexpr int NB = (MS <= 5 ? 8 : 4) / NS;
+  constexpr int NB = (MS <= 5 ? 8 : 4) / NS, Q = LoraRows<MS>::Q, LG = NS == 1 ? 0 : NS == 2 ? 1 : 2;
+  const int m16 = lane & 15, kb = lane >> 4;
+  LoraRows<MS> adapters(id);
+  // rows 16 ms + m16 share m16's swizzle: chunk 4 st + kb of row tile ms is
+  // 64 NS * 16 ms + 64 (st ^ swizzle / 4) behind the lane's row
+  uint32_t at[NS];
+#pragma unroll
+  for (int st = 0; st < NS; ++st)
+    at[st] = (uint32_t)m16 * (64u * NS) + 16u * (uint32_t)((4 * st + kb) ^ lora_swz(m16, LG));
   for (;;) {
     int l[NB];
     uint64_t rows[NB][Q];
@@ -174,25 +175,33 @@ __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], uint8_t* lds,
         constexpr int ms = decltype(i)::value;
         const uint32_t mine = (uint32_t)(rows[k][ms / 4] >> (16 * (ms % 4))) & 0xFFFFu;
         if (mine != 0) {
-          u32x4 hi[NS], lo[NS];
+          u32x4 h[NS], g[NS];
 #pragma unroll
           for (int st = 0; st < NS; ++st) {
-            hi[st] = *reinterpret_cast<const u32x4*>(base + 16 * ms * RB + 64 * st);
-            lo[st] = *reinterpret_cast<const u32x4*>(base + (ROWS + 16 * ms) * RB + 64 * st);
+            h[st] = *reinterpret_cast<const u32x4*>(hi + at[st] + 1024 * NS * ms);
+            g[st] = *reinterpret_cast<const u32x4*>(lo + at[st] + 1024 * NS * ms);
           }
-          lora_mac<SN, NS>(acc[ms], hi, lo, bf[k], mine, kb);
+          lora_mac<SN, NS>(acc[ms], h, g, bf[k], mine, kb);
         }
       });
     }
   }
 }
 
-template <int MS, int SN, int NTHR>
-__device__ __forceinline__ void lora_tile(f32x4 (&acc)[MS][SN], uint8_t* lds, const LoraArgs& la, int row0, int live,
-                                          int n0, int tid, int part, int nparts) {
-  if (la.R <= 32) lora_tile_ns<MS, SN, 1, NTHR>(acc, lds, la, row0, live, n0, tid, part, nparts);
-  else if (la.R <= 64) lora_tile_ns<MS, SN, 2, NTHR>(acc, lds, la, row0, live, n0, tid, part, nparts);
-  else lora_tile_ns<MS, SN, 4, NTHR>(acc, lds, la, row0, live, n0, tid, part, nparts);
+// behind a wait for the DMA and a barrier; part = K slice of nparts, so that
+// the slices share the adapters
+template <int MS, int SN>
+__device__ __forceinline__ void lora_tile_add(f32x4 (&acc)[MS][SN], const uint8_t* hi, const uint8_t* lo,
+                                              const LoraArgs& la, int live, int n0, int lane, int part, int nparts) {
+  int id[LoraRows<MS>::Q];
+#pragma unroll
+  for (int q = 0; q < LoraRows<MS>::Q; ++q) {
+    const int i = reinterpret_cast<const int*>(hi + 4096 * MS)[64 * q + lane];
+    id[q] = 64 * q + lane < live && (uint32_t)i < (uint32_t)la.L ? i : -1;
+  }
+  if (la.R <= 32) lora_tile_ns<MS, SN, 1>(acc, hi, lo, id, la, n0, lane, part, nparts);
+  else if (la.R <= 64) lora_tile_ns<MS, SN, 2>(acc, hi, lo, id, la, n0, lane, part, nparts);
+  else lora_tile_ns<MS, SN, 4>(acc, hi, lo, id, la, n0, lane, part, nparts);
 }
 
 // ---- small batch (M <= 16 MS rows): h read straight into the fragments by the

@@ -465,7 +465,17 @@ __global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs arg
       wait_vm_barrier<0>();
     }
   }
+  // adapters: their h goes into the two stages that the last group leaves free
+  static_assert(sizeof...(LA) == 0 || lora_plane_bytes(BM) <= ST::kBytes, "each part of h fits a stage");
+  [[maybe_unused]] auto adapter_fetch = [&] {
+    (lora_tile_fetch<MS, kNW>(lds + stage_off(ng % NSTAGE), lds + stage_off((ng + 1) % NSTAGE), la, row0, rows, lane,
+                              wv),
+     ...);
+  };
   for (int j = 0; j < ng; ++j) {
+    if constexpr (sizeof...(LA) > 0) {
+      if (j == ng - 1) adapter_fetch();
+    }
     const int g = gb + j;
     const bool ahead = j + NSTAGE - 1 < ng;
     if (ahead) issue(g + NSTAGE - 1, (j + NSTAGE - 1) % NSTAGE);
@@ -486,11 +496,13 @@ __global__ __launch_bounds__(64 * kNW) void prefill_kernel(const PrefillArgs arg
     }
   }
 
-  // ---- adapters (the stages are free once every wave is past its last group)
+  // ---- adapters
   if constexpr (sizeof...(LA) > 0) {
-    static_assert(lora_lds_bytes(BM) <= NSTAGE * ST::kBytes, "staged rows fit the stages' LDS");
-    __syncthreads();
-    (lora_tile<MS, SN, 64 * kNW>(acc, lds, la, row0, rows, n0 + TN * wv, tid, slice, (int)gridDim.y), ...);
+    if (ng == 0) adapter_fetch();
+    wait_vm_barrier<0>();
+    (lora_tile_add<MS, SN>(acc, lds + stage_off(ng % NSTAGE), lds + stage_off((ng + 1) % NSTAGE), la, rows,
+                           n0 + TN * wv, lane, slice, (int)gridDim.y),
+     ...);
   }
 
   // ---- epilogue: lane holds rows 16 ms + 4 kb + i of column TN wv + 16 ns + m16

@@ -12,6 +12,7 @@
 //                 dw[t, j] = sum_n dy[t, n] z[pos[t, j], n] in fp32
 // The gradient of gather is combine without weights. No atomics on results:
 // every result is bitwise reproducible.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -66,14 +67,24 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float c) {
 
 constexpr int kBatch = 4;   // slots of a token whose rows are in flight together
 
-// Sort: a block of 16 waves (8 where G needs the LDS) takes tiles of 256 slots
-// per wave in turn.
+// Sort: a block of 16 waves (fewer where G needs the LDS) takes tiles of 256
+// slots per wave in turn.
 constexpr int kSortPer = 4;                 // slots per lane and tile
 constexpr int kSortMaxBlocks = 256;
 constexpr int kSortSingle = 8192;           // slots that one block takes alone
 
 __device__ __forceinline__ int bin_of(int e, int G) {
   return (uint32_t)e < (uint32_t)G ? e : G;   // bin G: dropped
+}
+
+// inclusive sum over the wave's lanes
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
 }
 
 // Counts the bins of slots [lo, hi) into cnt (LDS, zeroed). The lanes that
@@ -134,6 +145,8 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
   int32_t* at = lds;             // [nb] where the block's next slot of each bin goes
   int32_t* total = lds + nb;     // [nb] slots of each bin: aliased by the waves' counts below
   int32_t* run = lds + nb;       // [W][nb]
+  int32_t* shift = run + W * nb;   // [nb]
+  int2* place = reinterpret_cast<int2*>(lds + ((W + 2) * nb + 1) / 2 * 2);   // [tile]
   __shared__ int32_t wave_sum[W];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t lo = (int64_t)blockIdx.x * chunk, hi = lo + chunk < S ? lo + chunk : S;
@@ -167,12 +180,7 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
   const int g0 = min(nb, tid * per), g1 = min(nb, g0 + per);
   int mine = 0;
   for (int g = g0; g < g1; ++g) mine += total[g];
-  int in = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(in, d);
-    if (lane >= d) in += o;
-  }
+  const int in = wave_scan(mine, lane);
   if (lane == 63) wave_sum[wv] = in;
   __syncthreads();
   int below = in - mine;
@@ -209,23 +217,55 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
       if (e[i] >= 0 && (same >> lane) == 1ull) r[e[i]] = rank[i] + 1;
     }
     __syncthreads();
-    for (int g = tid; g < nb; g += NTHR) {
+    // the waves' counts become their starts
+    int own = 0;
+    for (int g = g0; g < g1; ++g) {
       int a = at[g];
+      shift[g] = a;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const int c = run[w * nb + g];
         run[w * nb + g] = a;
         a += c;
       }
+      own += a - shift[g];
       at[g] = a;
+    }
+    if (blocks > 1) {
+      // the bins' starts within the tile: shift = global row minus place in the tile
+      const int sum = wave_scan(own, lane);
+      if (lane == 63) wave_sum[wv] = sum;
+      __syncthreads();
+      int first = sum - own;
+#pragma unroll
+      for (int w = 0; w < W; ++w) first += w < wv ? wave_sum[w] : 0;
+      for (int g = g0; g < g1; ++g) {
+        const int n = at[g] - shift[g];
+        shift[g] -= first;
+        first += n;
+      }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kSortPer; ++i) {
       if (e[i] >= 0) {
         const int p = r[e[i]] + rank[i];
-        order[p] = (int32_t)(s0 + 64 * i);
-        pos[s0 + 64 * i] = e[i] < G ? p : -1;
+        const int s = (int)(s0 + 64 * i);
+        pos[s] = e[i] < G ? p : -1;
+        if (blocks > 1) place[p - shift[e[i]]] = make_int2(p, s);
+        else order[p] = s;
+      }
+    }
+    if (blocks > 1) {
+      // order goes through LDS in bin order, so that a bin's slots of the tile
+      // leave as one run (65536 x 8 slots, 128 experts: 12.1 -> 11.1 us for
+      // this kernel; one block's few slots are 0.7 us faster without)
+      __syncthreads();
+      const int n = hi - t0 < kSortPer * NTHR ? (int)(hi - t0) : kSortPer * NTHR;
+#pragma unroll
+      for (int i = 0; i < kSortPer; ++i) {
+        const int q = i * NTHR + tid;
+        if (q < n) order[place[q].x] = place[q].y;
       }
     }
   }
@@ -414,7 +454,8 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t
 // ---------------------------------------------------------------- launchers
 // One block up to kSortSingle slots (one launch), else whole tiles per block,
 // at most kSortMaxBlocks blocks (each reads all blocks' counts).
-static int sort_waves(int G) { return G < 2048 ? 16 : 8; }
+// waves of a block: what G leaves of the LDS
+static int sort_waves(int G) { return G <= 1024 ? 16 : G <= 2048 ? 8 : 4; }
 static int64_t sort_chunk(int64_t S, int G) {
   const int64_t tile = 64 * kSortPer * sort_waves(G);
   if (S <= kSortSingle) return kSortSingle;
@@ -433,10 +474,12 @@ static hipError_t launch_sort_w(const int32_t* ids, int32_t* order, int32_t* pos
   const int blocks = expert_sort_blocks(S, G);
   int bits = 1;
   while ((1 << bits) <= G) ++bits;
-  const int lds1 = (G + 1) * 4, lds2 = (G + 1) * 4 * (1 + W);
+  const int lds1 = (G + 1) * 4;
+  // starts, waves' counts, shifts; then the tile's (row, slot) pairs
+  const int lds2 = ((G + 1) * (2 + W) + 1) / 2 * 8 + 64 * W * kSortPer * 8;
   static std::atomic<uint64_t> set{0};
   const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&expert_scatter_kernel<W>),
-                                       ((W == 16 ? 2047 : kExpertMaxGroups) + 1) * 4 * (1 + W), set);
+                                       160 * 1024 - 512, set);
   if (ea != hipSuccess) return ea;
   if (blocks > 1) {
     hipLaunchKernelGGL(expert_hist_kernel<W>, dim3(blocks), dim3(64 * W), lds1, stream, ids, ws, S, G, chunk);
@@ -454,8 +497,11 @@ hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, 
     hipLaunchKernelGGL(expert_zero_kernel, dim3(1), dim3(256), 0, stream, m_sizes, G);
     return hipGetLastError();
   }
-  return sort_waves(G) == 16 ? launch_sort_w<16>(ids, order, pos, m_sizes, S, G, ws, stream)
-                             : launch_sort_w<8>(ids, order, pos, m_sizes, S, G, ws, stream);
+  switch (sort_waves(G)) {
+    case 16: return launch_sort_w<16>(ids, order, pos, m_sizes, S, G, ws, stream);
+    case 8: return launch_sort_w<8>(ids, order, pos, m_sizes, S, G, ws, stream);
+    default: return launch_sort_w<4>(ids, order, pos, m_sizes, S, G, ws, stream);
+  }
 }
 
 // The variant by the rows: threads per token, the power of two that holds the
@@ -474,7 +520,7 @@ static hipError_t by_rows(int64_t rows, int width, F launch) {
     else if (chunks <= 128) launch(aligned, std::integral_constant<int, 128>{}, nt);
     else launch(aligned, std::integral_constant<int, 256>{}, nt);
   };
-  const bool nt = rows * width * 2 > ((int64_t)256 << 20);
+  const bool nt = rows * width > ((int64_t)128 << 20);   // values of 2 bytes
   if (width % 8 == 0 && nt) go(std::true_type{}, std::true_type{});
   else if (width % 8 == 0) go(std::true_type{}, std::false_type{});
   else if (nt) go(std::false_type{}, std::true_type{});
@@ -482,11 +528,14 @@ static hipError_t by_rows(int64_t rows, int width, F launch) {
   return hipGetLastError();
 }
 
-// x: tokens, 256 / tpt per workgroup (the kernels stride over what is beyond
-// the grid); y: 8 tpt columns each where `split`
+// x: tokens, 256 / tpt per workgroup; y: 8 tpt columns each where `split` (the
+// kernels stride over what is beyond the grid, which has at most 2^23
+// workgroups: a launch takes fewer than 2^32 threads)
 static dim3 row_grid(int64_t T, int width, int tpt, bool split) {
-  const int64_t x = (T + 256 / tpt - 1) / (256 / tpt), y = split ? ((int64_t)width + 8 * tpt - 1) / (8 * tpt) : 1;
-  return dim3((unsigned)(x < (1 << 20) ? x : 1 << 20), (unsigned)(y < 64 ? y : 64));
+  const int64_t most = (int64_t)1 << 20;
+  const int64_t x = std::min((T + 256 / tpt - 1) / (256 / tpt), most);
+  const int64_t y = split ? ((int64_t)width + 8 * tpt - 1) / (8 * tpt) : 1;
+  return dim3((unsigned)x, (unsigned)std::min(y, std::min<int64_t>(65535, 8 * most / x)));
 }
 
 hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int k, int64_t rows,

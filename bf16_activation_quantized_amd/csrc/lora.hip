@@ -55,9 +55,10 @@ __device__ __forceinline__ void shrink_row(const uint16_t* __restrict__ x, const
 #pragma unroll
   for (int r = 0; r < RP; ++r) acc[r] = 0.0f;
   u32x4 xv[2], av[2][RP];
-  auto issue = [&](int u, uint32_t c) {
-    const uint32_t o = 1024u * c + 16u * (uint32_t)lane;
-    const bool ok = o < KB;   // pieces past the row read zeros
+  const int pieces = (K + 511) / 512;
+  auto issue = [&](int u, int c) {
+    const uint32_t o = 1024u * (uint32_t)c + 16u * (uint32_t)lane;
+    const bool ok = c < pieces && o < KB;   // past the row: zeros
     xv[u] = ld128(rx, ok ? o : kOutside);
 #pragma unroll
     for (int r = 0; r < RP; ++r) av[u][r] = ld128(ra, ok ? o + (uint32_t)r * KB : kOutside);
@@ -74,12 +75,11 @@ __device__ __forceinline__ void shrink_row(const uint16_t* __restrict__ x, const
       acc[r] = __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(v.w), as_bf16x2(w.w), acc[r], false);
     }
   };
-  const int pieces = (K + 511) / 512;
-  issue(0, (uint32_t)wv);
+  issue(0, wv);
   for (int c = wv; c < pieces; c += 2 * kRowWaves) {
-    issue(1, (uint32_t)(c + kRowWaves));
+    issue(1, c + kRowWaves);
     add(0);
-    issue(0, (uint32_t)(c + 2 * kRowWaves));
+    issue(0, c + 2 * kRowWaves);
     add(1);
   }
 #pragma unroll

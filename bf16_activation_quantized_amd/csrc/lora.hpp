@@ -206,8 +206,8 @@ __device__ __forceinline__ void lora_tile_add(f32x4 (&acc)[MS][SN], const uint8_
 
 // ---- small batch (M <= 16 MS rows): h read straight into the fragments by the
 // waves that hold an adapter, `part` of `nparts`; 4 / NS adapters' B fragments
-// are in flight at once, the first ones together with h. start() requests
-// them; add() uses them, and goes on with the adapters that are left.
+// are in flight at once, together with h of their rows. start() requests them;
+// add() uses them, and goes on with the adapters that are left.
 
 // the adapter of row `lane`: a load at the kernel's start, used at its end
 __device__ __forceinline__ int lora_id(const LoraArgs& la, int lane) { return lane < la.M ? la.ids[lane] : -1; }
@@ -226,16 +226,18 @@ struct LoraSmall {
   __device__ __forceinline__ LoraSmall(const LoraArgs& la, int row_id, int lane)
       : id{lane < 16 * MS && (uint32_t)row_id < (uint32_t)la.L ? row_id : -1}, adapters(id) {}
 
-  __device__ __forceinline__ void batch(const LoraArgs& la, int n0, int lane, int part, int nparts) {
+  // the next adapters' B, and h of their rows (the other rows' loads go past
+  // the extent and move nothing)
+  __device__ __forceinline__ void start(const LoraArgs& la, int n0, int lane, int part, int nparts) {
+    uint64_t own = 0;
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       l[k] = (k == 0 || l[k > 0 ? k - 1 : 0] >= 0) ? adapters.next(id, rows[k], part, nparts) : -1;
-      if (l[k] >= 0) lora_load_b<SN, NS>(bf[k], la, l[k], n0, lane);
+      if (l[k] >= 0) {
+        lora_load_b<SN, NS>(bf[k], la, l[k], n0, lane);
+        own |= rows[k][0];
+      }
     }
-  }
-
-  __device__ __forceinline__ void start(const LoraArgs& la, int n0, int lane, int part, int nparts) {
-    batch(la, n0, lane, part, nparts);
     if (l[0] < 0) return;
     const int m16 = lane & 15, kb = lane >> 4;
     const uint32_t plane = (uint32_t)la.M * (uint32_t)la.R * 2u;
@@ -245,7 +247,7 @@ struct LoraSmall {
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
         const int r = 32 * st + 8 * kb, m = 16 * ms + m16;
-        const bool ok = m < la.M && r < la.R;
+        const bool ok = ((own >> m) & 1) && r < la.R;
         const uint32_t off = ((uint32_t)m * (uint32_t)la.R + (uint32_t)r) * 2u;
         hi[ms][st] = ld128(rh, ok ? off : 0xFFFFFFF0u);
         lo[ms][st] = ld128(rh, ok ? plane + off : 0xFFFFFFF0u);
@@ -264,7 +266,7 @@ struct LoraSmall {
           if (mine != 0) lora_mac<SN, NS>(acc[ms], hi[ms], lo[ms], bf[k], mine, lane >> 4);
         });
       }
-      batch(la, n0, lane, part, nparts);
+      start(la, n0, lane, part, nparts);
     }
   }
 };

@@ -274,10 +274,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lora_shrink_tile_kernel(const 
 // Few rows one by one, more in row tiles: the row kernel reads A once per row,
 // the tile kernel once per adapter of 16 rows, but through fewer workgroups
 // and in shorter runs. The whole call, row against tile kernel: 64 x 8192 x
-// 8192, rank 16, an adapter each, 50.1 against 54.9 us; 333 x 2560 x 9728,
-// rank 24, 5 adapters mixed, 58.5 / 62.5; 512 x 8192 x 8192, rank 32, 32
-// adapters, mixed 129.7 / 136.0, one after the other 114.1 / 102.3; 2048 x
-// 4096 x 4096, rank 16, one after the other, 99.0 / 80.2. Turns: about a
+// 8192, rank 16, an adapter each 36.9 / 39.9 us, 4 adapters one after the other
+// 28.5 / 32.9; 100 x 8192 x 4096, rank 64, 8 adapters, mixed 32.4 / 30.6, one
+// after the other 31.4 / 29.4; 333 x 2560 x 9728, group 32, rank 24, 5
+// adapters, mixed 54.5 / 54.6, one after the other 53.2 / 49.3. Turns: about a
 // thousand workgroups, for row tiles of many adapters; one that finds no
 // adapter left to it ends at once.
 template <int GS>
@@ -286,7 +286,7 @@ static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
   p.turns = 1;
   const int64_t MR = (int64_t)p.M * p.R;
   const dim3 threads(64 * kWaves);
-  if (MR <= 8192) {
+  if (MR <= 4096) {
 #define W4A16_ROW(RP) \
   hipLaunchKernelGGL((lora_shrink_row_kernel<RP, GS>), dim3(p.rowsum_blocks + p.M * (p.R / RP)), threads, 0, stream, p)
     // ranks per workgroup: x is read once for all of them, but a few hundred

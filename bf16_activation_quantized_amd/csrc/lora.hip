@@ -299,7 +299,7 @@ static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
     return hipGetLastError();
   }
   const int64_t tiles = (int64_t)((p.M + 15) / 16) * ((p.R + 15) / 16);
-  while (p.turns < 16 && 2 * p.turns <= p.L && tiles * 2 * p.turns <= 1024) p.turns *= 2;
+  while (p.turns < 16 && p.turns < p.L && tiles * 2 * p.turns <= 1024) p.turns *= 2;
   hipLaunchKernelGGL((lora_shrink_tile_kernel<GS>), dim3((unsigned)(p.rowsum_blocks + tiles * p.turns)), threads, 0,
                      stream, p);
   return hipGetLastError();

@@ -176,7 +176,7 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* __restrict__ x, cons
       todo = lead;
       g += kTileWaves;
     }
-    __builtin_amdgcn_sched_barrier(0);   // one fetch's loads together: waits are exact counts
+    __builtin_amdgcn_sched_barrier(0);   // one fetch's loads stay together
   };
   u32x4* tw = tile[wv];
   // lane (m16, kb) of step j: row m16, piece 4 kb + j (k = 32 kb + 8 j + 0..7, the same in both operands)
@@ -277,9 +277,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lora_shrink_tile_kernel(const 
 // 8192, rank 16, an adapter each 36.9 / 39.9 us, 4 adapters one after the other
 // 28.5 / 32.9; 100 x 8192 x 4096, rank 64, 8 adapters, mixed 32.4 / 30.6, one
 // after the other 31.4 / 29.4; 333 x 2560 x 9728, group 32, rank 24, 5
-// adapters, mixed 54.5 / 54.6, one after the other 53.2 / 49.3. Turns: about a
-// thousand workgroups, for row tiles of many adapters; one that finds no
-// adapter left to it ends at once.
+// adapters, mixed 54.5 / 54.6, one after the other 53.2 / 49.3. Turns: as many
+// as there are adapters, up to 16 and about a thousand workgroups, for row
+// tiles of several adapters (the 333 rows mixed: 54.6 us with 4 turns, 50.7
+// with 8); a workgroup that finds no adapter left to it ends at once.
 template <int GS>
 static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
   p.rowsum_blocks = GS != 0 ? (p.M + kWaves - 1) / kWaves : 0;

@@ -36,10 +36,11 @@ template <int MS>
 struct LoraRows {
   static constexpr int Q = (16 * MS + 63) / 64;
   uint64_t todo[Q];
-  int turn = 0;
-  __device__ __forceinline__ explicit LoraRows(const int (&id)[Q]) {
+  int turn;
+  __device__ __forceinline__ void reset(const int (&id)[Q]) {
 #pragma unroll
     for (int q = 0; q < Q; ++q) todo[q] = __ballot(id[q] >= 0);
+    turn = 0;
   }
   // The next adapter (in the order of their first row) whose turn is `part` of
   // `nparts`: its id, or -1 when none is left, and its rows.
@@ -152,7 +153,8 @@ __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], const uint8_t
   // accumulators of a short tile leave)
   constexpr int NB = (MS <= 5 ? 8 : 4) / NS, Q = LoraRows<MS>::Q, LG = NS == 1 ? 0 : NS == 2 ? 1 : 2;
   const int m16 = lane & 15, kb = lane >> 4;
-  LoraRows<MS> adapters(id);
+  LoraRows<MS> adapters;
+  adapters.reset(id);
   // rows 16 ms + m16 share m16's swizzle: chunk 4 st + kb of row tile ms is
   // 64 NS * 16 ms + 64 (st ^ swizzle / 4) behind the lane's row
   uint32_t at[NS];
@@ -206,7 +208,7 @@ __device__ __forceinline__ void lora_tile_add(f32x4 (&acc)[MS][SN], const uint8_
 
 // ---- small batch (M <= 16 MS rows): h read straight into the fragments by the
 // waves that hold an adapter, `part` of `nparts`; 4 / NS adapters' B fragments
-// are in flight at once, together with h of their rows. start() requests them;
+// are in flight at once, together with h of their rows. begin() requests them;
 // add() uses them, and goes on with the adapters that are left.
 
 // the adapter of row `lane`: a load at the kernel's start, used at its end
@@ -217,14 +219,18 @@ struct LoraSmall {
   static_assert(MS <= 4, "one row per lane");
   static constexpr int NB = 4 / NS;
   int id[1];
-  LoraRows<MS> adapters;
+  LoraRows<MS> adapters;   // from begin() on
   int l[NB];
   uint64_t rows[NB][1];
   bf16x8 bf[NB][NS][SN];
   u32x4 hi[MS][NS], lo[MS][NS];
 
-  __device__ __forceinline__ LoraSmall(const LoraArgs& la, int row_id, int lane)
-      : id{lane < 16 * MS && (uint32_t)row_id < (uint32_t)la.L ? row_id : -1}, adapters(id) {}
+  // (here row_id is waited for)
+  __device__ __forceinline__ void begin(const LoraArgs& la, int row_id, int n0, int lane, int part, int nparts) {
+    id[0] = lane < 16 * MS && (uint32_t)row_id < (uint32_t)la.L ? row_id : -1;
+    adapters.reset(id);
+    start(la, n0, lane, part, nparts);
+  }
 
   // the next adapters' B, and h of their rows (the other rows' loads go past
   // the extent and move nothing)

@@ -261,8 +261,8 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const uint16_t* __re
 
   if constexpr (sizeof...(LA) > 0) {
     const int part = __builtin_amdgcn_readfirstlane(wave) + WAVES * slice, nparts = WAVES * (int)gridDim.y;
-    LoraSmall<MT, NT, LNS> adapters(la..., row_id, lane);
-    (adapters.start(la, nb, lane, part, nparts), ...);
+    LoraSmall<MT, NT, LNS> adapters;
+    (adapters.begin(la, row_id, nb, lane, part, nparts), ...);
     (adapters.add(acc, la, nb, lane, part, nparts), ...);
   }
 

@@ -28,6 +28,8 @@
 // gridDim.y = SK slices of the K range ("Add Triton BF16xINT4 rowwise GEMM for
 // ROCm gfx942/gfx950", Implementation "Split-K without atomics": fp32 partials
 // to ws[s, :, :] with plain stores; an empty slice writes zeros).
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "lora.hpp"
@@ -172,10 +174,7 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
 
   const int ct = wv & 1;                       // the wave's column tile
   [[maybe_unused]] const int part = (wv >> 1) + 4 * slice, nparts = 4 * (int)gridDim.y;
-  auto adapters = [&] {
-    if constexpr (sizeof...(LA) > 0) return LoraSmall<1, 1, LNS>(la..., row_id, lane);
-    else return 0;
-  }();
+  [[maybe_unused]] typename std::conditional<(sizeof...(LA) > 0), LoraSmall<1, 1, (LNS > 0 ? LNS : 1)>, int>::type adapters;
   f32x4 acc1[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
   f32x4& acc = acc1[0][0];
 
@@ -225,7 +224,7 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
     const bool ahead = j + NS - 1 < nst;
     if (ahead) issue(j + NS - 1, (j + NS - 1) % NS);
     if constexpr (sizeof...(LA) > 0) {
-      if (j == max(0, nst - NS)) (adapters.start(la, n0 + 16 * ct, lane, part, nparts), ...);
+      if (j == max(0, nst - NS)) (adapters.begin(la, row_id, n0 + 16 * ct, lane, part, nparts), ...);
     }
     const uint8_t* sb = lds + (j % NS) * ST::kBytes;
 #pragma unroll
@@ -246,7 +245,7 @@ __global__ __launch_bounds__(64 * kSLWaves) void skinny_lds_kernel(const uint16_
   }
 
   if constexpr (sizeof...(LA) > 0) {
-    if (nst == 0) (adapters.start(la, n0 + 16 * ct, lane, part, nparts), ...);
+    if (nst == 0) (adapters.begin(la, row_id, n0 + 16 * ct, lane, part, nparts), ...);
     (adapters.add(acc1, la, n0 + 16 * ct, lane, part, nparts), ...);
   }
 

@@ -289,8 +289,9 @@ w4a16_status w4a16_splitk_reduce(const float* workspace, uint16_t* y,
  *                 least w4a16_gemm_lora_workspace_bytes, 16-byte aligned.
  * Values of an adapter reach only the rows that name it: an infinity or NaN in
  * another adapter, or in another row, leaves a row as it is. X . A[l]^T is
- * held in fp32 and enters the second product as the sum of two bf16 values
- * (relative error of each element at most 2^-16). No atomics are used: the
+ * summed in fp32 and enters the second product as the sum of two bf16 values
+ * (relative error of each element at most 2^-16; where it is infinite the row
+ * becomes NaN). No atomics are used: the
  * result is bitwise reproducible for a given shape and split_k.
  */
 size_t w4a16_gemm_lora_workspace_bytes(int64_t M, int64_t N, int64_t K,
@@ -337,7 +338,8 @@ w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,
  * expert-ordered arrays of `rows` rows (T * k hold every slot; with fewer, a
  * slot whose position is not below `rows` counts as dropped). Two slots of
  * one call never share a position. The rows that no slot names (those behind
- * the last kept one) are neither read nor written.
+ * the last kept one) are neither read nor written. Written arrays do not
+ * overlap the read ones, except that dz may be z.
  *
  * w4a16_expert_gather: xs[pos[t, j]] = x[t].
  *   x : [T, width] bf16, device;  xs : [rows, width] bf16, device, written
@@ -363,7 +365,6 @@ w4a16_status w4a16_expert_gather_grad(const uint16_t* dxs, const int32_t* pos,
  *   slot).
  *   dy : [T, width] bf16, device;  z, dz : [rows, width] bf16, device (dz
  *   written);  weights, dweights : [T, k] fp32, device (dweights written)
- * Written arrays must not overlap the read ones, except that dz may be z.
  */
 w4a16_status w4a16_expert_combine(const uint16_t* z, const int32_t* pos,
                                   const float* weights, uint16_t* y, int64_t T,

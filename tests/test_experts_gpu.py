@@ -243,6 +243,39 @@ def test_arrays_past_32_bit_offsets():
     assert torch.allclose(dw[-64:, 0], (src[-64:].float() ** 2).sum(1), rtol=1e-4)
 
 
+def test_binding_refuses_what_does_not_fit():
+    x, z, w, pos, dpos = _case(8, 2, 4, 64, "rand", 1)
+    x, z, w = x.to(dev()), z.to(dev()), w.to(dev())
+    for f in (lambda: w4.w4a16_expert_sort(dpos[0], 4), lambda: w4.w4a16_expert_sort(dpos.t(), 4),
+              lambda: w4.w4a16_expert_sort(dpos, 4, order=torch.empty(3, dtype=torch.int32, device=dev())),
+              lambda: w4.w4a16_expert_gather(x[:7], dpos), lambda: w4.w4a16_expert_gather(x, dpos, xs=z[:, :32]),
+              lambda: w4.w4a16_expert_combine(z.t(), dpos), lambda: w4.w4a16_expert_combine(z, dpos, w[:, :1]),
+              lambda: w4.w4a16_expert_combine(z, dpos.cpu()), lambda: w4.w4a16_expert_gather_grad(z[0], dpos),
+              lambda: w4.w4a16_expert_combine_grad(x[:, :32], z, dpos, w)):
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: w4.w4a16_expert_sort(dpos.long(), 4), lambda: w4.w4a16_expert_gather(x.float(), dpos),
+              lambda: w4.w4a16_expert_combine(z, dpos, w.bfloat16()),
+              lambda: w4.w4a16_expert_combine_grad(x, z, dpos, None)):
+        with pytest.raises(TypeError):
+            f()
+    for G in (0, 4097):
+        with pytest.raises((w4.W4A16Error, RuntimeError)):
+            w4.w4a16_expert_sort(dpos, G)
+
+
+@pytest.mark.parametrize("G,T", [(7, 40000), (2000, 3000), (4096, 9000)])
+def test_sort_workspace_is_written_before_it_is_read(G, T):
+    ids = _ids(np.random.default_rng(T), T, 3, G, "holes")
+    need = w4.w4a16_expert_sort_workspace_bytes(T, 3, G)
+    ws = torch.full((need // 4 + 8,), -7, dtype=torch.int32, device=dev())
+    order, pos, sizes = w4.w4a16_expert_sort(torch.from_numpy(ids).to(dev()), G, workspace=ws[:need // 4])
+    ro, rp, rs = sort_ref(ids, G)
+    assert np.array_equal(order.cpu().numpy(), ro) and np.array_equal(pos.cpu().numpy(), rp)
+    assert np.array_equal(sizes.cpu().numpy(), rs)
+    assert (ws[need // 4:] == -7).all()
+
+
 def test_side_stream_and_graph_replays():
     """On a stream of the caller's own, and captured: every replay equals the
     eager result, with eager work between."""

@@ -162,6 +162,59 @@ def test_other_adapters_stay_out(M, N, K, group, R, bad):
         assert torch.equal(got[1:], want[1:]) and not torch.isfinite(got[0]).any()
 
 
+@pytest.mark.parametrize("M,N,K,group,R,sk", [(1, 300, 1024, 128, 16, 0), (1, 300, 1280, 128, 16, 0),
+                                              (5, 300, 1024, 128, 40, 2), (14, 300, 512, 128, 128, 0),
+                                              (40, 300, 512, 128, 128, 0), (100, 8448, 256, 128, 64, 1),
+                                              (300, 300, 512, 32, 16, 4)])
+def test_workspace_is_written_before_it_is_read(M, N, K, group, R, sk):
+    """A workspace full of NaN, of the size asked for, gives the same result."""
+    c = Case(M, N, K, group, R, 4, "holes", seed=M + R)
+    if M == 1:
+        c.d["adapter_ids"].fill_(2)
+    need = w4.w4a16_gemm_lora_workspace_bytes(M, N, K, 4, R, sk, group)
+    ws = torch.full((need // 4 + 16,), float("nan"), device=dev())
+    ws[need // 4:] = 5.0
+    got = c.run(split_k=sk, workspace=ws[:need // 4])
+    assert torch.equal(got, c.run(split_k=sk)) and torch.isfinite(got).all()
+    assert (ws[need // 4:] == 5.0).all()
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    cases = [Case(200, 2048, 1024, 128, 32, 6, "mixed", seed=1), Case(12, 4096, 2048, 128, 16, 12, "each", seed=2)]
+    want = [c.run().clone() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate(cases):
+            got[i].append(c.run(stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in (0, 1) for y in got[i])
+
+
+def test_binding_refuses_what_does_not_fit():
+    c = Case(4, 64, 256, 128, 8, 2, "each", seed=3)
+    d = c.d
+    for kw in (dict(x=d["x"][:, :128]), dict(x=d["x"][0]), dict(w_packed=d["w_packed"][:, :64].contiguous()),
+               dict(scales=d["scales"][:32]), dict(a=d["a"][:1]), dict(a=d["a"][0]), dict(b=d["b"].transpose(1, 2)),
+               dict(adapter_ids=d["adapter_ids"][:3]), dict(scaling=d["scaling"][:1]),
+               dict(y=torch.empty(4, 65, dtype=torch.bfloat16, device=dev())), dict(x=d["x"].cpu()),
+               dict(scaling=d["scaling"].cpu())):
+        with pytest.raises(ValueError):
+            c.run(**kw)
+    for kw in (dict(x=d["x"].half()), dict(adapter_ids=d["adapter_ids"].long()), dict(scaling=d["scaling"].double()),
+               dict(a=None), dict(workspace=torch.zeros(1 << 16, dtype=torch.int32, device=dev()))):
+        with pytest.raises(TypeError):
+            c.run(**kw)
+    with pytest.raises(w4.W4A16Error) as e:
+        c.run(workspace=torch.zeros(4, device=dev()))
+    assert e.value.status == 5
+    with pytest.raises(w4.W4A16Error) as e:
+        c.run(a=d["a"][:, :4].contiguous(), b=d["b"][:, :, :4].contiguous())    # rank 4
+    assert e.value.status == 2
+
+
 def test_no_rows():
     c = Case(4, 64, 128, 128, 8, 2, "each", seed=1)
     y = c.run(x=c.d["x"][:0], adapter_ids=c.d["adapter_ids"][:0])

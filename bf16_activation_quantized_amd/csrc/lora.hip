@@ -211,6 +211,14 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* __restrict__ x, cons
     fetch(t1);
   }
   red[wv][lane] = acc;
+  // the lane's rows' scales, with every lane active (a lane of a rank past R
+  // may hold the id)
+  float sc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int l = __shfl(id, 4 * kb + i);
+    sc[i] = scaling != nullptr && l >= 0 ? scaling[l] : 1.0f;
+  }
   __syncthreads();
   if (wv == 0 && r0 + m16 < R) {
     f32x4 v = red[0][lane];
@@ -226,9 +234,8 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* __restrict__ x, cons
     const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = 4 * kb + i, l = __shfl(id, r);
-      if ((own >> r) & 1)
-        store_h(h, (size_t)M * R, (size_t)(m0 + r) * R + r0 + m16, scaling != nullptr ? scaling[l] * f[i] : f[i]);
+      const int r = 4 * kb + i;
+      if ((own >> r) & 1) store_h(h, (size_t)M * R, (size_t)(m0 + r) * R + r0 + m16, sc[i] * f[i]);
     }
   }
 }

@@ -117,6 +117,19 @@ def test_parity(M, N, K, group, R, L, kind, sk):
     assert torch.equal(first, c.run(split_k=sk))        # bitwise repeatable
 
 
+@pytest.mark.parametrize("M,group", [(1, 128), (6, 128), (14, 128), (30, 128), (45, 128), (333, 128), (333, 32),
+                                     (2000, 128)])
+@pytest.mark.parametrize("R", [8, 24, 40, 72, 88, 104, 120, 128])
+@pytest.mark.parametrize("kind", ["mixed", "runs", "holes"])
+def test_each_row_takes_its_own_scale(M, group, R, kind):
+    """Scales that differ by adapter, at every kind of rank (the last rank tile
+    full or half) and of row order."""
+    c = Case(M, 96, 256, group, R, 5, kind, seed=M + R)
+    c.sc = torch.tensor([1.0, -2.0, 4.0, 0.5, 8.0])
+    ref, bound = c.ref()
+    within(f64(c.run(scaling=c.sc.to(dev()))), ref, bound, f"scales {M} r{R}")
+
+
 @pytest.mark.parametrize("M,N,K,group,sk", [(1, 512, 1024, 128, 0), (4, 512, 1024, 128, 0), (12, 512, 1024, 128, 2),
                                             (40, 512, 512, 128, 0), (100, 8448, 256, 128, 0), (100, 512, 256, 32, 2)])
 def test_rows_without_adapter_equal_the_projection(M, N, K, group, sk):

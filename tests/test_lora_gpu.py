@@ -77,6 +77,12 @@ CASES = [
     (13, 1030, 2560, 128, 56, 4, "holes", 2),
     (16, 2048, 4096, 128, 16, 16, "each", 0),
     (16, 96, 8192, 128, 128, 20, "holes", 8),
+    (10, 100, 128, 128, 32, 3, "each", 0),       # 1, 3, 4, 5 and 12 stages of the LDS-staged kernel
+    (11, 70, 1536, 128, 64, 11, "each", 0),
+    (12, 1000, 2048, 128, 128, 4, "mixed", 1),
+    (15, 130, 2560, 128, 96, 15, "each", 1),
+    (16, 200, 6144, 128, 40, 7, "holes", 1),
+    (16, 64, 1024, 128, 16, 16, "each", 16),     # more slices than groups
     (17, 640, 1024, 128, 16, 3, "runs", 0),
     (31, 1025, 896, 128, 48, 31, "each", 2),
     (33, 512, 1280, 128, 16, 4, "holes", 0),

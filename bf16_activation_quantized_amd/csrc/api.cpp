@@ -518,7 +518,7 @@ bool expert_slots_ok(int64_t T, int32_t k) { return T >= 0 && k >= 1 && T <= kMa
 
 uint64_t expert_sort_bytes(int64_t T, int32_t k, int32_t G) {
   const int blocks = w4a16::expert_sort_blocks(T * k, G);
-  return blocks > 1 ? round_up((uint64_t)blocks * (uint64_t)(G + 1) * 4u, 256) : 0u;
+  return blocks > 1 ? round_up((uint64_t)(blocks + 1) * (uint64_t)(G + 1) * 4u, 256) : 0u;
 }
 
 // Checks of the calls on rows; *empty: nothing to enqueue.

@@ -67,11 +67,9 @@ __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float c) {
 
 constexpr int kBatch = 4;   // slots of a token whose rows are in flight together
 
-// Sort: a block of 16 waves (fewer where G needs the LDS) takes tiles of 256
-// slots per wave in turn.
-constexpr int kSortPer = 4;                 // slots per lane and tile
+// Sort: a block of W waves takes tiles of PER slots per lane in turn.
 constexpr int kSortMaxBlocks = 256;
-constexpr int kSortSingle = 8192;           // slots that one block takes alone
+constexpr int kSortSingle = 2048;           // slots that one block takes alone
 
 __device__ __forceinline__ int bin_of(int e, int G) {
   return (uint32_t)e < (uint32_t)G ? e : G;   // bin G: dropped
@@ -90,17 +88,18 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
 // Counts the bins of slots [lo, hi) into cnt (LDS, zeroed). The lanes that
 // share the first lane's bin are counted at once (a popular expert would
 // otherwise be up to 64 additions to one address), the others one by one.
+template <int PER>
 __device__ __forceinline__ void count_bins(int32_t* cnt, const int32_t* ids, int64_t lo, int64_t hi, int G, int tid,
                                            int nthr) {
-  for (int64_t s0 = lo; s0 < hi; s0 += kSortPer * nthr) {
-    int e[kSortPer];
+  for (int64_t s0 = lo; s0 < hi; s0 += PER * nthr) {
+    int e[PER];
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int64_t s = s0 + (int64_t)i * nthr + tid;
       e[i] = s < hi ? bin_of(ids[s], G) : -1;
     }
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const uint64_t live = __ballot(e[i] >= 0);
       if (live == 0) continue;
       const int first = __builtin_ctzll(live);
@@ -116,7 +115,7 @@ __device__ __forceinline__ void count_bins(int32_t* cnt, const int32_t* ids, int
 // ---------------------------------------------------------------- sort
 // Pass 1 (more than one block): block b counts the bins of its slots,
 // hist[b][0 .. G].
-template <int W>
+template <int W, int PER>
 __global__ __launch_bounds__(64 * W) void expert_hist_kernel(const int32_t* __restrict__ ids,
                                                              int32_t* __restrict__ hist, int64_t S, int G,
                                                              int64_t chunk) {
@@ -124,9 +123,38 @@ __global__ __launch_bounds__(64 * W) void expert_hist_kernel(const int32_t* __re
   for (int g = threadIdx.x; g <= G; g += 64 * W) cnt[g] = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * chunk, hi = lo + chunk < S ? lo + chunk : S;
-  count_bins(cnt, ids, lo, hi, G, threadIdx.x, 64 * W);
+  count_bins<PER>(cnt, ids, lo, hi, G, threadIdx.x, 64 * W);
   __syncthreads();
   for (int g = threadIdx.x; g <= G; g += 64 * W) hist[(int64_t)blockIdx.x * (G + 1) + g] = cnt[g];
+}
+
+// Between them, where the blocks' counts are many: each becomes the sum of the
+// blocks before it, and row `blocks` the sum of all. A workgroup takes 64 bins,
+// its 16 waves consecutive runs of blocks.
+__global__ __launch_bounds__(1024) void expert_prefix_kernel(int32_t* __restrict__ hist, int nb, int blocks) {
+  __shared__ int32_t sum[16][64];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int g = 64 * (int)blockIdx.x + lane;
+  constexpr int kRun = kSortMaxBlocks / 16;
+  const int run = (blocks + 15) / 16;   // <= kRun
+  const int b0 = wv * run, b1 = min(blocks, b0 + run);
+  int v[kRun], mine = 0;
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) {
+    v[u] = g < nb && b0 + u < b1 ? hist[(b0 + u) * nb + g] : 0;
+  }
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) mine += v[u];
+  sum[wv][lane] = mine;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < wv; ++w) at += sum[w][lane];
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) {
+    if (g < nb && b0 + u < b1) hist[(b0 + u) * nb + g] = at;
+    at += v[u];
+  }
+  if (wv == 15 && g < nb) hist[blocks * nb + g] = at;
 }
 
 // Pass 2: the start of each bin for the block's slots (all bins before it,
@@ -135,10 +163,11 @@ __global__ __launch_bounds__(64 * W) void expert_hist_kernel(const int32_t* __re
 // bin bit; the last of them moves the wave's count of the bin on), the waves'
 // counts become their starts, and every slot is written. Slots keep their
 // order within a bin: the sort is stable, and exact whatever the scheduling.
-template <int W>
+template <int W, int PER>
 __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
     const int32_t* __restrict__ ids, const int32_t* __restrict__ hist, int32_t* __restrict__ order,
-    int32_t* __restrict__ pos, int32_t* __restrict__ m_sizes, int64_t S, int G, int64_t chunk, int blocks, int bits) {
+    int32_t* __restrict__ pos, int32_t* __restrict__ m_sizes, int64_t S, int G, int64_t chunk, int blocks, int bits,
+    bool summed) {
   constexpr int NTHR = 64 * W;
   extern __shared__ __attribute__((aligned(16))) int32_t lds[];
   const int nb = G + 1;
@@ -154,24 +183,31 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
   for (int g = tid; g < 2 * nb; g += NTHR) lds[g] = 0;
   __syncthreads();
   if (blocks == 1) {
-    count_bins(total, ids, lo, hi, G, tid, NTHR);
+    count_bins<PER>(total, ids, lo, hi, G, tid, NTHR);
+  } else if (summed) {
+    for (int g = tid; g < nb; g += NTHR) {
+      total[g] = hist[blocks * nb + g];
+      at[g] = hist[(int)blockIdx.x * nb + g];
+    }
   } else {
-    const int me = (int)blockIdx.x * nb, all = blocks * nb;   // blocks <= 256, nb <= 4097
-    const int step = NTHR % nb;
-    int g = tid % nb;
-    for (int i0 = tid; i0 < all; i0 += 8 * NTHR) {
-      int v[8];
+    // thread (q, g): bin g of every parts-th block, 16 blocks in flight (a
+    // thread takes bins in turn where there are more of them than threads)
+    const int parts = nb < NTHR ? NTHR / nb : 1;
+    const int q = nb < NTHR ? tid / nb : 0;
+    for (int g = tid - q * nb; g < nb && q < parts; g += NTHR) {
+      int all = 0, before = 0;
+      for (int b0 = q; b0 < blocks; b0 += 16 * parts) {   // blocks <= 256, nb <= 4097
+        int v[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = i0 + u * NTHR < all ? hist[i0 + u * NTHR] : 0;
+        for (int u = 0; u < 16; ++u) v[u] = b0 + u * parts < blocks ? hist[(b0 + u * parts) * nb + g] : 0;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (v[u] != 0) {
-          atomicAdd(&total[g], v[u]);
-          if (i0 + u * NTHR < me) atomicAdd(&at[g], v[u]);
+        for (int u = 0; u < 16; ++u) {
+          all += v[u];
+          before += b0 + u * parts < (int)blockIdx.x ? v[u] : 0;
         }
-        g += step;
-        g = g >= nb ? g - nb : g;
       }
+      atomicAdd(&total[g], all);
+      atomicAdd(&at[g], before);
     }
   }
   __syncthreads();
@@ -194,16 +230,16 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
   }
 
   int32_t* r = run + wv * nb;
-  for (int64_t t0 = lo; t0 < hi; t0 += kSortPer * NTHR) {
-    const int64_t s0 = t0 + (int64_t)wv * (64 * kSortPer) + lane;
-    int e[kSortPer], rank[kSortPer];
+  for (int64_t t0 = lo; t0 < hi; t0 += PER * NTHR) {
+    const int64_t s0 = t0 + (int64_t)wv * (64 * PER) + lane;
+    int e[PER], rank[PER];
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) e[i] = s0 + 64 * i < hi ? bin_of(ids[s0 + 64 * i], G) : -1;
+    for (int i = 0; i < PER; ++i) e[i] = s0 + 64 * i < hi ? bin_of(ids[s0 + 64 * i], G) : -1;
     __syncthreads();   // the tile before (or the totals) is done with the counts
     for (int i = tid; i < W * nb; i += NTHR) run[i] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       uint64_t same = __ballot(e[i] >= 0);
       if (same == 0) break;   // the waves past the last slot
       for (int b = 0; b < bits; ++b) {
@@ -247,7 +283,7 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       if (e[i] >= 0) {
         const int p = r[e[i]] + rank[i];
         const int s = (int)(s0 + 64 * i);
@@ -259,11 +295,11 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
     if (blocks > 1) {
       // order goes through LDS in bin order, so that a bin's slots of the tile
       // leave as one run (65536 x 8 slots, 128 experts: 12.1 -> 11.1 us for
-      // this kernel; one block's few slots are 0.7 us faster without)
+      // this kernel in tiles of 4096; one block's few slots are 0.7 us faster without)
       __syncthreads();
-      const int n = hi - t0 < kSortPer * NTHR ? (int)(hi - t0) : kSortPer * NTHR;
+      const int n = hi - t0 < PER * NTHR ? (int)(hi - t0) : PER * NTHR;
 #pragma unroll
-      for (int i = 0; i < kSortPer; ++i) {
+      for (int i = 0; i < PER; ++i) {
         const int q = i * NTHR + tid;
         if (q < n) order[place[q].x] = place[q].y;
       }
@@ -452,42 +488,57 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t
 }
 
 // ---------------------------------------------------------------- launchers
-// One block up to kSortSingle slots (one launch), else whole tiles per block,
-// at most kSortMaxBlocks blocks (each reads all blocks' counts).
-// waves of a block: what G leaves of the LDS
-static int sort_waves(int G) { return G <= 1024 ? 16 : G <= 2048 ? 8 : 4; }
-static int64_t sort_chunk(int64_t S, int G) {
-  const int64_t tile = 64 * kSortPer * sort_waves(G);
-  if (S <= kSortSingle) return kSortSingle;
-  const int64_t tiles = (S + tile - 1) / tile;
-  return (tiles + kSortMaxBlocks - 1) / kSortMaxBlocks * tile;
+// Shape of a sort: one block up to kSortSingle slots (one launch), else whole
+// tiles per block, at most kSortMaxBlocks blocks. Smaller tiles spread fewer
+// slots over more blocks, larger ones keep the blocks' counts few (pairs of
+// waves and slots per lane, us, 128 experts: 32768 slots 8.3 with 8 x 2, 9.6
+// with 16 x 2, 11.7 with 16 x 4; 524288 slots 15.1, 13.3, 13.8; 2097152 slots
+// 26.7, 29.1, 23.3); past 1024 bins the waves' counts take the LDS.
+struct SortShape {
+  int waves, per, blocks;
+  int64_t chunk;   // slots of a block
+};
+static SortShape sort_shape(int64_t S, int G) {
+  SortShape h;
+  h.waves = G > 2048 ? 4 : G > 1024 || S <= (1 << 17) ? 8 : 16;
+  h.per = G > 2048 ? 8 : G > 1024 || S > (1 << 19) ? 4 : 2;
+  const int64_t tile = 64 * h.per * h.waves, tiles = (S + tile - 1) / tile;
+  h.chunk = S <= kSortSingle ? kSortSingle : (tiles + kSortMaxBlocks - 1) / kSortMaxBlocks * tile;
+  h.blocks = (int)((S + h.chunk - 1) / h.chunk);
+  return h;
 }
-int expert_sort_blocks(int64_t S, int G) {
-  const int64_t c = sort_chunk(S, G);
-  return (int)((S + c - 1) / c);
-}
+int expert_sort_blocks(int64_t S, int G) { return sort_shape(S, G).blocks; }
 
-template <int W>
+template <int W, int PER>
 static hipError_t launch_sort_w(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t S, int G,
-                                int32_t* ws, hipStream_t stream) {
-  const int64_t chunk = sort_chunk(S, G);
-  const int blocks = expert_sort_blocks(S, G);
+                                int32_t* ws, const SortShape& h, hipStream_t stream) {
+  const int64_t chunk = h.chunk;
+  const int blocks = h.blocks;
   int bits = 1;
   while ((1 << bits) <= G) ++bits;
   const int lds1 = (G + 1) * 4;
   // starts, waves' counts, shifts; then the tile's (row, slot) pairs
-  const int lds2 = ((G + 1) * (2 + W) + 1) / 2 * 8 + 64 * W * kSortPer * 8;
+  const int lds2 = ((G + 1) * (2 + W) + 1) / 2 * 8 + 64 * W * PER * 8;
   static std::atomic<uint64_t> set{0};
-  const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&expert_scatter_kernel<W>),
+  const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&expert_scatter_kernel<W, PER>),
                                        160 * 1024 - 512, set);
   if (ea != hipSuccess) return ea;
+  // Up to 48 counts per thread every block adds the others' up itself; past
+  // that a third launch does (524288 slots: 128 experts 13.3 us without it, 14.7
+  // with it; 256 experts 18.0 and 15.7; 1024 experts 40 and 20).
+  const bool summed = blocks > 1 && blocks * (G + 1) > 48 * 64 * W;
   if (blocks > 1) {
-    hipLaunchKernelGGL(expert_hist_kernel<W>, dim3(blocks), dim3(64 * W), lds1, stream, ids, ws, S, G, chunk);
+    hipLaunchKernelGGL((expert_hist_kernel<W, PER>), dim3(blocks), dim3(64 * W), lds1, stream, ids, ws, S, G, chunk);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(expert_scatter_kernel<W>, dim3(blocks), dim3(64 * W), lds2, stream, ids, ws, order, pos, m_sizes,
-                     S, G, chunk, blocks, bits);
+  if (summed) {
+    hipLaunchKernelGGL(expert_prefix_kernel, dim3((G + 64) / 64), dim3(1024), 0, stream, ws, G + 1, blocks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((expert_scatter_kernel<W, PER>), dim3(blocks), dim3(64 * W), lds2, stream, ids, ws, order, pos,
+                     m_sizes, S, G, chunk, blocks, bits, summed);
   return hipGetLastError();
 }
 
@@ -497,11 +548,12 @@ hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, 
     hipLaunchKernelGGL(expert_zero_kernel, dim3(1), dim3(256), 0, stream, m_sizes, G);
     return hipGetLastError();
   }
-  switch (sort_waves(G)) {
-    case 16: return launch_sort_w<16>(ids, order, pos, m_sizes, S, G, ws, stream);
-    case 8: return launch_sort_w<8>(ids, order, pos, m_sizes, S, G, ws, stream);
-    default: return launch_sort_w<4>(ids, order, pos, m_sizes, S, G, ws, stream);
-  }
+  const SortShape h = sort_shape(S, G);
+  if (h.waves == 4) return launch_sort_w<4, 8>(ids, order, pos, m_sizes, S, G, ws, h, stream);
+  if (h.waves == 8 && h.per == 4) return launch_sort_w<8, 4>(ids, order, pos, m_sizes, S, G, ws, h, stream);
+  if (h.waves == 8) return launch_sort_w<8, 2>(ids, order, pos, m_sizes, S, G, ws, h, stream);
+  if (h.per == 2) return launch_sort_w<16, 2>(ids, order, pos, m_sizes, S, G, ws, h, stream);
+  return launch_sort_w<16, 4>(ids, order, pos, m_sizes, S, G, ws, h, stream);
 }
 
 // The variant by the rows: threads per token, the power of two that holds the

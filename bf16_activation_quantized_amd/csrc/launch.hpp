@@ -64,8 +64,8 @@ hipError_t launch_rowsum_neg136(const uint16_t* x, float* out, int M, int K, int
 // (m_sizes == nullptr, m_uniform == 0, G == 1), grouped (rows per weight group
 // in m_sizes on the device) or batched (G weight groups of m_uniform rows
 // each). With ws != nullptr (plain and batched) slice s of gridDim.y = sk
-// writes fp32 partials ws[s, :, :]. la (plain): per-row adapters, added in
-// slice 0. sxn: the -136 * row sums [K/gsize, ld] of
+// writes fp32 partials ws[s, :, :]. la (plain): per-row adapters, dealt
+// out over the slices. sxn: the -136 * row sums [K/gsize, ld] of
 // launch_rowsum_neg136, or nullptr for the kernel to form them itself.
 hipError_t launch_tile(const uint16_t* x, const uint8_t* w, const uint16_t* s, const float* sxn, int ld, uint16_t* y,
                        float* ws, const int32_t* m_sizes, int m_uniform, int M_total, int N, int K, int G, int gps,
@@ -83,7 +83,7 @@ hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_
 
 // ---- rows of a mixture of experts (experts.hip)
 constexpr int kExpertMaxGroups = 4096;
-int expert_sort_blocks(int64_t S, int G);   // past one, each has a row of G + 1 counts of workspace
+int expert_sort_blocks(int64_t S, int G);   // past one: a row of G + 1 counts of workspace for each, and one more
 hipError_t launch_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* m_sizes, int64_t S, int G,
                               int32_t* ws, hipStream_t stream);
 hipError_t launch_expert_gather(const uint16_t* x, const int32_t* pos, uint16_t* xs, int64_t T, int k, int64_t rows,

@@ -281,10 +281,10 @@ w4a16_status w4a16_splitk_reduce(const float* workspace, uint16_t* y,
  *                 any value outside [0, L) means none.
  *   scaling     : [L] fp32, device, 4-byte aligned, or NULL (all 1)
  *   L >= 1; R a multiple of 8, 8 <= R <= 128 (pad an adapter of another rank
- *   with zeros: W4A16_ERR_SHAPE otherwise); N * R * 2 and M * R * 4 < 2^32
- *   bytes. a and b may be larger than 2^32 bytes. Adapters of the parts of a fused projection
- *   (gate and up, or q, k and v) are one adapter of the ranks' sum, with zeros
- *   in B outside each part's columns.
+ *   with zeros: W4A16_ERR_SHAPE otherwise); N * R * 2, K * R * 2 and M * R * 4
+ *   < 2^32 bytes. a and b may be larger than 2^32 bytes. Adapters of the parts
+ *   of a fused projection (gate and up, or q, k and v) are one adapter of the
+ *   ranks' sum, with zeros in B outside each part's columns.
  *   workspace   : fp32 device scratch, overwritten, never NULL when M > 0: at
  *                 least w4a16_gemm_lora_workspace_bytes, 16-byte aligned.
  * Values of an adapter reach only the rows that name it: an infinity or NaN in
@@ -325,7 +325,7 @@ w4a16_status w4a16_gemm_lora(const uint16_t* x, const uint8_t* w_packed,
  *             w4a16_gemm_grouped); all zero when T == 0
  *   workspace: device scratch, overwritten, 16-byte aligned, at least
  *             w4a16_expert_sort_workspace_bytes (0, and NULL allowed, up to
- *             8192 slots, which take one kernel; 0 on invalid arguments).
+ *             2048 slots, which take one kernel; 0 on invalid arguments).
  */
 size_t w4a16_expert_sort_workspace_bytes(int64_t T, int32_t k, int32_t G);
 w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,

@@ -43,6 +43,11 @@ SORT_CASES = [
     (40000, 8, 128, "skew"), (33333, 7, 255, "holes"), (300000, 1, 16, "one"), (270001, 2, 1000, "rand"),
     (20000, 8, 4096, "holes"), (8192, 1, 2047, "rand"), (8193, 1, 2048, "holes"), (4096, 2, 4096, "one"),
     (1100000, 2, 60, "skew"), (700001, 3, 4095, "holes"),
+    # each shape of the sort, on both sides of its borders, with few and many counts
+    (2048, 1, 2048, "rand"), (2049, 1, 2049, "holes"), (683, 3, 5, "skew"), (131072, 1, 190, "holes"),
+    (131072, 1, 191, "holes"), (131073, 1, 300, "rand"), (65536, 8, 190, "skew"), (65536, 8, 192, "holes"),
+    (174763, 3, 1024, "holes"), (524289, 1, 383, "rand"), (524289, 1, 50, "holes"), (40961, 1, 1025, "holes"),
+    (9000, 1, 1200, "rand"),
 ]
 
 

@@ -92,9 +92,9 @@ def test_sort_refusals(lib, kw, want):
 def test_sort_workspace(lib):
     f = w4.w4a16_expert_sort_workspace_bytes
     assert f(0, 2, 8) == 0 and f(4, 0, 8) == 0 and f(4, 2, 0) == 0 and f(4, 2, 4097) == 0 and f(1 << 30, 2, 8) == 0
-    for T, k, G in ((1, 1, 1), (16, 4, 8), (8192, 1, 4096)):   # one kernel
+    for T, k, G in ((1, 1, 1), (16, 4, 8), (2048, 1, 4096), (256, 8, 128)):   # one kernel
         assert f(T, k, G) == 0
-    for T, k, G in ((8193, 1, 1), (65536, 8, 128), (1 << 20, 8, 4096), (1 << 28, 7, 300)):
+    for T, k, G in ((2049, 1, 1), (8193, 1, 2048), (65536, 8, 128), (1 << 20, 8, 4096), (1 << 28, 7, 300)):
         assert 0 < f(T, k, G) < 1 << 30
         assert sort(lib, T=T, k=k, G=G, wsb=f(T, k, G) - 1) == ERR_WS
 

@@ -8,6 +8,8 @@
 // once and rounded once. There h enters the matrix core as two bf16 values
 // (its rounding and the rounding of what is left: 16 of its bits). Rows whose id is outside [0, L) get the
 // projection alone.
+#include <algorithm>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "lora.hpp"
@@ -98,86 +100,56 @@ __device__ __forceinline__ void shrink_row(const uint16_t* __restrict__ x, const
 }
 
 // ---------------------------------------------------------------- many rows
-// Workgroup (turn, row tile of 16, rank tile of 16): MFMA 16x16x32 over the
-// whole K range, for every turns-th adapter of the row tile in the order
-// of their first row (one, where the rows of a request lie together). The 8
-// waves take the 128-k groups in turn; a group of x (only the rows of the
-// turn's adapters) and of A is fetched in whole lines (4 rows x 256 bytes per
-// instruction) and turned into fragments through the wave's own LDS tile, two
-// fetches ahead. x stays in registers while the turn's adapters follow one
-// another, and each product is added to the rows of its adapter only (one
-// accumulator: a row has one adapter). The waves are summed through LDS in
-// wave order.
+// Workgroup (turn, block of 64 rows, rank tile of 16): MFMA 16x16x32 over the
+// whole K range, for every turns-th unit of the block. A unit is up to 16 rows
+// of one adapter, wherever they lie in the block, in the order of their first
+// rows; so the rows of a request, one after another, are units of 16, and A is
+// read once per block for an adapter whose rows are strewn over it (against
+// 16-row tiles, this kernel: 2048 x 5120 x 5120, rank 64, 16 adapters mixed 54
+// -> 45 us, 512 x 8192 x 8192, rank 64, 8 mixed 26.5 -> 14.7; one after the
+// other 12.2 -> 9.6). Bound by its round trips where units are few (1322 rows,
+// rank 64, with the row sums: 9.8 us), by reading x and A again from the
+// caches where they are many (11 TB/s at 4096 rows, rank 128). The 8 waves take the 128-k groups in turn; a group of x
+// and of A is fetched in whole lines (4 rows x 256 bytes per instruction) and
+// turned into fragments through the wave's own LDS tile, two fetches ahead.
+// The waves are summed through LDS in wave order.
 constexpr int kTileWaves = kWaves;
+constexpr int kUnitBlock = 64;   // rows: one per lane
 
 __device__ __forceinline__ void shrink_tile(const uint16_t* __restrict__ x, const uint16_t* __restrict__ a,
                                             const int32_t* __restrict__ ids, const float* __restrict__ scaling,
                                             uint16_t* __restrict__ h, int M, int K, int L, int R, int block,
-                                            int turns) {
+                                            int turns, int bits) {
   __shared__ u32x4 tile[kTileWaves][16 * 16];   // [row][piece p of a group in slot p ^ row]
-  __shared__ f32x4 red[kTileWaves][64];
+  __shared__ f32x4 red[2][kTileWaves][64];
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m16 = lane & 15, kb = lane >> 4;
-  const int rt = (R + 15) / 16, mt = (M + 15) / 16;
-  const int r0 = block % rt * 16, m0 = block / rt % mt * 16, me = block / rt / mt;
+  const int rt = (R + 15) / 16, mt = (M + kUnitBlock - 1) / kUnitBlock;
+  // the rank tiles of a unit follow one another on one XCD (workgroups go
+  // round the 8 of them), whose L2 then holds its rows of x
+  const int at = block / (8 * rt) * 8 + block % 8;
+  const int r0 = block % (8 * rt) / 8 * 16, m0 = at % mt * kUnitBlock, me = at / mt;
+  if (me >= turns) return;   // the grid's last workgroups
   const int Gk = K / kGroup;
   const uint32_t KB = (uint32_t)K * 2u;
-  int id = m0 + m16 < M ? ids[m0 + m16] : -1;
+  int id = m0 + lane < M ? ids[m0 + lane] : -1;
   id = (uint32_t)id < (uint32_t)L ? id : -1;
 
-  // this turn's adapters (bits: the first row of each) and their rows
-  uint32_t lead = 0, own = 0;
-  {
-    uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xFFFFu;
-    for (int turn = 0; todo != 0; turn = turn + 1 == turns ? 0 : turn + 1) {
-      const int first = __builtin_ctz(todo);
-      const uint32_t rows = (uint32_t)__ballot(id == __builtin_amdgcn_readlane(id, first)) & 0xFFFFu;
-      if (turn == me) {
-        lead |= 1u << first;
-        own |= rows;
-      }
-      todo &= ~rows;
-    }
+  // the rows of the lane's adapter, the lane's place among them, and the units' first rows
+  uint64_t same = __ballot(id >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (id >> b) & 1;
+    const uint64_t v = __ballot(one);
+    same &= one ? v : ~v;
   }
-  if (lead == 0) return;   // the same in every wave
+  const int place = (int)__popcll(same & ((1ull << lane) - 1));
+  uint64_t todo = __ballot(id >= 0 && place % 16 == 0);
+  for (int i = 0; i < me; ++i) todo &= todo - 1;   // (0 stays 0)
 
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(x + (size_t)m0 * K, (uint32_t)min(16, M - m0) * KB);
-  // row 4 j + kb, 16-byte piece m16 of a group
-  const uint32_t off = (uint32_t)kb * KB + 16u * (uint32_t)m16;
-  uint32_t xo[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) xo[j] = (own >> (4 * j + kb)) & 1 ? off + (uint32_t)(4 * j) * KB : kOutside;
-  struct Item {
-    u32x4 xv[4], av[4];
-    uint32_t rows;
-    bool fresh, live;
-  };
-  // the sequence of (group, adapter) of this wave
-  uint32_t todo = lead;
-  int g = wv;
-  auto fetch = [&](Item& t) {
-    t.live = g < Gk;
-    if (!t.live) return;
-    t.fresh = todo == lead;
-    const int first = __builtin_ctz(todo);
-    const int l = __builtin_amdgcn_readlane(id, first);
-    t.rows = (uint32_t)__ballot(id == l) & 0xFFFFu;
-    const __amdgpu_buffer_rsrc_t ra =   // ranks past R read zeros
-        make_rsrc(a + ((size_t)l * R + r0) * K, (uint32_t)min(16, R - r0) * KB);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) t.av[j] = ld128(ra, off + (uint32_t)(4 * j) * KB + (uint32_t)g * 256u);
-    if (t.fresh) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) t.xv[j] = ld128(rx, __builtin_elementwise_add_sat(xo[j], (uint32_t)g * 256u));
-    }
-    todo &= todo - 1;
-    if (todo == 0) {
-      todo = lead;
-      g += kTileWaves;
-    }
-    __builtin_amdgcn_sched_barrier(0);   // one fetch's loads stay together
-  };
+  const __amdgpu_buffer_rsrc_t rx =
+      make_rsrc(x + (size_t)m0 * K, (uint32_t)min(kUnitBlock, M - m0) * KB);
+  const uint32_t piece = 16u * (uint32_t)m16;   // of a group
   u32x4* tw = tile[wv];
   // lane (m16, kb) of step j: row m16, piece 4 kb + j (k = 32 kb + 8 j + 0..7, the same in both operands)
   auto turned = [&](const u32x4 (&v)[4], u32x4 (&f)[4]) {
@@ -188,55 +160,75 @@ __device__ __forceinline__ void shrink_tile(const uint16_t* __restrict__ x, cons
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = tw[16 * m16 + ((4 * kb + j) ^ m16)];
   };
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  u32x4 xf[4];
-  auto use = [&](const Item& t) {
-    u32x4 af[4];
-    if (t.fresh) turned(t.xv, xf);
-    turned(t.av, af);
-    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+
+  for (int parity = 0; todo != 0; parity ^= 1) {   // the same in every wave
+    const int first = __builtin_ctzll(todo);
+    const int l = __builtin_amdgcn_readlane(id, first);
+    const int from = __builtin_amdgcn_readlane(place, first);
+    const bool own = id == l && place >= from && place < from + 16;
+    const int count = (int)__popcll(__ballot(own));
+    // lane i < count: the unit's row i (the others are sent to lanes past the 16th)
+    const int row = __builtin_amdgcn_ds_permute(4 * (own ? place - from : 16 + (lane & 31)), lane);
+    // row (rank) 4 j + kb, 16-byte piece m16 of a group; zeros past the unit's rows and past R
+    uint32_t xo[4], ao[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xf[j]), frag(af[j]), d, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += (t.rows >> (4 * kb + i)) & 1 ? d[i] : 0.0f;
-  };
-  Item t0, t1;
-  fetch(t0);
-  fetch(t1);
-  while (t0.live) {
-    use(t0);
-    fetch(t0);
-    if (!t1.live) break;
-    use(t1);
-    fetch(t1);
-  }
-  red[wv][lane] = acc;
-  // the lane's rows' scales, with every lane active (a lane of a rank past R
-  // may hold the id)
-  float sc[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int l = __shfl(id, 4 * kb + i);
-    sc[i] = scaling != nullptr && l >= 0 ? scaling[l] : 1.0f;
-  }
-  __syncthreads();
-  if (wv == 0 && r0 + m16 < R) {
-    f32x4 v = red[0][lane];
-#pragma unroll
-    for (int q = 1; q < kTileWaves; ++q) {
-      const f32x4 p = red[q][lane];
-      v.x += p.x;
-      v.y += p.y;
-      v.z += p.z;
-      v.w += p.w;
+    for (int j = 0; j < 4; ++j) {
+      const int r = __shfl(row, 4 * j + kb);
+      xo[j] = 4 * j + kb < count ? (uint32_t)r * KB + piece : kOutside;
+      ao[j] = r0 + 4 * j + kb < R ? (uint32_t)(4 * j + kb) * KB + piece : kOutside;
     }
-    // lane: rows 4 kb + i, rank r0 + m16
-    const float f[4] = {v.x, v.y, v.z, v.w};
+    const __amdgpu_buffer_rsrc_t ra = make_rsrc(a + ((size_t)l * R + r0) * K, (uint32_t)min(16, R - r0) * KB);
+    struct Item {
+      u32x4 xv[4], av[4];
+    };
+    auto fetch = [&](Item& t, int g) {
+      const uint32_t o = g < Gk ? (uint32_t)g * 256u : kOutside;   // past K: zeros
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * kb + i;
-      if ((own >> r) & 1) store_h(h, (size_t)M * R, (size_t)(m0 + r) * R + r0 + m16, sc[i] * f[i]);
+      for (int j = 0; j < 4; ++j) t.av[j] = ld128(ra, __builtin_elementwise_add_sat(ao[j], o));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t.xv[j] = ld128(rx, __builtin_elementwise_add_sat(xo[j], o));
+      __builtin_amdgcn_sched_barrier(0);   // one fetch's loads stay together
+    };
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    auto use = [&](const Item& t) {
+      u32x4 xf[4], af[4];
+      turned(t.xv, xf);
+      turned(t.av, af);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(xf[j]), frag(af[j]), acc, 0, 0, 0);
+    };
+    Item t0, t1;
+    fetch(t0, wv);
+    fetch(t1, wv + kTileWaves);
+    for (int g = wv; g < Gk; g += 2 * kTileWaves) {
+      use(t0);
+      fetch(t0, g + 2 * kTileWaves);
+      use(t1);
+      fetch(t1, g + 3 * kTileWaves);
     }
+    red[parity][wv][lane] = acc;
+    __syncthreads();   // (the other half is written while wave 0 reads this one)
+    if (wv == 0) {
+      f32x4 v = red[parity][0][lane];
+#pragma unroll
+      for (int q = 1; q < kTileWaves; ++q) {
+        const f32x4 p = red[parity][q][lane];
+        v.x += p.x;
+        v.y += p.y;
+        v.z += p.z;
+        v.w += p.w;
+      }
+      const float sc = scaling != nullptr ? scaling[l] : 1.0f;
+      // lane: rows 4 kb + i, rank r0 + m16 (every lane is active where their places are read)
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + __shfl(row, 4 * kb + i);
+        if (4 * kb + i < count && r0 + m16 < R) store_h(h, (size_t)M * R, (size_t)m * R + r0 + m16, sc * f[i]);
+      }
+    }
+    for (int i = 0; i < turns; ++i) todo &= todo - 1;
   }
 }
 
@@ -251,7 +243,7 @@ struct ShrinkArgs {
   const float* scaling;
   uint16_t* h;
   float* rowsums;
-  int M, K, L, R, ld, rowsum_blocks, turns;
+  int M, K, L, R, ld, rowsum_blocks, turns, bits;
 };
 
 template <int GS>
@@ -275,19 +267,19 @@ __global__ __launch_bounds__(64 * kWaves) void lora_shrink_row_kernel(const Shri
 template <int GS>
 __global__ __launch_bounds__(64 * kWaves, 4) void lora_shrink_tile_kernel(const ShrinkArgs p) {
   if (rowsum_block<GS>(p)) return;
-  shrink_tile(p.x, p.a, p.ids, p.scaling, p.h, p.M, p.K, p.L, p.R, (int)blockIdx.x - p.rowsum_blocks, p.turns);
+  shrink_tile(p.x, p.a, p.ids, p.scaling, p.h, p.M, p.K, p.L, p.R, (int)blockIdx.x - p.rowsum_blocks, p.turns,
+              p.bits);
 }
 
-// Few rows one by one, more in row tiles: the row kernel reads A once per row,
-// the tile kernel once per adapter of 16 rows, but through fewer workgroups
-// and in shorter runs. The whole call, row against tile kernel: 64 x 8192 x
+// Few rows one by one, more in units: the row kernel reads A once per row,
+// the tile kernel once per unit of 16, but through fewer workgroups and in
+// shorter runs. The whole call, row against tile kernel: 64 x 8192 x
 // 8192, rank 16, an adapter each 36.9 / 39.9 us, 4 adapters one after the other
-// 28.5 / 32.9; 100 x 8192 x 4096, rank 64, 8 adapters, mixed 32.4 / 30.6, one
-// after the other 31.4 / 29.4; 333 x 2560 x 9728, group 32, rank 24, 5
-// adapters, mixed 54.5 / 54.6, one after the other 53.2 / 49.3. Turns: as many
-// as there are adapters, up to 16 and about a thousand workgroups, for row
-// tiles of several adapters (the 333 rows mixed: 54.6 us with 4 turns, 50.7
-// with 8); a workgroup that finds no adapter left to it ends at once.
+// 28.5 / 32.9; rank 64, 64 adapters 53.3 / 53.8, 4 adapters 31.6 / 33.4; 100 x
+// 8192 x 4096, rank 64, 8 adapters, mixed 32.6 / 30.3, one after the other 31.7
+// / 30.1; 333 x 2560 x 9728, group 32, rank 24, 5 adapters, mixed 54.5 / 50.2.
+// Turns: as many as a block can have units, up to about a thousand workgroups,
+// but four at least; a workgroup that finds no unit left to it ends at once.
 template <int GS>
 static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
   p.rowsum_blocks = GS != 0 ? (p.M + kWaves - 1) / kWaves : 0;
@@ -306,17 +298,21 @@ static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
 #undef W4A16_ROW
     return hipGetLastError();
   }
-  const int64_t tiles = (int64_t)((p.M + 15) / 16) * ((p.R + 15) / 16);
-  while (p.turns < 16 && p.turns < p.L && tiles * 2 * p.turns <= 1024) p.turns *= 2;
-  hipLaunchKernelGGL((lora_shrink_tile_kernel<GS>), dim3((unsigned)(p.rowsum_blocks + tiles * p.turns)), threads, 0,
-                     stream, p);
+  const int64_t mt = (p.M + kUnitBlock - 1) / kUnitBlock, rt = (p.R + 15) / 16;
+  // units of a block: at most 64, and 64 / 16 + 15 / 16 for each adapter
+  const int64_t units = std::min(kUnitBlock, 4 + std::min(p.L, kUnitBlock) * 15 / 16);
+  p.turns = (int)std::min(units, std::max<int64_t>(4, 1024 / (mt * rt)));
+  p.bits = 1;
+  while (p.bits < 31 && (1 << p.bits) < p.L) ++p.bits;
+  const int64_t blocks = p.rowsum_blocks + rt * ((mt * p.turns + 7) / 8 * 8);
+  hipLaunchKernelGGL((lora_shrink_tile_kernel<GS>), dim3((unsigned)blocks), threads, 0, stream, p);
   return hipGetLastError();
 }
 
 hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, const float* scaling,
                               uint16_t* h, int M, int K, int L, int R, float* rowsums, int ld, int gsize,
                               hipStream_t stream) {
-  const ShrinkArgs p = {x, a, ids, scaling, h, rowsums, M, K, L, R, ld, 0, 1};
+  const ShrinkArgs p = {x, a, ids, scaling, h, rowsums, M, K, L, R, ld, 0, 1, 0};
   if (rowsums == nullptr) return launch_shrink_gs<0>(p, stream);
   if (gsize == 128) return launch_shrink_gs<128>(p, stream);
   if (gsize == 32) return launch_shrink_gs<32>(p, stream);

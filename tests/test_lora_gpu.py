@@ -123,6 +123,20 @@ def test_parity(M, N, K, group, R, L, kind, sk):
     assert torch.equal(first, c.run(split_k=sk))        # bitwise repeatable
 
 
+@pytest.mark.parametrize("M,group,R", [(64, 128, 72), (128, 128, 40), (129, 32, 128), (191, 128, 24), (700, 128, 88)])
+@pytest.mark.parametrize("sizes", [(1, 15, 16, 32), (17, 33, 14), (31, 1, 1, 1, 30), (48, 16), (64,), (63,), (2,) * 32])
+def test_adapters_strewn_over_blocks(M, group, R, sizes):
+    """Adapters with these numbers of rows, shuffled within each 64 rows (the
+    rows behind them bare): x . A^T is formed in units of up to 16 such rows."""
+    rng = np.random.default_rng(M + R + len(sizes))
+    c = Case(M, 80, 384, group, R, len(sizes) + 2, "mixed", seed=M + R)
+    ids = np.concatenate([rng.permutation(np.r_[np.repeat(rng.permutation(len(sizes) + 2)[:len(sizes)], sizes),
+                                                np.full(64 - sum(sizes), -1)]) for _ in range(-(-M // 64))])[:M]
+    c.ids = ids.astype(np.int32)
+    ref, bound = c.ref()
+    within(f64(c.run(adapter_ids=torch.from_numpy(c.ids).to(dev()))), ref, bound, f"strewn {M} {sizes}")
+
+
 @pytest.mark.parametrize("M,group", [(1, 128), (6, 128), (14, 128), (30, 128), (45, 128), (333, 128), (333, 32),
                                      (2000, 128)])
 @pytest.mark.parametrize("R", [8, 24, 40, 72, 88, 104, 120, 128])

@@ -328,15 +328,20 @@ def _rank(t, name: str, dtype, dims: int):
     return t.shape
 
 
-def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """torch.empty from the memory pool of the stream that will write it."""
-    if stream is None or not like.is_cuda:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else \
-            torch.cuda.default_stream(like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+def _out(t, name: str, dtype, shape, like: torch.Tensor, dev: int, stream) -> tuple:
+    """An output and its address: the caller's, checked as `_in` does, or a new
+    one from the memory pool of the stream that will write it."""
+    if t is not None:
+        return t, _in(t, name, dtype, shape, dev)
+    if stream is None:
+        t = like.new_empty(shape, dtype=dtype)
+    else:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device) if int(stream) else \
+                torch.cuda.default_stream(like.device)
+        with torch.cuda.stream(stream):
+            t = like.new_empty(shape, dtype=dtype)
+    return t, t.data_ptr()
 
 
 # the current stream of a device as an address, without building a Stream object
@@ -384,13 +389,13 @@ def w4a16_gemm_lora(x: torch.Tensor, w_packed: torch.Tensor, scales: torch.Tenso
     pb = _in(b, "b", bf16, (L, N, R), dev)
     pi = _in(adapter_ids, "adapter_ids", torch.int32, (M,), dev)
     pc = None if scaling is None else _in(scaling, "scaling", torch.float32, (L,), dev)
-    if y is None:
-        y = _empty((M, N), bf16, x, stream)
-    py = _in(y, "y", bf16, (M, N), dev)
+    y, py = _out(y, "y", bf16, (M, N), x, dev, stream)
     if workspace is None:
-        need = _lib().w4a16_gemm_lora_workspace_bytes(M, N, K, group_size, L, R, split_k)
-        workspace = _empty((need // 4,), torch.float32, x, stream)
-    pws, nws = _in(workspace, "workspace", torch.float32, workspace.shape, dev), workspace.numel()
+        nws = _lib().w4a16_gemm_lora_workspace_bytes(M, N, K, group_size, L, R, split_k) // 4
+        workspace, pws = _out(None, "workspace", torch.float32, (nws,), x, dev, stream)
+    else:
+        pws = _in(workspace, "workspace", torch.float32, getattr(workspace, "shape", None), dev)
+        nws = workspace.numel()
     _run("w4a16_gemm_lora", dev, stream, px, pw, ps, pa, pb, pi, pc, py, M, N, K, group_size, L, R, split_k, pws,
          nws * 4)
     return y
@@ -410,22 +415,17 @@ def w4a16_expert_sort(ids: torch.Tensor, G: int, order: Optional[torch.Tensor] =
     T, k = _rank(ids, "ids", i32, 2)
     dev = ids.get_device()
     pi = _in(ids, "ids", i32, (T, k), dev)
-    if order is None:
-        order = _empty((T * k,), i32, ids, stream)
-    if pos is None:
-        pos = _empty((T, k), i32, ids, stream)
-    if m_sizes is None:
-        m_sizes = _empty((G,), i32, ids, stream)
-    po = _in(order, "order", i32, (T * k,), dev)
-    pp = _in(pos, "pos", i32, (T, k), dev)
-    pm = _in(m_sizes, "m_sizes", i32, (G,), dev)
+    order, po = _out(order, "order", i32, (T * k,), ids, dev, stream)
+    pos, pp = _out(pos, "pos", i32, (T, k), ids, dev, stream)
+    m_sizes, pm = _out(m_sizes, "m_sizes", i32, (G,), ids, dev, stream)
+    pws = None
     if workspace is None:
-        need = _lib().w4a16_expert_sort_workspace_bytes(T, k, G)
-        if need > 0:
-            workspace = _empty((need // 4,), i32, ids, stream)
-    pws, nws = None, 0
-    if workspace is not None:
-        pws, nws = _in(workspace, "workspace", i32, workspace.shape, dev), workspace.numel()
+        nws = _lib().w4a16_expert_sort_workspace_bytes(T, k, G) // 4
+        if nws > 0:
+            workspace, pws = _out(None, "workspace", i32, (nws,), ids, dev, stream)
+    else:
+        pws = _in(workspace, "workspace", i32, getattr(workspace, "shape", None), dev)
+        nws = workspace.numel()
     _run("w4a16_expert_sort", dev, stream, pi, po, pp, pm, T, k, G, pws, nws * 4)
     return order, pos, m_sizes
 
@@ -439,10 +439,9 @@ def w4a16_expert_gather(x: torch.Tensor, pos: torch.Tensor, xs: Optional[torch.T
     dev = x.get_device()
     px = _in(x, "x", bf16, (T, width), dev)
     pp = _in(pos, "pos", torch.int32, (T, k), dev)
-    if xs is None:
-        xs = _empty((T * k, width), bf16, x, stream)
-    rows = _rank(xs, "xs", bf16, 2)[0]
-    _run("w4a16_expert_gather", dev, stream, px, pp, _in(xs, "xs", bf16, (rows, width), dev), T, k, rows, width)
+    rows = T * k if xs is None else _rank(xs, "xs", bf16, 2)[0]
+    xs, pxs = _out(xs, "xs", bf16, (rows, width), x, dev, stream)
+    _run("w4a16_expert_gather", dev, stream, px, pp, pxs, T, k, rows, width)
     return xs
 
 
@@ -455,9 +454,8 @@ def w4a16_expert_gather_grad(dxs: torch.Tensor, pos: torch.Tensor, dx: Optional[
     dev = dxs.get_device()
     pd = _in(dxs, "dxs", bf16, (rows, width), dev)
     pp = _in(pos, "pos", torch.int32, (T, k), dev)
-    if dx is None:
-        dx = _empty((T, width), bf16, dxs, stream)
-    _run("w4a16_expert_gather_grad", dev, stream, pd, pp, _in(dx, "dx", bf16, (T, width), dev), T, k, rows, width)
+    dx, pdx = _out(dx, "dx", bf16, (T, width), dxs, dev, stream)
+    _run("w4a16_expert_gather_grad", dev, stream, pd, pp, pdx, T, k, rows, width)
     return dx
 
 
@@ -471,9 +469,8 @@ def w4a16_expert_combine(z: torch.Tensor, pos: torch.Tensor, weights: Optional[t
     pz = _in(z, "z", bf16, (rows, width), dev)
     pp = _in(pos, "pos", torch.int32, (T, k), dev)
     pw = None if weights is None else _in(weights, "weights", torch.float32, (T, k), dev)
-    if y is None:
-        y = _empty((T, width), bf16, z, stream)
-    _run("w4a16_expert_combine", dev, stream, pz, pp, pw, _in(y, "y", bf16, (T, width), dev), T, k, rows, width)
+    y, py = _out(y, "y", bf16, (T, width), z, dev, stream)
+    _run("w4a16_expert_combine", dev, stream, pz, pp, pw, py, T, k, rows, width)
     return y
 
 
@@ -490,11 +487,7 @@ def w4a16_expert_combine_grad(dy: torch.Tensor, z: torch.Tensor, pos: torch.Tens
     pz = _in(z, "z", bf16, (rows, width), dev)
     pp = _in(pos, "pos", torch.int32, (T, k), dev)
     pw = _in(weights, "weights", f32, (T, k), dev)
-    if dz is None:
-        dz = _empty((rows, width), bf16, z, stream)
-    if dweights is None:
-        dweights = _empty((T, k), f32, z, stream)
-    pdz = _in(dz, "dz", bf16, (rows, width), dev)
-    pdw = _in(dweights, "dweights", f32, (T, k), dev)
+    dz, pdz = _out(dz, "dz", bf16, (rows, width), z, dev, stream)
+    dweights, pdw = _out(dweights, "dweights", f32, (T, k), z, dev, stream)
     _run("w4a16_expert_combine_grad", dev, stream, pd, pz, pp, pw, pdz, pdw, T, k, rows, width)
     return dz, dweights

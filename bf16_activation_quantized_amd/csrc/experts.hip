@@ -191,20 +191,25 @@ __global__ __launch_bounds__(64 * W) void expert_scatter_kernel(
     }
   } else {
     // thread (q, g): bin g of every parts-th block, 16 blocks in flight (a
-    // thread takes bins in turn where there are more of them than threads)
+    // thread takes bins in turn where there are more of them than threads);
+    // counts past the last block's read as zeros
     const int parts = nb < NTHR ? NTHR / nb : 1;
     const int q = nb < NTHR ? tid / nb : 0;
+    const uint32_t row = 4u * (uint32_t)nb, before_me = blockIdx.x * row, step = (uint32_t)parts * row;
+    const __amdgpu_buffer_rsrc_t rh = make_rsrc(hist, (uint32_t)blocks * row);   // blocks <= 256, nb <= 4097
     for (int g = tid - q * nb; g < nb && q < parts; g += NTHR) {
+      uint32_t o = (uint32_t)q * row + 4u * (uint32_t)g;
       int all = 0, before = 0;
-      for (int b0 = q; b0 < blocks; b0 += 16 * parts) {   // blocks <= 256, nb <= 4097
+      for (int b0 = 0; b0 < blocks; b0 += 16 * parts) {
         int v[16];
 #pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] = b0 + u * parts < blocks ? hist[(b0 + u * parts) * nb + g] : 0;
+        for (int u = 0; u < 16; ++u) v[u] = (int)ld32(rh, o + (uint32_t)u * step);
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
           all += v[u];
-          before += b0 + u * parts < (int)blockIdx.x ? v[u] : 0;
+          before += o + (uint32_t)u * step < before_me ? v[u] : 0;
         }
+        o += 16u * step;
       }
       atomicAdd(&total[g], all);
       atomicAdd(&at[g], before);
@@ -491,9 +496,9 @@ __global__ __launch_bounds__(256) void expert_combine_grad_kernel(const uint16_t
 // Shape of a sort: one block up to kSortSingle slots (one launch), else whole
 // tiles per block, at most kSortMaxBlocks blocks. Smaller tiles spread fewer
 // slots over more blocks, larger ones keep the blocks' counts few (pairs of
-// waves and slots per lane, us, 128 experts: 32768 slots 8.3 with 8 x 2, 9.6
-// with 16 x 2, 11.7 with 16 x 4; 524288 slots 15.1, 13.3, 13.8; 2097152 slots
-// 26.7, 29.1, 23.3); past 1024 bins the waves' counts take the LDS.
+// waves and slots per lane, us, 128 experts: 32768 slots 8.0 with 8 x 2, 9.3
+// with 16 x 2, 11.5 with 16 x 4; 524288 slots 15.0, 12.0, 12.9; 2097152 slots
+// 34.5, 24.8, 22.5); past 1024 bins the waves' counts take the LDS.
 struct SortShape {
   int waves, per, blocks;
   int64_t chunk;   // slots of a block
@@ -523,10 +528,11 @@ static hipError_t launch_sort_w(const int32_t* ids, int32_t* order, int32_t* pos
   const hipError_t ea = ensure_dyn_lds(reinterpret_cast<const void*>(&expert_scatter_kernel<W, PER>),
                                        160 * 1024 - 512, set);
   if (ea != hipSuccess) return ea;
-  // Up to 48 counts per thread every block adds the others' up itself; past
-  // that a third launch does (524288 slots: 128 experts 13.3 us without it, 14.7
-  // with it; 256 experts 18.0 and 15.7; 1024 experts 40 and 20).
-  const bool summed = blocks > 1 && blocks * (G + 1) > 48 * 64 * W;
+  // Up to 64 counts per thread every block adds the others' up itself; past
+  // that a third launch does (524288 slots: 128 experts 12.1 us without it, 14.7
+  // with it; 256 experts 14.5 and 14.6; 512 experts 19.8 and 16.1; 65536 x 8
+  // slots of 4096 experts 124 and 37).
+  const bool summed = blocks > 1 && blocks * (G + 1) > 64 * 64 * W;
   if (blocks > 1) {
     hipLaunchKernelGGL((expert_hist_kernel<W, PER>), dim3(blocks), dim3(64 * W), lds1, stream, ids, ws, S, G, chunk);
     const hipError_t e = hipGetLastError();

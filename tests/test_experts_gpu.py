@@ -47,7 +47,8 @@ SORT_CASES = [
     (2048, 1, 2048, "rand"), (2049, 1, 2049, "holes"), (683, 3, 5, "skew"), (131072, 1, 190, "holes"),
     (131072, 1, 191, "holes"), (131073, 1, 300, "rand"), (65536, 8, 190, "skew"), (65536, 8, 192, "holes"),
     (174763, 3, 1024, "holes"), (524289, 1, 383, "rand"), (524289, 1, 50, "holes"), (40961, 1, 1025, "holes"),
-    (9000, 1, 1200, "rand"),
+    (9000, 1, 1200, "rand"), (131072, 1, 255, "rand"), (131072, 1, 256, "skew"), (65536, 8, 255, "holes"),
+    (65536, 8, 256, "one"),
 ]
 
 

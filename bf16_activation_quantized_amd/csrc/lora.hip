@@ -6,8 +6,8 @@
 // The kernels here form h, the first product; the second joins the fp32
 // accumulators of the projection's own kernels (lora.hpp), so y is written
 // once and rounded once. There h enters the matrix core as two bf16 values
-// (its rounding and the rounding of what is left: 16 of its bits). Rows whose id is outside [0, L) get the
-// projection alone.
+// (its rounding and the rounding of what is left: 16 of its bits). Rows whose
+// id is outside [0, L) get the projection alone.
 #include <algorithm>
 
 #include "common.hpp"
@@ -25,10 +25,18 @@ constexpr int kWaves = 8;   // per workgroup, in every kernel here
 
 constexpr uint32_t kOutside = 0xFFFFFFF0u;   // a buffer offset past every extent: the load returns zeros
 
+// An element of h as its rounding to bf16 and the rounding of what is left. A
+// finite element that rounds to infinity (past the largest bf16, 255 * 2^120)
+// is that largest value and what is left of it, cut off so that the two do not
+// add up to infinity either (off by less than 2^112, 2^-16 of it); the second
+// part of an infinite one is 0, where infinity - infinity would be NaN.
 __device__ __forceinline__ void store_h(uint16_t* h, size_t plane, size_t e, float v) {
-  const uint16_t hi = to_bf16(v);
+  uint16_t hi = to_bf16(v);
+  const bool past = (hi & 0x7FFFu) == 0x7F80u, finite = fabsf(v) < __builtin_inff();
+  if (past && finite) hi -= 1;
+  const float left = v - bf16f(hi);
   h[e] = hi;
-  h[plane + e] = to_bf16(v - bf16f(hi));
+  h[plane + e] = !past ? to_bf16(left) : finite ? (uint16_t)(__float_as_uint(left) >> 16) : (uint16_t)0;
 }
 
 }  // namespace

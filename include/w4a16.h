@@ -291,9 +291,9 @@ w4a16_status w4a16_splitk_reduce(const float* workspace, uint16_t* y,
  * another adapter, or in another row, leaves a row as it is. X . A[l]^T is
  * summed in fp32 and enters the second product as the sum of two bf16 values
  * (relative error of each element at most 2^-16 down to magnitudes of 2^-109,
- * below which the second value may be lost; an infinite element counts as
- * such). No atomics are used: the result is bitwise reproducible for a given
- * shape and split_k.
+ * below which the second value may be lost; infinite elements, of it and of
+ * b, count as such). No atomics are used: the result is bitwise reproducible
+ * for a given shape and split_k.
  */
 size_t w4a16_gemm_lora_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                        int32_t group_size, int32_t L, int32_t R,

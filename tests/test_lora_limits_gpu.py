@@ -122,3 +122,17 @@ def test_small_elements(M, N, K, group, sk, R):
     c.sc[:] = np.array([1.2345678 * 2.0 ** -100, 1.9999 * 2.0 ** -109, 1.0039 * 2.0 ** -109], dtype=np.float32)
     c.b *= 2.0 ** 100
     c.check(sk)
+
+
+@pytest.mark.parametrize("M,N,K,group,sk", SHAPES)
+@pytest.mark.parametrize("R", [8, 48, 128])
+def test_infinite_elements_of_b(M, N, K, group, sk, R):
+    """An infinite element of B gives +-infinity in its column, whatever the
+    second part of the element of x . A^T that it meets (0, or of either sign)."""
+    for seed in range(8 if M == 1 else 2):
+        c = Case(M, N, K, group, R, 3, 3, seed=M + K + R + seed)
+        c.sc[:] = np.array([1.0, 0.7, 1.3], dtype=np.float32)
+        c.b[:, 3, R - 1] = np.inf
+        c.b[:, 9, 0] = -np.inf
+        c.b[:, 20, :] = np.where(c.b[:, 20, :] > 1.5, np.inf, c.b[:, 20, :])
+        c.check(sk)

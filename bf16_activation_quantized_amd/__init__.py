@@ -349,16 +349,20 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _on(dev: int, f, *args):
+    """f(*args) with device `dev` current (sizes and plans go by its compute units)."""
+    if dev == torch.cuda.current_device():
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
 def _run(name: str, dev: int, stream, *args) -> None:
     """Calls a C entry point with device `dev` current, on `stream` or that
     device's current stream."""
     f = getattr(_lib_handle or _lib(), name)
     raw = _current_raw_stream(dev) if stream is None else _stream(stream)
-    if dev == torch.cuda.current_device():
-        status = f(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = f(*args, raw)
+    status = _on(dev, f, *args, raw)
     if status != 0:
         raise W4A16Error(status, name)
 
@@ -391,7 +395,7 @@ def w4a16_gemm_lora(x: torch.Tensor, w_packed: torch.Tensor, scales: torch.Tenso
     pc = None if scaling is None else _in(scaling, "scaling", torch.float32, (L,), dev)
     y, py = _out(y, "y", bf16, (M, N), x, dev, stream)
     if workspace is None:
-        nws = _lib().w4a16_gemm_lora_workspace_bytes(M, N, K, group_size, L, R, split_k) // 4
+        nws = _on(dev, _lib().w4a16_gemm_lora_workspace_bytes, M, N, K, group_size, L, R, split_k) // 4
         workspace, pws = _out(None, "workspace", torch.float32, (nws,), x, dev, stream)
     else:
         pws = _in(workspace, "workspace", torch.float32, getattr(workspace, "shape", None), dev)

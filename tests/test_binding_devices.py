@@ -74,3 +74,23 @@ def test_sizes_are_asked_on_the_tensors_device(on_device_1):
     assert [(n, d) for n, d, _ in on_device_1.calls] == [("w4a16_gemm_lora_workspace_bytes", 1),
                                                          ("w4a16_gemm_lora", 1)]
     assert on_device_1.current == 0
+
+
+def test_a_stream_of_another_device_is_refused(on_device_1):
+    t = Tensor
+    calls = [lora, lambda **kw: w4.w4a16_expert_sort(t(8, 2), 4, **kw),
+             lambda **kw: w4.w4a16_expert_gather(t(8, 64), t(8, 2), **kw),
+             lambda **kw: w4.w4a16_expert_gather_grad(t(16, 64), t(8, 2), **kw),
+             lambda **kw: w4.w4a16_expert_combine(t(16, 64), t(8, 2), **kw)]
+    own = on_device_1.Stream(1)
+    for f in calls:
+        on_device_1.calls.clear()
+        with pytest.raises(ValueError, match="device"):
+            f(stream=on_device_1.Stream(0))
+        assert not [n for n, _, _ in on_device_1.calls if not n.endswith("_bytes")]
+        f(stream=own)
+        assert on_device_1.calls[-1][1] == 1 and on_device_1.calls[-1][2][-1] == own.cuda_stream
+        f()                                             # the tensors' device's current stream
+        assert on_device_1.calls[-1][1] == 1 and on_device_1.calls[-1][2][-1] == 0x201
+        f(stream=0x7000)                                # an address is taken as it is
+        assert on_device_1.calls[-1][2][-1] == 0x7000

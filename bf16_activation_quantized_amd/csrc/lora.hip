@@ -297,11 +297,14 @@ static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
   if (MR <= 4096) {
 #define W4A16_ROW(RP) \
   hipLaunchKernelGGL((lora_shrink_row_kernel<RP, GS>), dim3(p.rowsum_blocks + p.M * (p.R / RP)), threads, 0, stream, p)
-    // ranks per workgroup: x is read once for all of them, but a few hundred
-    // workgroups should be there
-    if (MR >= 2048) W4A16_ROW(8);
-    else if (MR >= 1024) W4A16_ROW(4);
-    else if (MR >= 512) W4A16_ROW(2);
+    // Ranks per workgroup: x is read once for all of them, against the number of
+    // workgroups. The whole call with 1, 2, 4 (and 8) ranks: 16 x 4096 x 4096,
+    // rank 16, an adapter each 12.7, 12.8, 13.2 (13.8) us, 1 x 17408 x 5120,
+    // rank 16 12.9, 13.0, 13.2 (13.9); 64 x 8192 x 8192, rank 64, an adapter
+    // each 52.4, 50.6, 51.8 (53.4), 4 adapters one after the other 33.2, 30.9,
+    // 30.7 (31.6); 120 x 2560 x 9728, group 32, rank 32, 5 mixed 40.0, 37.7,
+    // 39.0 (two and four swap places by 1 % here and there, never by more).
+    if (MR >= 512) W4A16_ROW(2);
     else W4A16_ROW(1);
 #undef W4A16_ROW
     return hipGetLastError();

@@ -90,10 +90,11 @@ __device__ __forceinline__ void lora_load_b(bf16x8 (&bf)[NS][SN], const LoraArgs
 // they are (any value: the first parts' sum is infinite or NaN then; where the
 // second parts overflow by themselves, a product of the first, at least 2^8
 // times as large, does too). Up to 2 % of a call: 1000 x 5120 x 5120, rank 128,
-// 8 adapters mixed 116.8 -> 119.0 us, 1322 x 19456 x 2560, rank 64, 4 mixed
-// 185.1 -> 187.0, requests one after the other and small batches within 0.3 us
-// (a compare and a select in its place 190.0, a test of each adapter's B for
-// infinities and a clear only then 186.2 and 121.3).
+// 8 adapters mixed 116.8 -> 119.0 us, one after the other 92.4 -> 94.1, 1322 x
+// 19456 x 2560, rank 64, 4 mixed 185.1 -> 187.0, one after the other and small
+// batches within 0.3 us (a compare and a select in its place 190.0 for the 4
+// mixed; a test of each adapter's B for infinities and a clear only then 121.3
+// for the 8).
 template <int SN, int NS>
 __device__ __forceinline__ void lora_mac(f32x4 (&acc)[SN], const u32x4 (&hi)[NS], const u32x4 (&lo)[NS],
                                          const bf16x8 (&bf)[NS][SN], uint32_t mine, int kb) {
@@ -165,9 +166,11 @@ template <int MS, int SN, int NS>
 __device__ __forceinline__ void lora_tile_ns(f32x4 (&acc)[MS][SN], const uint8_t* hi, const uint8_t* lo,
                                              const int (&id)[LoraRows<MS>::Q], const LoraArgs& la, int n0, int lane,
                                              int part, int nparts) {
-  // adapters whose B fragments are in flight at once (in the registers that the
-  // accumulators of a short tile leave)
-  constexpr int NB = (MS <= 5 ? 8 : 4) / NS, Q = LoraRows<MS>::Q, LG = NS == 1 ? 0 : NS == 2 ? 1 : 2;
+  // adapters whose B fragments are in flight at once: 4 fragment steps of them
+  // (with 2 and 8: 200 x 4096 x 4096, rank 32, an adapter each 52.0, 50.7, 50.4
+  // us, rank 128, an adapter each 107.1, 106.1, 108.4; 1322 x 19456 x 2560, rank
+  // 64, 4 mixed 179.1, 181.3, 186.6)
+  constexpr int NB = 4 / NS, Q = LoraRows<MS>::Q, LG = NS == 1 ? 0 : NS == 2 ? 1 : 2;
   const int m16 = lane & 15, kb = lane >> 4;
   LoraRows<MS> adapters;
   adapters.reset(id);
@@ -223,8 +226,11 @@ __device__ __forceinline__ void lora_tile_add(f32x4 (&acc)[MS][SN], const uint8_
 
 // ---- small batch (M <= 16 MS rows): h read straight into the fragments by the
 // waves that hold an adapter, `part` of `nparts`; 4 / NS adapters' B fragments
-// are in flight at once, together with h of their rows. begin() requests them;
-// add() uses them, and goes on with the adapters that are left.
+// are in flight at once, together with h of their rows (with half as many, and
+// twice: 5 x 17408 x 5120, rank 16, an adapter each 24.9, 21.4, 21.5 us, 24 x
+// 17408 x 5120 46.0, 43.4, 44.8, 16 x 8192 x 8192, rank 64 23.4, 22.5, 22.4).
+// begin() requests them; add() uses them, and goes on with the adapters that
+// are left.
 
 // the adapter of row `lane`: a load at the kernel's start, used at its end
 __device__ __forceinline__ int lora_id(const LoraArgs& la, int lane) { return lane < la.M ? la.ids[lane] : -1; }

@@ -361,10 +361,14 @@ def _run(name: str, dev: int, stream, *args) -> None:
     """Calls a C entry point with device `dev` current, on `stream` or that
     device's current stream."""
     f = getattr(_lib_handle or _lib(), name)
-    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+    if stream is None:
+        raw = _current_raw_stream(dev)
+    elif isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
         raise ValueError(f"{name}: stream is on {stream.device}, the tensors on device {dev}")
-    raw = _current_raw_stream(dev) if stream is None else _stream(stream)
-    status = _on(dev, f, *args, raw)
+    else:
+        raw = _stream(stream)
+    # (the usual case without a frame of its own: these calls last a few us)
+    status = f(*args, raw) if dev == torch.cuda.current_device() else _on(dev, f, *args, raw)
     if status != 0:
         raise W4A16Error(status, name)
 

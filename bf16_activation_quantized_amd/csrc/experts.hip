@@ -69,7 +69,11 @@ constexpr int kBatch = 4;   // slots of a token whose rows are in flight togethe
 
 // Sort: a block of W waves takes tiles of PER slots per lane in turn.
 constexpr int kSortMaxBlocks = 256;
-constexpr int kSortSingle = 2048;           // slots that one block takes alone
+// Slots that one block takes alone, in up to two tiles, ahead of two launches
+// (one block against several, us: 1500 slots of 8 experts 5.6 / 6.9, 2048 slots
+// of 8 6.0 / 7.1, of 128 7.0 / 7.3; but 4096 slots of 8 9.7 / 7.2, of 128 11.8 /
+// 7.7).
+constexpr int kSortSingle = 2048;
 
 __device__ __forceinline__ int bin_of(int e, int G) {
   return (uint32_t)e < (uint32_t)G ? e : G;   // bin G: dropped

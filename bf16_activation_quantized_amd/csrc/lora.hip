@@ -282,10 +282,14 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lora_shrink_tile_kernel(const 
 // Few rows one by one, more in units: the row kernel reads A once per row,
 // the tile kernel once per unit of 16, but through fewer workgroups and in
 // shorter runs. The whole call, row against tile kernel: 64 x 8192 x
-// 8192, rank 16, an adapter each 36.9 / 39.9 us, 4 adapters one after the other
-// 28.5 / 32.9; rank 64, 64 adapters 53.3 / 53.8, 4 adapters 31.6 / 33.4; 100 x
-// 8192 x 4096, rank 64, 8 adapters, mixed 32.6 / 30.3, one after the other 31.7
-// / 30.1; 333 x 2560 x 9728, group 32, rank 24, 5 adapters, mixed 54.5 / 50.2.
+// 8192, rank 16, an adapter each 36.9 / 40.3 us, 4 adapters one after the other
+// 28.5 / 32.4; rank 64, 64 adapters 50.0 / 53.6, 4 adapters 30.9 / 32.9; 100 x
+// 8192 x 4096, rank 64, 8 adapters, mixed 33.1 / 30.8, one after the other 31.9
+// / 29.9; 333 x 2560 x 9728, group 32, rank 24, 5 adapters, mixed 54.9 / 50.3;
+// 1000 x 5120 x 5120, rank 8, 8 mixed 91.7 / 88.0. Past the border the row
+// kernel still wins where every row has an adapter of its own (64 x 4096 x
+// 9728, rank 128: 63.7 / 68.1; 4 adapters 36.1 / 34.2), which the host does not
+// know.
 // Turns: as many as a block can have units, up to about a thousand workgroups,
 // but four at least; a workgroup that finds no unit left to it ends at once.
 template <int GS>

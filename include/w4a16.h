@@ -341,6 +341,10 @@ w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,
  * one call never share a position. The rows that no slot names (those behind
  * the last kept one) are neither read nor written. Written arrays do not
  * overlap the read ones, except that dz may be z.
+ * The two gradients stand on both sides of the grouped product's own: from the
+ * dz of combine's to the dxs of gather's the caller brings dXs = dZ .
+ * dequant(W_g), which this library does not compute (nor gradients of the
+ * packed weights and their scales).
  *
  * w4a16_expert_gather: xs[pos[t, j]] = x[t].
  *   x : [T, width] bf16, device;  xs : [rows, width] bf16, device, written
@@ -361,7 +365,7 @@ w4a16_status w4a16_expert_gather_grad(const uint16_t* dxs, const int32_t* pos,
  *   z : [rows, width] bf16, device;  weights : [T, k] fp32, device (4-byte
  *   aligned), or NULL (all 1);  y : [T, width] bf16, device, written
  * w4a16_expert_combine_grad, its gradients from dy = dL/dy:
- *   dz[pos[t, j]] = weights[t, j] * dy[t] (bf16, rounded once), and
+ *   dz[pos[t, j]] = weights[t, j] * dy[t] (the fp32 product, rounded to bf16), and
  *   dweights[t, j] = sum_n dy[t, n] * z[pos[t, j], n] (fp32; 0 for a dropped
  *   slot).
  *   dy : [T, width] bf16, device;  z, dz : [rows, width] bf16, device (dz

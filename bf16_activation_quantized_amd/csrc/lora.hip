@@ -307,7 +307,7 @@ static hipError_t launch_shrink_gs(ShrinkArgs p, hipStream_t stream) {
     // rank 16 12.9, 13.0, 13.2 (13.9); 64 x 8192 x 8192, rank 64, an adapter
     // each 52.4, 50.6, 51.8 (53.4), 4 adapters one after the other 33.2, 30.9,
     // 30.7 (31.6); 120 x 2560 x 9728, group 32, rank 32, 5 mixed 40.0, 37.7,
-    // 39.0 (two and four swap places by 1 % here and there, never by more).
+    // 39.0 (four wins by 2 % at most, where it does).
     if (MR >= 512) W4A16_ROW(2);
     else W4A16_ROW(1);
 #undef W4A16_ROW

@@ -287,7 +287,7 @@ struct LoraSmall {
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         if (l[k] < 0) return;
-          static_for<MS>([&](auto i) {
+        static_for<MS>([&](auto i) {
           constexpr int ms = decltype(i)::value;
           const uint32_t mine = (uint32_t)(rows[k][0] >> (16 * ms)) & 0xFFFFu;
           if (mine != 0) lora_mac<SN, NS>(acc[ms], hi[ms], lo[ms], bf[k], mine, lane >> 4);

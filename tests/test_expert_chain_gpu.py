@@ -54,3 +54,57 @@ def test_run_of_all_four(T, k, G, K, N, group):
     assert (z[r0:] == 7.0).all()                         # rows behind the last expert: left as they were
     y = w4.w4a16_expert_combine(z, pos, w.to(dev()))
     within(f64(y), *combine_ref(f64(z), rp, f64(w)), "combine")
+
+
+def test_streams_by_address_and_threads():
+    """A stream given by its address (and 0, the default stream), outputs made by
+    the calls; no weights; and two host threads, each on a stream of its own."""
+    import threading
+
+    T, k, G, width = 500, 3, 9, 520
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(T, width, generator=gen).bfloat16().to(dev())
+    ids = torch.randint(-1, G + 1, (T, k), generator=gen, dtype=torch.int32).to(dev())
+    a, b = (torch.randn(4, *s, generator=gen).bfloat16().to(dev()) for s in ((16, 512), (64, 16)))
+    q = torch.randint(0, 256, (64, 256), generator=gen, dtype=torch.uint8).to(dev())
+    s = torch.ones(64, 4, dtype=torch.bfloat16, device=dev())
+    who = (torch.arange(T) % 5).int().to(dev())
+    xc = x[:, :512].contiguous()
+
+    def calls(stream):
+        order, pos, sizes = w4.w4a16_expert_sort(ids, G, stream=stream)
+        kept = int((pos >= 0).sum()) if stream is None else None
+        xs = w4.w4a16_expert_gather(x, pos, stream=stream)
+        y = w4.w4a16_expert_combine(xs, pos, stream=stream)
+        return kept, (order, pos, sizes, y, w4.w4a16_gemm_lora(xc, q, s, a, b, who, stream=stream))
+
+    kept, want = calls(None)
+    torch.cuda.synchronize()
+    ro, rp, rs = sort_ref(ids.cpu().numpy(), G)
+    assert kept == rs.sum()
+    xs = gather_ref(f64(x), rp, np.zeros((T * k, width)))
+    within(f64(want[3]), *combine_ref(xs, rp, None), "combine without weights")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side.cuda_stream, 0):
+        torch.cuda.synchronize()
+        got = calls(stream)[1]
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(want, got))
+    bad = []
+
+    def work():
+        mine = torch.cuda.Stream()
+        with torch.cuda.stream(mine):
+            for _ in range(20):
+                got = calls(mine)[1]
+                mine.synchronize()
+                if not all(torch.equal(u, v) for u, v in zip(want, got)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad

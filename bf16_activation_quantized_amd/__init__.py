@@ -74,6 +74,14 @@ def _lib():
         "w4a16_expert_gather_grad": (ctypes.c_int, [P, P, P, I64, I32, I64, I64, P]),
         "w4a16_expert_combine": (ctypes.c_int, [P, P, P, P, I64, I32, I64, I64, P]),
         "w4a16_expert_combine_grad": (ctypes.c_int, [P, P, P, P, P, P, I64, I32, I64, I64, P]),
+        "w4a16_fp8_quantize": (ctypes.c_int, [P, P, P, I64, I64, I32, P]),
+        "w4a16_fp8_gemm_workspace_bytes": (SZ, [I64, I64, I64]),
+        "w4a16_fp8_gemm": (ctypes.c_int, [P, P, P, P, P, I64, I64, I64, P, SZ, P]),
+        "w4a16_fp8_gemm_grouped": (ctypes.c_int, [P, P, P, P, P, P, I32, I64, I64, I64, P]),
+        "w4a16_fp8_gemm_grad_workspace_bytes": (SZ, [I64, I64, I64]),
+        "w4a16_fp8_gemm_grad": (ctypes.c_int, [P, P, P, P, P, P, I32, I64, I64, I64, P, SZ, P]),
+        "w4a16_gemm_grad_workspace_bytes": (SZ, [I32, I64, I64, I64, I32]),
+        "w4a16_gemm_grad": (ctypes.c_int, [P, P, P, P, P, I32, I64, I64, I64, I32, P, SZ, P]),
         # internal entry points that force a kernel (tests, benchmarks)
         "w4a16_gemm_auto_config": (ctypes.c_int, [I64, I64, I64, I32, P, P]),
         "w4a16_gemm_workspace_bytes_ex": (SZ, [I64, I64, I64, I32, I32, P]),
@@ -82,6 +90,14 @@ def _lib():
         "w4a16_gemm_batched_workspace_bytes_ex": (SZ, [I32, I64, I64, I64, I32, I32, P]),
         "w4a16_gemm_batched_ex": (ctypes.c_int, [P, P, P, P, I32, I64, I64, I64, I32, I32, P, SZ, P, P]),
     }
+    sig.update({
+        "w4a16_fp8_gemm_workspace_bytes_ex": (SZ, [I32, I64, I64, I64, I32, I32]),
+        "w4a16_fp8_gemm_ex": (ctypes.c_int, [I32, P, P, P, P, P, P, I32, I64, I64, I64, I32, I32, P, SZ, P]),
+        "w4a16_fp8_gemm_auto": (ctypes.c_int, [I32, I32, I32, I64, I64, I64, P, P]),
+        "w4a16_gemm_grad_workspace_bytes_ex": (SZ, [I32, I64, I64, I64, I32, I32, I32]),
+        "w4a16_gemm_grad_ex": (ctypes.c_int, [P, P, P, P, P, I32, I64, I64, I64, I32, I32, I32, P, SZ, P]),
+        "w4a16_gemm_grad_auto": (ctypes.c_int, [I32, I32, I64, I64, I64, I32, P, P]),
+    })
     for name, (res, args) in sig.items():
         f = getattr(L, name)
         f.restype = res
@@ -501,3 +517,142 @@ def w4a16_expert_combine_grad(dy: torch.Tensor, z: torch.Tensor, pos: torch.Tens
     dweights, pdw = _out(dweights, "dweights", f32, (T, k), z, dev, stream)
     _run("w4a16_expert_combine_grad", dev, stream, pd, pz, pp, pw, pdz, pdw, T, k, rows, width)
     return dz, dweights
+
+
+# ------------------------------------------------------------------ 8-bit products, input gradients
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _given_workspace(workspace, dtype, need: int, like: torch.Tensor, dev: int, stream) -> tuple:
+    """(address, bytes) of the caller's workspace or a new one of `need` bytes, and the tensor."""
+    if workspace is not None:
+        p = _in(workspace, "workspace", dtype, getattr(workspace, "shape", None), dev)
+        return workspace, p, workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, None, 0
+    workspace, p = _out(None, "workspace", dtype, (-(-need // dtype.itemsize),), like, dev, stream)
+    return workspace, p, need
+
+
+def w4a16_fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                       block_rows: int = 1, stream=None) -> tuple:
+    """x [M, K] bf16 -> (q [M, K] e4m3, scales [ceil(M / block_rows), K / 128]
+    fp32) in blocks of block_rows (1 or 128) x 128."""
+    M, K = _rank(x, "x", torch.bfloat16, 2)
+    dev = x.get_device()
+    px = _in(x, "x", torch.bfloat16, (M, K), dev)
+    q, pq = _out(q, "q", _E4M3, (M, K), x, dev, stream)
+    scales, ps = _out(scales, "scales", torch.float32, (-(-M // max(block_rows, 1)), K // 128), x, dev, stream)
+    _run("w4a16_fp8_quantize", dev, stream, px, pq, ps, M, K, block_rows)
+    return q, scales
+
+
+def w4a16_fp8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib().w4a16_fp8_gemm_workspace_bytes(M, N, K))
+
+
+def w4a16_fp8_gemm_grad_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib().w4a16_fp8_gemm_grad_workspace_bytes(M, N, K))
+
+
+def _fp8(name: str, grad: bool, x, x_scales, w, w_scales, m_sizes, y, workspace, stream, tile) -> torch.Tensor:
+    """The three calls on e4m3 operands; `tile`: (rows per tile, split of the
+    contraction), forced (internal entry point), or None."""
+    f32 = torch.float32
+    nx, ny = ("dy", "dx") if grad else ("x", "y")
+    M, C = _rank(x, nx, _E4M3, 2)
+    if m_sizes is None:
+        G, (N, K) = 1, _rank(w, "w", _E4M3, 2)
+        lead = ()
+    else:
+        G, N, K = _rank(w, "w", _E4M3, 3)
+        lead = (G,)
+    inner, outer = (N, K) if grad else (K, N)
+    dev = x.get_device()
+    px = _in(x, nx, _E4M3, (M, inner), dev)
+    pxs = _in(x_scales, nx + "_scales", f32, (M, inner // 128), dev)
+    pw = _in(w, "w", _E4M3, (*lead, N, K), dev)
+    pws = _in(w_scales, "w_scales", f32, (*lead, -(-N // 128), K // 128), dev)
+    pm = None if m_sizes is None else _in(m_sizes, "m_sizes", torch.int32, (G,), dev)
+    y, py = _out(y, ny, torch.bfloat16, (M, outer), x, dev, stream)
+    L = _lib_handle or _lib()
+    if tile is not None:
+        need = 0 if pm else _on(dev, L.w4a16_fp8_gemm_workspace_bytes_ex, int(grad), M, N, K, *tile)
+        workspace, pk, nk = _given_workspace(workspace, f32, need, x, dev, stream)
+        _run("w4a16_fp8_gemm_ex", dev, stream, int(grad), px, pxs, pw, pws, pm, py, G, M, N, K, *tile, pk, nk)
+    elif grad:
+        need = 0 if pm else _on(dev, L.w4a16_fp8_gemm_grad_workspace_bytes, M, N, K)
+        workspace, pk, nk = _given_workspace(workspace, f32, need, x, dev, stream)
+        _run(name, dev, stream, px, pxs, pw, pws, pm, py, G, M, N, K, pk, nk)
+    elif pm is None:
+        need = _on(dev, L.w4a16_fp8_gemm_workspace_bytes, M, N, K)
+        workspace, pk, nk = _given_workspace(workspace, f32, need, x, dev, stream)
+        _run(name, dev, stream, px, pxs, pw, pws, py, M, N, K, pk, nk)
+    else:
+        _run(name, dev, stream, px, pxs, pw, pws, pm, py, G, M, N, K)
+    return y
+
+
+def w4a16_fp8_gemm(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                   y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
+                   tile=None) -> torch.Tensor:
+    """Y [M, N] bf16 = (x x_scales) . (w w_scales)^T: x [M, K] e4m3 with scales
+    [M, K / 128], w [N, K] e4m3 with scales [ceil(N / 128), K / 128] (fp32)."""
+    return _fp8("w4a16_fp8_gemm", False, x, x_scales, w, w_scales, None, y, workspace, stream, tile)
+
+
+def w4a16_fp8_gemm_grouped(x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                           m_sizes: torch.Tensor, y: Optional[torch.Tensor] = None, stream=None,
+                           tile=None) -> torch.Tensor:
+    """w4a16_fp8_gemm for rows grouped by expert (w [G, N, K]); m_sizes [G]
+    int32 stays on the device. Rows past the last expert's are left as they were."""
+    return _fp8("w4a16_fp8_gemm_grouped", False, x, x_scales, w, w_scales, _sizes(m_sizes), y, None, stream, tile)
+
+
+def w4a16_fp8_gemm_grad(dy: torch.Tensor, dy_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                        m_sizes: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None, tile=None) -> torch.Tensor:
+    """dX [M, K] bf16 of w4a16_fp8_gemm (with m_sizes: of _grouped) from dy
+    [M, N] e4m3 with scales [M, N / 128]; N a multiple of 128."""
+    return _fp8("w4a16_fp8_gemm_grad", True, dy, dy_scales, w, w_scales, m_sizes, dx, workspace, stream, tile)
+
+
+def _sizes(m_sizes):
+    if m_sizes is None:
+        raise TypeError("m_sizes must be a torch.Tensor")
+    return m_sizes
+
+
+def w4a16_gemm_grad_workspace_bytes(G: int, M: int, N: int, K: int, group_size: int = GROUP_SIZE) -> int:
+    return int(_lib().w4a16_gemm_grad_workspace_bytes(G, M, N, K, group_size))
+
+
+def w4a16_gemm_grad(dy: torch.Tensor, w_packed: torch.Tensor, scales: torch.Tensor,
+                    m_sizes: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None, group_size: int = GROUP_SIZE,
+                    tile=None) -> torch.Tensor:
+    """dX [M, K] = dY [M, N] . dequant(W): the gradient of w4a16_gemm with
+    respect to x (with m_sizes and w_packed [G, N, K / 2]: of
+    w4a16_gemm_grouped). N a multiple of 8; workspace uint8."""
+    bf16, u8 = torch.bfloat16, torch.uint8
+    M, N = _rank(dy, "dy", bf16, 2)
+    shape = _rank(w_packed, "w_packed", u8, 2 if m_sizes is None else 3)
+    lead, K = tuple(shape[:-2]), 2 * shape[-1]
+    G = lead[0] if lead else 1
+    dev = dy.get_device()
+    pd = _in(dy, "dy", bf16, (M, N), dev)
+    pw = _in(w_packed, "w_packed", u8, (*lead, N, K // 2), dev)
+    ps = _in(scales, "scales", bf16, (*lead, N, K // group_size), dev)
+    pm = None if m_sizes is None else _in(m_sizes, "m_sizes", torch.int32, (G,), dev)
+    dx, px = _out(dx, "dx", bf16, (M, K), dy, dev, stream)
+    L = _lib_handle or _lib()
+    if tile is None:
+        need = 0 if workspace is not None else _on(dev, L.w4a16_gemm_grad_workspace_bytes, G, M, N, K, group_size)
+        workspace, pk, nk = _given_workspace(workspace, u8, need, dy, dev, stream)
+        _run("w4a16_gemm_grad", dev, stream, pd, pw, ps, pm, px, G, M, N, K, group_size, pk, nk)
+    else:
+        need = _on(dev, L.w4a16_gemm_grad_workspace_bytes_ex, G, M, N, K, group_size, *tile)
+        workspace, pk, nk = _given_workspace(workspace, u8, need, dy, dev, stream)
+        _run("w4a16_gemm_grad_ex", dev, stream, pd, pw, ps, pm, px, G, M, N, K, group_size, *tile, pk, nk)
+    return dx

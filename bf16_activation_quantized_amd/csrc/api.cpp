@@ -545,6 +545,146 @@ w4a16_status run_expert_combine(const uint16_t* z, const int32_t* pos, const flo
                                                reinterpret_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- 8-bit products and input gradients
+struct RowsPlan {
+  int bm;       // rows per tile
+  int32_t sk;   // slices of the contraction
+};
+
+// Slices of the contraction (cb steps) where fewer than half of the compute
+// units have a tile: as far as one round of workgroups goes, while a slice
+// keeps at least four steps.
+int32_t fill_split(int64_t tiles, int64_t cb) {
+  int32_t sk = 1;
+  while (sk < 16 && tiles * sk * 2 <= device_cus() && cb >= 8 * (int64_t)sk) sk <<= 1;
+  return sk;
+}
+
+// M rows of G groups (0: plain), O output columns, cb contraction blocks
+RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb) {
+  const int64_t per = G > 0 ? ceil_div(M, G) : M;
+  RowsPlan p = {256, 1};
+  if (per <= 16 && !grad) p.bm = 16;
+  else if (per <= 64) p.bm = 64;
+  else if (per <= 128) p.bm = 128;
+  if (G == 0 && p.bm != 16) p.sk = fill_split(ceil_div(M, p.bm) * ceil_div(O, 256), cb);
+  return p;
+}
+
+w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
+  if (G < 1 || (!grouped && G != 1)) return W4A16_ERR_SHAPE;
+  if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return W4A16_ERR_SHAPE;
+  if (K % kGroup != 0 || (grad && N % kGroup != 0)) return W4A16_ERR_SHAPE;
+  const uint64_t m = (uint64_t)M, n = (uint64_t)N, k = (uint64_t)K;
+  if (n * k > kMaxBytes || m * k * 2u > kMaxBytes || m * n * 4u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if (n * k * (uint64_t)G > (uint64_t)INT64_MAX / 2) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
+// The plan with the forced choices; partial sums in *bytes.
+w4a16_status make_fp8_plan(bool grad, int64_t G, int64_t M, int64_t N, int64_t K, int32_t bm, int32_t sk, RowsPlan* p,
+                           uint64_t* bytes) {
+  const int64_t O = grad ? K : N, cb = (grad ? N : K) / kGroup;
+  *p = fp8_plan(grad, G, M, O, cb);
+  if (bm != 0) {
+    if (bm != 64 && bm != 128 && bm != 256 && (bm != 16 || grad)) return W4A16_ERR_SHAPE;
+    p->bm = bm;
+    p->sk = 1;
+  }
+  if (sk != 0) {
+    if (sk < 1 || sk > 16 || (sk > 1 && (G > 0 || p->bm == 16))) return W4A16_ERR_SPLIT_K;
+    p->sk = sk;
+  }
+  *bytes = p->sk > 1 ? (uint64_t)p->sk * (uint64_t)M * (uint64_t)O * 4u : 0u;
+  return *bytes > kMaxBytes ? W4A16_ERR_SHAPE : W4A16_OK;
+}
+
+size_t fp8_workspace_bytes(bool grad, int64_t M, int64_t N, int64_t K, int32_t bm, int32_t sk) {
+  RowsPlan p;
+  uint64_t bytes = 0;
+  if (check_fp8(grad, false, 1, M, N, K) != W4A16_OK || M == 0) return 0;
+  if (make_fp8_plan(grad, 0, M, N, K, bm, sk, &p, &bytes) != W4A16_OK) return 0;
+  return (size_t)round_up(bytes, 256);
+}
+
+w4a16_status run_fp8(bool grad, const uint8_t* x, const float* xs, const uint8_t* w, const float* ws,
+                     const int32_t* m_sizes, uint16_t* y, int32_t G, int64_t M, int64_t N, int64_t K, int32_t bm,
+                     int32_t sk, float* workspace, size_t workspace_bytes, void* stream) {
+  RowsPlan p;
+  uint64_t bytes = 0;
+  w4a16_status st = check_fp8(grad, m_sizes != nullptr, G, M, N, K);
+  if (st != W4A16_OK || M == 0) return st;
+  if (x == nullptr || xs == nullptr || w == nullptr || ws == nullptr || y == nullptr) return W4A16_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned4(xs) || !aligned4(ws) || !aligned4(m_sizes))
+    return W4A16_ERR_ALIGN;
+  st = make_fp8_plan(grad, m_sizes != nullptr ? G : 0, M, N, K, bm, sk, &p, &bytes);
+  if (st != W4A16_OK) return st;
+  if (bytes > 0) {
+    if (workspace == nullptr || workspace_bytes < bytes) return W4A16_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+  }
+  const int64_t O = grad ? K : N, cb = (grad ? N : K) / kGroup;
+  hipStream_t strm = reinterpret_cast<hipStream_t>(stream);
+  const hipError_t e =
+      w4a16::launch_fp8_gemm(x, xs, w, ws, y, p.sk > 1 ? workspace : nullptr, m_sizes, (int)M, (int)N, (int)K, G,
+                             grad, (int)ceil_div(cb, p.sk), p.sk, p.bm, strm);
+  if (e != hipSuccess || p.sk == 1) return launched(e);
+  return launched(w4a16::launch_splitk_reduce(workspace, y, (uint64_t)M * (uint64_t)O, p.sk, strm));
+}
+
+// ---- input gradient of the 4-bit products
+w4a16_status check_w4_grad(bool grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size) {
+  if (G < 1 || (!grouped && G != 1)) return W4A16_ERR_SHAPE;
+  const w4a16_status st = check_dims(M, N, K, group_size);
+  if (st != W4A16_OK) return st;
+  if (N % 8 != 0) return W4A16_ERR_SHAPE;
+  const uint64_t np = (uint64_t)w4a16::w4_grad_padded(N);
+  if ((uint64_t)M * np * 2u > kMaxBytes || (uint64_t)M * (uint64_t)K * 4u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if ((uint64_t)G * np * (uint64_t)(K / group_size) * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if ((uint64_t)N * (uint64_t)K / 2u * (uint64_t)G > (uint64_t)INT64_MAX / 2) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
+w4a16_status make_w4_grad_plan(bool grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size,
+                               int32_t bm, int32_t sk, w4a16::W4GradPlan* p) {
+  const uint64_t np = (uint64_t)w4a16::w4_grad_padded(N), kg = (uint64_t)(K / group_size);
+  const int64_t per = grouped ? ceil_div(M, G) : M;
+  p->bm = per <= 16 ? 16 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
+  if (bm != 0) {
+    if (bm != 16 && bm != 64 && bm != 128 && bm != 256) return W4A16_ERR_SHAPE;
+    p->bm = bm;
+  }
+  p->sk = grouped ? 1 : fill_split(ceil_div(M, p->bm) * ceil_div(K, 256), (int64_t)np / 64);
+  if (sk != 0) {
+    if (sk < 1 || sk > 16 || (sk > 1 && grouped)) return W4A16_ERR_SPLIT_K;
+    p->sk = sk;
+  }
+  p->h = 0;
+  p->up = round_up((uint64_t)M * np * 2u, 256);
+  p->st = p->up + round_up((uint64_t)M * 4u, 256);
+  p->tops = p->st + round_up((uint64_t)G * kg * np * 2u, 256);
+  p->part = p->tops + round_up((uint64_t)G * (np / 128) * kg * 2u, 256);
+  const uint64_t part = p->sk > 1 ? (uint64_t)p->sk * (uint64_t)M * (uint64_t)K * 4u : 0u;
+  p->bytes = p->part + round_up(part, 256);
+  return part > kMaxBytes ? W4A16_ERR_SHAPE : W4A16_OK;
+}
+
+w4a16_status run_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* s, const int32_t* m_sizes, uint16_t* dx,
+                         int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t bm, int32_t sk,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  w4a16::W4GradPlan p;
+  w4a16_status st = check_w4_grad(m_sizes != nullptr, G, M, N, K, group_size);
+  if (st != W4A16_OK || M == 0) return st;
+  if (dy == nullptr || w == nullptr || s == nullptr || dx == nullptr) return W4A16_ERR_NULL;
+  if (!aligned16(dy) || !aligned16(w) || !aligned16(s) || !aligned16(dx) || !aligned4(m_sizes)) return W4A16_ERR_ALIGN;
+  st = make_w4_grad_plan(m_sizes != nullptr, G, M, N, K, group_size, bm, sk, &p);
+  if (st != W4A16_OK) return st;
+  if (workspace == nullptr || workspace_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
+  return launched(w4a16::launch_w4_grad(dy, w, s, dx, m_sizes, (int)M, (int)N, (int)K, G, group_size, p,
+                                        reinterpret_cast<uint8_t*>(workspace), reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -829,6 +969,111 @@ w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z, co
     return W4A16_ERR_ALIGN;
   return launched(w4a16::launch_expert_combine_grad(dy, z, pos, weights, dz, dweights, T, k, rows, (int)width,
                                                     reinterpret_cast<hipStream_t>(stream)));
+}
+
+w4a16_status w4a16_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int64_t M, int64_t K,
+                                int32_t block_rows, void* stream) {
+  if (M < 0 || K < 1 || M > kMaxDim || K > kMaxDim || K % kGroup != 0) return W4A16_ERR_SHAPE;
+  if (block_rows != 1 && block_rows != kGroup) return W4A16_ERR_SHAPE;
+  if ((uint64_t)M * (uint64_t)K >= (uint64_t{1} << 37)) return W4A16_ERR_SHAPE;
+  if (M == 0) return W4A16_OK;
+  if (x == nullptr || q == nullptr || scales == nullptr) return W4A16_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scales)) return W4A16_ERR_ALIGN;
+  return launched(
+      w4a16::launch_fp8_quantize(x, q, scales, M, (int)K, block_rows, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t w4a16_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return fp8_workspace_bytes(false, M, N, K, 0, 0);
+}
+
+size_t w4a16_fp8_gemm_grad_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return fp8_workspace_bytes(true, M, N, K, 0, 0);
+}
+
+size_t w4a16_fp8_gemm_workspace_bytes_ex(int32_t grad, int64_t M, int64_t N, int64_t K, int32_t bm, int32_t sk) {
+  return fp8_workspace_bytes(grad != 0, M, N, K, bm, sk);
+}
+
+w4a16_status w4a16_fp8_gemm(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                            uint16_t* y, int64_t M, int64_t N, int64_t K, float* workspace, size_t workspace_bytes,
+                            void* stream) {
+  return run_fp8(false, x, x_scales, w, w_scales, nullptr, y, 1, M, N, K, 0, 0, workspace, workspace_bytes, stream);
+}
+
+w4a16_status w4a16_fp8_gemm_grouped(const uint8_t* x, const float* x_scales, const uint8_t* w, const float* w_scales,
+                                    const int32_t* m_sizes, uint16_t* y, int32_t G, int64_t M_total, int64_t N,
+                                    int64_t K, void* stream) {
+  const w4a16_status st = check_fp8(false, true, G, M_total, N, K);
+  if (st != W4A16_OK || M_total == 0) return st;
+  if (m_sizes == nullptr) return W4A16_ERR_NULL;
+  return run_fp8(false, x, x_scales, w, w_scales, m_sizes, y, G, M_total, N, K, 0, 0, nullptr, 0, stream);
+}
+
+w4a16_status w4a16_fp8_gemm_grad(const uint8_t* dy, const float* dy_scales, const uint8_t* w, const float* w_scales,
+                                 const int32_t* m_sizes, uint16_t* dx, int32_t G, int64_t M, int64_t N, int64_t K,
+                                 float* workspace, size_t workspace_bytes, void* stream) {
+  return run_fp8(true, dy, dy_scales, w, w_scales, m_sizes, dx, G, M, N, K, 0, 0, workspace, workspace_bytes, stream);
+}
+
+w4a16_status w4a16_fp8_gemm_ex(int32_t grad, const uint8_t* x, const float* x_scales, const uint8_t* w,
+                               const float* w_scales, const int32_t* m_sizes, uint16_t* y, int32_t G, int64_t M,
+                               int64_t N, int64_t K, int32_t bm, int32_t sk, float* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return run_fp8(grad != 0, x, x_scales, w, w_scales, m_sizes, y, G, M, N, K, bm, sk, workspace, workspace_bytes,
+                 stream);
+}
+
+w4a16_status w4a16_fp8_gemm_auto(int32_t grad, int32_t grouped, int32_t G, int64_t M, int64_t N, int64_t K,
+                                 int32_t* bm_out, int32_t* sk_out) {
+  if (bm_out == nullptr || sk_out == nullptr) return W4A16_ERR_NULL;
+  const w4a16_status st = check_fp8(grad != 0, grouped != 0, G, M, N, K);
+  if (st != W4A16_OK) return st;
+  RowsPlan p;
+  uint64_t bytes = 0;
+  const w4a16_status sp = make_fp8_plan(grad != 0, grouped != 0 ? G : 0, M, N, K, 0, 0, &p, &bytes);
+  *bm_out = p.bm;
+  *sk_out = p.sk;
+  return sp;
+}
+
+size_t w4a16_gemm_grad_workspace_bytes_ex(int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t bm,
+                                          int32_t sk) {
+  w4a16::W4GradPlan p;
+  if (check_w4_grad(true, G, M, N, K, group_size) != W4A16_OK || M == 0) return 0;
+  if (make_w4_grad_plan(G > 1, G, M, N, K, group_size, bm, sk, &p) != W4A16_OK) return 0;
+  return (size_t)p.bytes;
+}
+
+size_t w4a16_gemm_grad_workspace_bytes(int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size) {
+  return w4a16_gemm_grad_workspace_bytes_ex(G, M, N, K, group_size, 0, 0);
+}
+
+w4a16_status w4a16_gemm_grad(const uint16_t* dy, const uint8_t* w_packed, const uint16_t* scales,
+                             const int32_t* m_sizes, uint16_t* dx, int32_t G, int64_t M, int64_t N, int64_t K,
+                             int32_t group_size, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_w4_grad(dy, w_packed, scales, m_sizes, dx, G, M, N, K, group_size, 0, 0, workspace, workspace_bytes,
+                     stream);
+}
+
+w4a16_status w4a16_gemm_grad_ex(const uint16_t* dy, const uint8_t* w_packed, const uint16_t* scales,
+                                const int32_t* m_sizes, uint16_t* dx, int32_t G, int64_t M, int64_t N, int64_t K,
+                                int32_t group_size, int32_t bm, int32_t sk, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return run_w4_grad(dy, w_packed, scales, m_sizes, dx, G, M, N, K, group_size, bm, sk, workspace, workspace_bytes,
+                     stream);
+}
+
+w4a16_status w4a16_gemm_grad_auto(int32_t grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size,
+                                  int32_t* bm_out, int32_t* sk_out) {
+  if (bm_out == nullptr || sk_out == nullptr) return W4A16_ERR_NULL;
+  const w4a16_status st = check_w4_grad(grouped != 0, G, M, N, K, group_size);
+  if (st != W4A16_OK) return st;
+  w4a16::W4GradPlan p;
+  const w4a16_status sp = make_w4_grad_plan(grouped != 0, G, M, N, K, group_size, 0, 0, &p);
+  *bm_out = p.bm;
+  *sk_out = p.sk;
+  return sp;
 }
 
 }  // extern "C"

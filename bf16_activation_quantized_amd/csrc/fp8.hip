@@ -1,0 +1,513 @@
+// 8-bit products with a scale for each block of 128, for gfx950.
+//
+//   Y[m, n] = sum_b sx[m, b] sw[n / 128, b] sum_{k in block b} X[m, k] W[n, k]
+//
+// and the input gradient, whose contraction runs over n instead of k. X and W
+// are e4m3 (OCP); the inner sums are exact products added in fp32 by the
+// matrix core (one v_mfma_f32_16x16x128_f8f6f4 is one block of 128), each is
+// scaled in fp32 and added to the fp32 accumulator, and the result is rounded
+// once to bf16.
+//
+// The weights are the MFMA's A operand (its rows are output columns) and the
+// activations its B operand, so a lane holds one row m and four consecutive
+// output columns of each tile: one product of scales per row tile and block
+// serves all of a wave's column tiles, and the outputs of a lane are
+// contiguous.
+#include "common.hpp"
+#include "launch.hpp"
+#include "tilemap.hpp"
+
+namespace w4a16 {
+
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kNW = 8;        // waves per workgroup
+constexpr int kBlk = 128;     // contraction elements per scale block (one MFMA)
+
+template <int VM>
+__device__ __forceinline__ void wait_vm_barrier() {
+  static_assert(VM >= 0 && VM < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds_dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds_dst, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint8_t* lds_dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds_dst, 4, voff, soff, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 frag(u32x4 a, u32x4 b) {
+  return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// one 16 x 16 tile's product over a block of 128, from zero
+__device__ __forceinline__ f32x4 block_product(i32x8 w, i32x8 x) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void add_scaled(f32x4& acc, float s, f32x4 t) {
+  acc.x = fmaf(s, t.x, acc.x);
+  acc.y = fmaf(s, t.y, acc.y);
+  acc.z = fmaf(s, t.z, acc.z);
+  acc.w = fmaf(s, t.w, acc.w);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- quantise
+// s = max(amax, 2^-100) / 448 and q = e4m3(x * (448 / max(amax, 2^-100))), both
+// in fp32, rounded to nearest even; a block with an infinity or a NaN: s = NaN,
+// q = 0. The largest magnitude of a block is taken on the bf16 bit patterns
+// (their order is that of the magnitudes, and infinities and NaN come last).
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinTop = 0x1p-100f;
+
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 r = __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b));
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// packed maxima of the magnitudes of 8 bf16
+__device__ __forceinline__ uint32_t top_of(u32x4 v) {
+  constexpr uint32_t m = 0x7FFF7FFFu;
+  return pk_max_u16(pk_max_u16(v.x & m, v.y & m), pk_max_u16(v.z & m, v.w & m));
+}
+
+struct BlockScale {
+  float s, r;   // the scale, and the factor that the values are multiplied by
+  bool fine;
+};
+__device__ __forceinline__ BlockScale block_scale(uint32_t top16) {
+  BlockScale b;
+  b.fine = top16 < 0x7F80u;
+  const float top = fmaxf(bf16f((uint16_t)top16), kMinTop);
+  b.s = b.fine ? top / kE4m3Max : __uint_as_float(0x7FC00000u);
+  b.r = kE4m3Max / top;
+  return b;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(uint32_t lo, uint32_t hi, float r) {
+  int o = __builtin_amdgcn_cvt_pk_fp8_f32(bf16lo(lo) * r, bf16hi(lo) * r, 0, false);
+  o = __builtin_amdgcn_cvt_pk_fp8_f32(bf16lo(hi) * r, bf16hi(hi) * r, o, true);
+  return (uint32_t)o;
+}
+__device__ __forceinline__ u32x4 e4m3x16(u32x4 a, u32x4 b, const BlockScale& s) {
+  if (!s.fine) return u32x4{0u, 0u, 0u, 0u};
+  return u32x4{e4m3x4(a.x, a.y, s.r), e4m3x4(a.z, a.w, s.r), e4m3x4(b.x, b.y, s.r), e4m3x4(b.z, b.w, s.r)};
+}
+
+// Blocks of 1 x 128: with K a multiple of 128 they are consecutive runs of 128
+// elements, 8 lanes each.
+__global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(const uint16_t* __restrict__ x,
+                                                                uint8_t* __restrict__ q, float* __restrict__ scales,
+                                                                int64_t blocks) {
+  const int64_t b = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  if (b >= blocks) return;   // whole groups of 8 lanes
+  const int l = threadIdx.x & 7;
+  const u32x4* src = reinterpret_cast<const u32x4*>(x + b * kBlk + 16 * l);
+  const u32x4 v0 = src[0], v1 = src[1];
+  uint32_t t = pk_max_u16(top_of(v0), top_of(v1));
+  t = max(t & 0xFFFFu, t >> 16);
+  t = max(t, (uint32_t)__shfl_xor((int)t, 1));
+  t = max(t, (uint32_t)__shfl_xor((int)t, 2));
+  t = max(t, (uint32_t)__shfl_xor((int)t, 4));
+  const BlockScale s = block_scale(t);
+  *reinterpret_cast<u32x4*>(q + b * kBlk + 16 * l) = e4m3x16(v0, v1, s);
+  if (l == 0) scales[b] = s.s;
+}
+
+// Blocks of 128 x 128 (the last rows' may be shorter): one workgroup each.
+__global__ __launch_bounds__(256) void fp8_quantize_blocks_kernel(const uint16_t* __restrict__ x,
+                                                                  uint8_t* __restrict__ q,
+                                                                  float* __restrict__ scales, int64_t M, int K,
+                                                                  int kblocks) {
+  __shared__ uint32_t tops[4];
+  const int64_t rb = blockIdx.x / kblocks;
+  const int cb = blockIdx.x % kblocks;
+  const int l = threadIdx.x & 7;
+  u32x4 v[4][2];
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = rb * kBlk + 32 * i + (threadIdx.x >> 3);
+    v[i][0] = v[i][1] = u32x4{0u, 0u, 0u, 0u};
+    if (row < M) {
+      const u32x4* src = reinterpret_cast<const u32x4*>(x + row * K + cb * kBlk + 16 * l);
+      v[i][0] = src[0];
+      v[i][1] = src[1];
+    }
+    t = pk_max_u16(t, pk_max_u16(top_of(v[i][0]), top_of(v[i][1])));
+  }
+  t = max(t & 0xFFFFu, t >> 16);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) t = max(t, (uint32_t)__shfl_xor((int)t, d));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = t;
+  __syncthreads();
+  const BlockScale s = block_scale(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = rb * kBlk + 32 * i + (threadIdx.x >> 3);
+    if (row < M) *reinterpret_cast<u32x4*>(q + row * K + cb * kBlk + 16 * l) = e4m3x16(v[i][0], v[i][1], s);
+  }
+  if (threadIdx.x == 0) scales[rb * kblocks + cb] = s.s;
+}
+
+hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int64_t M, int K, int block_rows,
+                               hipStream_t stream) {
+  const int kblocks = K / kBlk;
+  if (block_rows == 1) {
+    const int64_t grid = (M * kblocks + 31) / 32;
+    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fp8_quantize_rows_kernel, dim3((unsigned)grid), dim3(256), 0, stream, x, q, scales,
+                       M * kblocks);
+  } else {
+    const int64_t grid = (M + kBlk - 1) / kBlk * kblocks;
+    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(fp8_quantize_blocks_kernel, dim3((unsigned)grid), dim3(256), 0, stream, x, q, scales, M, K,
+                       kblocks);
+  }
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- tile kernel
+// One workgroup of 8 waves (WM x WN) per BM x 256 output tile; a stage is one
+// contraction block: X [BM rows, 128 B], W [256 columns, 128 B] (gradient: [128
+// rows, 256 B], transposed as it is read) and the BM row scales, filled by
+// buffer loads that write LDS directly, NS stages in a ring.
+struct Fp8Args {
+  const uint8_t* x;        // [M, C] e4m3: C = K, gradient: N
+  const float* xs;         // [M, C / 128]
+  const uint8_t* w;        // [G, N, K] e4m3
+  const float* ws;         // [G, ceil(N / 128), K / 128]
+  uint16_t* y;             // [M, O] bf16: O = N, gradient: K
+  float* part;             // [SK, M, O] fp32 partials, or nullptr
+  const int32_t* m_sizes;  // [G] on the device, or nullptr
+  int M, N, K, G;
+  int cps;                 // contraction blocks per slice
+  int mtiles, otiles;
+};
+
+constexpr int kBN = 256;      // output columns per tile
+
+template <int BM>
+constexpr int fp8_stage_bytes() { return BM * kBlk + kBN * kBlk + BM * 4; }
+
+template <int BM, int WM, int NS, bool GRAD>
+__global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
+  constexpr int WN = kNW / WM;
+  constexpr int TM = BM / WM, TN = kBN / WN;   // rows and columns per wave
+  constexpr int MS = TM / 16, SN = TN / 16;
+  constexpr int kX = BM * kBlk, kW = kBN * kBlk, kStage = fp8_stage_bytes<BM>();
+  constexpr int NQX = BM / 8;                  // 1 KiB loads of X per stage
+  constexpr int QX = (NQX + kNW - 1) / kNW;
+  constexpr int QW = kBN / 8 / kNW;            // of W per wave
+  static_assert(TN <= kBlk && MS >= 1 && SN >= 1, "a wave's columns lie in one block");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wv / WN, wn = wv % WN;
+  const int r16 = lane & 15, q4 = lane >> 4;
+
+  int mt, ot;
+  TileRows tr;
+  if (a.m_sizes != nullptr) {
+    const GroupScan gs(a.m_sizes, a.G, a.M, BM);
+    const int nblocks = gs.tiles * a.otiles;
+    if ((int)blockIdx.x >= nblocks) return;
+    tile_coords(blockIdx.x, nblocks, gs.tiles, a.otiles, &mt, &ot);
+    tr = gs.find(mt);
+  } else {
+    tile_coords(blockIdx.x, (int)gridDim.x, a.mtiles, a.otiles, &mt, &ot);
+    tr = TileRows{0, mt * BM, min(BM, a.M - mt * BM)};
+  }
+  if (tr.rows <= 0) return;
+
+  const int C = GRAD ? a.N : a.K, O = GRAD ? a.K : a.N;
+  const int Cb = C / kBlk, KB = a.K / kBlk, NB = (a.N + kBlk - 1) / kBlk;
+  const int o0 = ot * kBN;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tr.row0 * C, (uint32_t)tr.rows * (uint32_t)C);
+  const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.xs + (size_t)tr.row0 * Cb, (uint32_t)tr.rows * (uint32_t)Cb * 4u);
+  const uint32_t wk = (uint32_t)a.K;
+  const uint8_t* wg = a.w + (size_t)tr.wg * a.N * a.K;
+  const __amdgpu_buffer_rsrc_t rw = GRAD ? make_rsrc(wg + o0, (uint32_t)a.N * wk - (uint32_t)o0)
+                                         : make_rsrc(wg + (size_t)o0 * a.K, (uint32_t)min(kBN, O - o0) * wk);
+  // the wave's columns' scale of each contraction block (a wave past the last
+  // column takes the last block's: its outputs are not stored)
+  const int ob = min((o0 + TN * wn) / kBlk, (GRAD ? KB : NB) - 1);
+  const float* sw = a.ws + (size_t)tr.wg * NB * KB + (GRAD ? (size_t)ob : (size_t)ob * KB);
+  const int sw_step = GRAD ? KB : 1;
+
+  const int cb0 = blockIdx.y * a.cps;
+  const int nc = min(Cb, cb0 + a.cps) - cb0;
+
+  // 16-byte chunk c of an LDS row of X lies in slot c ^ ((row >> 1) & 7)
+  auto issue = [&](int cb, int stage) {
+    uint8_t* base = lds + stage * kStage;
+    const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)cb * kBlk);
+    {
+      const int rr = lane >> 3;
+#pragma unroll
+      for (int i = 0; i < QX; ++i) {
+        const int q = wv + kNW * i;
+        const int row = 8 * q + rr;
+        if (NQX % kNW == 0 || q < NQX)
+          dma16(rx, base + 1024 * q, (uint32_t)row * (uint32_t)C + 16u * (uint32_t)((lane & 7) ^ ((row >> 1) & 7)), so);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < QW; ++i) {
+      const int q = wv + kNW * i;
+      if constexpr (GRAD) {
+        const int row = 4 * q + (lane >> 4);
+        const int sl = (lane & 15) ^ ((row & 7) | ((row >> 2) & 8));
+        dma16(rw, base + kX + 1024 * q, ((uint32_t)cb * kBlk + (uint32_t)row) * wk + 16u * (uint32_t)sl, 0u);
+      } else {
+        const int row = 8 * q + (lane >> 3);
+        const int sl = (lane & 7) ^ (((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1);
+        dma16(rw, base + kX + 1024 * q, (uint32_t)row * wk + 16u * (uint32_t)sl, so);
+      }
+    }
+    const int srow = 64 * wv + lane;
+    if (srow < BM) dma4(rxs, base + kX + kW + 256 * wv, (uint32_t)srow * (uint32_t)Cb * 4u, (uint32_t)cb * 4u);
+  };
+
+  f32x4 acc[MS][SN];
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) acc[ms][ns] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto compute = [&](int stage, float sc) {
+    const uint8_t* base = lds + stage * kStage;
+    i32x8 wf[SN];
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) {
+      if constexpr (GRAD) {
+        // 8 rows x 16 columns transposed by each group of 16 lanes: lane 2 j, 2 j + 1
+        // point at row j's two 8-byte halves, lane c receives column c
+        u32x4 h[2];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int row = 32 * q4 + 8 * t + (r16 >> 1);
+          const int chunk = (TN * wn) / 16 + ns;
+          const uint32_t off = (uint32_t)row * kBN + 16u * (uint32_t)(chunk ^ ((row & 7) | ((row >> 2) & 8))) +
+                               8u * (uint32_t)(r16 & 1);
+          const i32x2 d = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2*)(base + kX + off));
+          h[t >> 1][2 * (t & 1)] = (uint32_t)d.x;
+          h[t >> 1][2 * (t & 1) + 1] = (uint32_t)d.y;
+        }
+        wf[ns] = frag(h[0], h[1]);
+      } else {
+        // MFMA row r of column tile ns is column 4 SN (r >> 2) + 4 ns + (r & 3): a
+        // lane's outputs are then 4 SN consecutive columns
+        const int row = TN * wn + 4 * SN * (r16 >> 2) + 4 * ns + (r16 & 3);
+        const int sz = ((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1;
+        const uint8_t* p = base + kX + row * kBlk;
+        wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4) ^ sz)),
+                      *reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4 + 1) ^ sz)));
+      }
+    }
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms) {
+      const int row = TM * wm + 16 * ms + r16;
+      const uint8_t* p = base + row * kBlk;
+      const int sz = (row >> 1) & 7;
+      const i32x8 xf = frag(*reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4) ^ sz)),
+                            *reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4 + 1) ^ sz)));
+      const float s = sc * *reinterpret_cast<const float*>(base + kX + kW + 4 * row);
+      f32x4 t[SN];
+#pragma unroll
+      for (int ns = 0; ns < SN; ++ns) t[ns] = block_product(wf[ns], xf);
+#pragma unroll
+      for (int ns = 0; ns < SN; ++ns) add_scaled(acc[ms][ns], s, t[ns]);
+    }
+  };
+
+  // stages j + 1 .. j + NS - 2 stay in flight over the wait for stage j
+  constexpr int kPer = QW + NQX / kNW;   // loads of a stage, by any wave at least
+  auto sw_at = [&](int j) { return sw[(size_t)(cb0 + min(j, nc - 1)) * sw_step]; };
+  if (nc > 0) {
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s)
+      if (s < nc) issue(cb0 + s, s);
+    float sc = sw_at(0);
+    for (int j = 0; j < nc; ++j) {
+      if (j + NS - 2 < nc) wait_vm_barrier<(NS - 2) * kPer>();
+      else wait_vm_barrier<0>();
+      if (j + NS - 1 < nc) issue(cb0 + j + NS - 1, (j + NS - 1) % NS);
+      const float sn = sw_at(j + 1);
+      compute(j % NS, sc);
+      sc = sn;
+    }
+  }
+
+  // ---- epilogue
+  const size_t part0 = ((size_t)blockIdx.y * a.M + tr.row0) * O;
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms) {
+    const int row = TM * wm + 16 * ms + r16;
+    if (row >= tr.rows) continue;
+    uint16_t* yr = a.y + (size_t)(tr.row0 + row) * O;
+    float* pr = a.part == nullptr ? nullptr : a.part + part0 + (size_t)row * O;
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) {
+      const int c = o0 + TN * wn + (GRAD ? 16 * ns + 4 * q4 : 4 * SN * q4 + 4 * ns);
+      if (a.part != nullptr) {
+        if (O % 4 == 0 && c < O) {
+          *reinterpret_cast<f32x4*>(pr + c) = acc[ms][ns];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < O) pr[c + i] = acc[ms][ns][i];
+        }
+      } else if (O % 4 == 0) {
+        if (c < O)
+          *reinterpret_cast<u32x2*>(yr + c) =
+              u32x2{pack_bf16x2(acc[ms][ns].x, acc[ms][ns].y), pack_bf16x2(acc[ms][ns].z, acc[ms][ns].w)};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < O) yr[c + i] = to_bf16(acc[ms][ns][i]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Up to 16 rows (of one expert): the weights stream from memory straight into
+// the MFMA's operand registers, each once; the 8 waves of a workgroup take
+// every eighth contraction block of the same 16 NT columns and add their sums
+// through LDS, in wave order.
+template <int NT>
+__global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
+  constexpr int U = 4;   // blocks in flight
+  __shared__ __attribute__((aligned(16))) float sums[kNW][NT][256];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, q4 = lane >> 4;
+
+  int mt, ot;
+  TileRows tr;
+  if (a.m_sizes != nullptr) {
+    const GroupScan gs(a.m_sizes, a.G, a.M, 16);
+    const int nblocks = gs.tiles * a.otiles;
+    if ((int)blockIdx.x >= nblocks) return;
+    tile_coords(blockIdx.x, nblocks, gs.tiles, a.otiles, &mt, &ot);
+    tr = gs.find(mt);
+  } else {
+    ot = blockIdx.x % a.otiles;
+    mt = blockIdx.x / a.otiles;
+    tr = TileRows{0, mt * 16, min(16, a.M - mt * 16)};
+  }
+  if (tr.rows <= 0) return;
+  const int K = a.K, KB = K / kBlk, NB = (a.N + kBlk - 1) / kBlk;
+  const int o0 = ot * 16 * NT;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tr.row0 * K, (uint32_t)tr.rows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.xs + (size_t)tr.row0 * KB, (uint32_t)tr.rows * (uint32_t)KB * 4u);
+  const __amdgpu_buffer_rsrc_t rw =
+      make_rsrc(a.w + ((size_t)tr.wg * a.N + o0) * K, (uint32_t)min(16 * NT, a.N - o0) * (uint32_t)K);
+  // 16 NT divides 128: the columns lie in one block
+  const float* sw = a.ws + ((size_t)tr.wg * NB + o0 / kBlk) * KB;
+  const uint32_t roff = (uint32_t)r16 * (uint32_t)K + 32u * (uint32_t)q4;
+
+  f32x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int b0 = wv; b0 < KB; b0 += kNW * U) {
+    u32x4 wr[U][NT][2], xr[U][2];
+    float sx[U], sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + kNW * u;
+      if (b >= KB) break;
+      const uint32_t so = (uint32_t)b * kBlk;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        wr[u][t][0] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K, so);
+        wr[u][t][1] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K + 16u, so);
+      }
+      xr[u][0] = ld128(rx, roff, so);
+      xr[u][1] = ld128(rx, roff + 16u, so);
+      sx[u] = __uint_as_float(ld32(rxs, (uint32_t)r16 * (uint32_t)KB * 4u, (uint32_t)b * 4u));
+      sc[u] = sw[b];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + kNW * u >= KB) break;
+      const i32x8 xf = frag(xr[u][0], xr[u][1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        add_scaled(acc[t], sx[u] * sc[u], block_product(frag(wr[u][t][0], wr[u][t][1]), xf));
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(&sums[wv][t][r16 * 16 + 4 * q4]) = acc[t];
+  __syncthreads();
+  // element e: row e / 16 NT, column e % 16 NT
+  for (int e = threadIdx.x; e < 256 * NT; e += 64 * kNW) {
+    const int row = e / (16 * NT), c = e % (16 * NT);
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kNW; ++w) s += sums[w][c >> 4][row * 16 + (c & 15)];
+    if (row < tr.rows && o0 + c < a.N) a.y[(size_t)(tr.row0 + row) * a.N + o0 + c] = to_bf16(s);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+template <int BM, int WM, int NS, bool GRAD>
+static hipError_t launch_fp8_tile_t(Fp8Args a, int sk, hipStream_t stream) {
+  constexpr int lds_bytes = NS * fp8_stage_bytes<BM>();
+  static_assert(lds_bytes <= 160 * 1024, "LDS");
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t ea =
+      ensure_dyn_lds(reinterpret_cast<const void*>(&fp8_tile_kernel<BM, WM, NS, GRAD>), lds_bytes, lds_set);
+  if (ea != hipSuccess) return ea;
+  a.mtiles = (a.M + BM - 1) / BM + (a.m_sizes != nullptr ? a.G : 0);
+  a.otiles = ((GRAD ? a.K : a.N) + kBN - 1) / kBN;
+  const long long blocks = (long long)a.mtiles * a.otiles;
+  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp8_tile_kernel<BM, WM, NS, GRAD>), dim3((unsigned)blocks, sk), dim3(64 * kNW), lds_bytes,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <int NT>
+static hipError_t launch_fp8_rows_t(Fp8Args a, hipStream_t stream) {
+  a.mtiles = (a.M + 15) / 16 + (a.m_sizes != nullptr ? a.G : 0);
+  a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
+  const long long blocks = (long long)a.mtiles * a.otiles;
+  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp8_rows_kernel<NT>), dim3((unsigned)blocks), dim3(64 * kNW), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_gemm(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, uint16_t* y,
+                           float* part, const int32_t* m_sizes, int M, int N, int K, int G, bool grad, int cps, int sk,
+                           int bm, hipStream_t stream) {
+  const Fp8Args a = {x, xs, w, ws, y, part, m_sizes, M, N, K, G, cps, 0, 0};
+  if (bm == 16 && !grad && sk == 1) return launch_fp8_rows_t<2>(a, stream);
+  if (grad) {
+    switch (bm) {
+      case 256: return launch_fp8_tile_t<256, 2, 2, true>(a, sk, stream);
+      case 128: return launch_fp8_tile_t<128, 2, 3, true>(a, sk, stream);
+      case 64: return launch_fp8_tile_t<64, 1, 3, true>(a, sk, stream);
+      default: return hipErrorInvalidValue;
+    }
+  }
+  switch (bm) {
+    case 256: return launch_fp8_tile_t<256, 2, 2, false>(a, sk, stream);
+    case 128: return launch_fp8_tile_t<128, 2, 3, false>(a, sk, stream);
+    case 64: return launch_fp8_tile_t<64, 1, 3, false>(a, sk, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace w4a16

@@ -95,4 +95,26 @@ hipError_t launch_expert_combine_grad(const uint16_t* dy, const uint16_t* z, con
                                       uint16_t* dz, float* dw, int64_t T, int k, int64_t rows, int width,
                                       hipStream_t stream);
 
+// ---- 8-bit products with a scale for each block of 128 (fp8.hip)
+// scales of blocks of block_rows (1 or 128) x 128
+hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int64_t M, int K, int block_rows,
+                               hipStream_t stream);
+// grad: the input gradient (x: dY, contraction over N). bm: rows per tile (16:
+// the kernel for few rows, whole contractions of the products only). With
+// part != nullptr slice s of sk, cps contraction blocks, writes fp32
+// partials part[s, :, :].
+hipError_t launch_fp8_gemm(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, uint16_t* y,
+                           float* part, const int32_t* m_sizes, int M, int N, int K, int G, bool grad, int cps, int sk,
+                           int bm, hipStream_t stream);
+
+// ---- input gradient of the 4-bit products (w4grad.hip)
+constexpr int64_t w4_grad_padded(int64_t N) { return (N + 127) / 128 * 128; }
+struct W4GradPlan {
+  int bm, sk;                       // rows per tile, slices of the contraction
+  uint64_t h, up, st, tops, part;   // byte offsets into the workspace
+  uint64_t bytes;
+};
+hipError_t launch_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* s, uint16_t* dx, const int32_t* m_sizes,
+                          int M, int N, int K, int G, int gsize, const W4GradPlan& p, uint8_t* ws, hipStream_t stream);
+
 }  // namespace w4a16

@@ -86,4 +86,68 @@ __device__ __forceinline__ int real_mtiles(int BM, int M_total, const int32_t* m
   return __builtin_amdgcn_readfirstlane(cnt);
 }
 
+// The row tiles of all groups, found by one wave: 64 groups at a time, their
+// sizes, starts and tile counts by prefix sums over the lanes (same clamping as
+// tile_rows). M_total < 2^25, so that the sums of 64 clamped sizes fit 32 bits.
+struct GroupScan {
+  const int32_t* m_sizes;
+  int G, M_total, BM;
+  int tiles;   // row tiles of all groups
+  struct Lanes {
+    uint32_t ms, start, cnt, before;   // rows, first row, tiles, tiles before
+  };
+  // groups base .. base + 63, with the rows and tiles of the groups before
+  __device__ __forceinline__ Lanes lanes(int base, uint32_t rows0, uint32_t tiles0) const {
+    const int g = base + (int)(threadIdx.x & 63);
+    int v = g < G ? m_sizes[g] : 0;
+    const uint32_t lim = (uint32_t)M_total;
+    const uint32_t want = min((uint32_t)max(v, 0), lim);
+    const uint32_t end = min(rows0 + prefix(want), lim);
+    Lanes l;
+    // the rows before: those of the lanes to the left, clamped likewise
+    const uint32_t left = (uint32_t)__shfl_up((int)end, 1);
+    l.start = (threadIdx.x & 63) == 0 ? min(rows0, lim) : left;
+    l.ms = end - l.start;
+    l.cnt = (l.ms + (uint32_t)BM - 1u) / (uint32_t)BM;
+    l.before = tiles0 + prefix(l.cnt) - l.cnt;
+    return l;
+  }
+  __device__ static __forceinline__ uint32_t prefix(uint32_t v) {   // inclusive, over the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_up((int)v, d);
+      if ((int)(threadIdx.x & 63) >= d) v += o;
+    }
+    return v;
+  }
+  __device__ __forceinline__ GroupScan(const int32_t* sizes, int G_, int M_total_, int BM_)
+      : m_sizes(sizes), G(G_), M_total(M_total_), BM(BM_) {
+    uint32_t rows = 0, t = 0;
+    for (int base = 0; base < G; base += 64) {
+      const Lanes l = lanes(base, rows, t);
+      rows = (uint32_t)__builtin_amdgcn_readlane((int)(l.start + l.ms), 63);
+      t = (uint32_t)__builtin_amdgcn_readlane((int)(l.before + l.cnt), 63);
+    }
+    tiles = __builtin_amdgcn_readfirstlane((int)t);
+  }
+  // the rows of tile mt (0 <= mt < tiles), the same in every lane
+  __device__ __forceinline__ TileRows find(int mt) const {
+    uint32_t rows = 0, t = 0;
+    for (int base = 0; base < G; base += 64) {
+      const Lanes l = lanes(base, rows, t);
+      const uint64_t hit = __ballot((uint32_t)mt >= l.before && (uint32_t)mt < l.before + l.cnt);
+      if (hit != 0) {
+        const int at = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+        const int start = __builtin_amdgcn_readlane((int)l.start, at);
+        const int ms = __builtin_amdgcn_readlane((int)l.ms, at);
+        const int off = (mt - __builtin_amdgcn_readlane((int)l.before, at)) * BM;
+        return TileRows{base + at, start + off, min(BM, ms - off)};
+      }
+      rows = (uint32_t)__builtin_amdgcn_readlane((int)(l.start + l.ms), 63);
+      t = (uint32_t)__builtin_amdgcn_readlane((int)(l.before + l.cnt), 63);
+    }
+    return TileRows{0, 0, 0};
+  }
+};
+
 }  // namespace w4a16

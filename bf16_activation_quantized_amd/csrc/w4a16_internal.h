@@ -75,6 +75,32 @@ w4a16_status w4a16_gemm_batched_ex(const uint16_t* x, const uint8_t* w_packed,
                                    float* workspace, size_t workspace_bytes,
                                    void* stream, const w4a16_config* cfg);
 
+/*
+ * The 8-bit products and the input gradients with a given tile height and
+ * split of the contraction (0: the automatic choice). bm: 16 (the kernel for
+ * few rows, w4a16_fp8_gemm and _grouped only, split 1), 64, 128 or 256 rows
+ * (w4a16_gemm_grad: 16 too); sk: 1 .. 16, 1 with m_sizes.
+ * grad: 0 the products, 1 w4a16_fp8_gemm_grad. Workspace bytes: of the call
+ * with these choices.
+ */
+size_t w4a16_fp8_gemm_workspace_bytes_ex(int32_t grad, int64_t M, int64_t N, int64_t K, int32_t bm, int32_t sk);
+w4a16_status w4a16_fp8_gemm_ex(int32_t grad, const uint8_t* x, const float* x_scales, const uint8_t* w,
+                               const float* w_scales, const int32_t* m_sizes, uint16_t* y, int32_t G, int64_t M,
+                               int64_t N, int64_t K, int32_t bm, int32_t sk, float* workspace,
+                               size_t workspace_bytes, void* stream);
+/* the automatic choice (grouped: with m_sizes) */
+w4a16_status w4a16_fp8_gemm_auto(int32_t grad, int32_t grouped, int32_t G, int64_t M, int64_t N, int64_t K,
+                                 int32_t* bm_out, int32_t* sk_out);
+
+size_t w4a16_gemm_grad_workspace_bytes_ex(int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t bm,
+                                          int32_t sk);
+w4a16_status w4a16_gemm_grad_ex(const uint16_t* dy, const uint8_t* w_packed, const uint16_t* scales,
+                                const int32_t* m_sizes, uint16_t* dx, int32_t G, int64_t M, int64_t N, int64_t K,
+                                int32_t group_size, int32_t bm, int32_t sk, void* workspace, size_t workspace_bytes,
+                                void* stream);
+w4a16_status w4a16_gemm_grad_auto(int32_t grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size,
+                                  int32_t* bm_out, int32_t* sk_out);
+
 #ifdef __cplusplus
 }
 #endif

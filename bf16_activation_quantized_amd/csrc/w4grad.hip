@@ -1,0 +1,397 @@
+// Input gradient of the 4-bit products, for gfx950:
+//
+//   dX[m, k] = sum_n dY[m, n] s[n, k / g] (q[n, k] - 8)
+//
+// The scale varies along the contraction, so it has to enter the matrix
+// core's operand. s (q - 8) has 8 + 3 significant bits: it is exact in fp16
+// and would be rounded in bf16. Both operands are therefore brought into fp16
+// by powers of two, each row of dY by its own and each column group of scales
+// by its own, and the accumulator is brought back by their product:
+//  * a row of dY has its largest finite magnitude in [2^14, 2^15): values down
+//    to 2^-29 of it are exact, smaller ones are rounded to 2^-40 of it;
+//  * a group of scales (one k group, all n) has its largest finite magnitude in
+//    [2^10, 2^11): products with q - 8 are exact for scales down to 2^-28 of
+//    it, smaller ones are rounded to 2^-35 of it.
+// A prepass writes dY in fp16, the scales transposed to [k group, n] and their
+// largest magnitudes per 128 n; both are ordered (0 4 1 5 2 6 3 7) within 8 n,
+// the order in which a word of 8 nibbles unpacks into pairs.
+#include "common.hpp"
+#include "launch.hpp"
+#include "tilemap.hpp"
+
+namespace w4a16 {
+
+namespace {
+
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kNW = 8;
+constexpr int kBN = 256;       // output columns (k) per tile
+constexpr int kSt = 64;        // contraction elements (n) per stage
+
+template <int VM>
+__device__ __forceinline__ void wait_vm_barrier() {
+  static_assert(VM >= 0 && VM < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
+typedef __attribute__((address_space(3))) void* lds_ptr;
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds_dst, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)lds_dst, 16, voff, soff, 0, 0);
+}
+
+// the power of two that brings the largest finite magnitude (bf16 bits) to
+// [2^to, 2^(to + 1)); subnormal maxima count as 2^-126
+__device__ __forceinline__ int up_by(uint32_t top16, int to) { return to + 127 - (int)max(top16 >> 7, 1u); }
+
+__device__ __forceinline__ uint32_t f16_pair(float a, float b, int e) {
+  const f16x2 h = {(_Float16)ldexpf(a, e), (_Float16)ldexpf(b, e)};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- prepass
+struct GradPrep {
+  const uint16_t* dy;   // [M, N]
+  const uint16_t* s;    // [G, N, Kg]
+  uint16_t* h;          // [M, Np] fp16, zero past N
+  int* up;              // [M] the power of two of each row
+  uint16_t* st;         // [G, Kg, Np] bf16 scales, zero past N
+  uint16_t* tops;       // [G, Np / 128, Kg] bf16 bits of the largest finite magnitudes
+  int M, N, Np, Kg, G;
+  int sblocks;          // workgroups per group of 128 n: ceil(Kg / 64)
+};
+
+// Workgroups 0 .. M - 1: a row of dY each; the others: 128 n x 64 k groups of
+// the scales of one expert.
+__global__ __launch_bounds__(256) void grad_prep_kernel(const GradPrep a) {
+  const int t = threadIdx.x;
+  if ((int)blockIdx.x < a.M) {
+    __shared__ uint32_t part[4];
+    const int m = blockIdx.x;
+    const u32x4* src = reinterpret_cast<const u32x4*>(a.dy + (size_t)m * a.N);
+    const int n8 = a.N / 8;
+    uint32_t top = 0;
+    auto take = [&](uint32_t v) {
+      v &= 0x7FFFu;
+      if (v < 0x7F80u) top = max(top, v);
+    };
+    for (int i = t; i < n8; i += 256) {
+      const u32x4 v = src[i];
+      take(v.x); take(v.x >> 16); take(v.y); take(v.y >> 16);
+      take(v.z); take(v.z >> 16); take(v.w); take(v.w >> 16);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if ((t & 63) == 0) part[t >> 6] = top;
+    __syncthreads();
+    top = max(max(part[0], part[1]), max(part[2], part[3]));
+    const int e = up_by(top, 14);
+    u32x4* dst = reinterpret_cast<u32x4*>(a.h + (size_t)m * a.Np);
+    for (int i = t; i < a.Np / 8; i += 256) {
+      const u32x4 v = i < n8 ? src[i] : u32x4{0u, 0u, 0u, 0u};
+      dst[i] = u32x4{f16_pair(bf16lo(v.x), bf16lo(v.z), e), f16_pair(bf16hi(v.x), bf16hi(v.z), e),
+                     f16_pair(bf16lo(v.y), bf16lo(v.w), e), f16_pair(bf16hi(v.y), bf16hi(v.w), e)};
+    }
+    if (t == 0) a.up[m] = e;
+    return;
+  }
+  __shared__ uint16_t tile[128][65];   // [n][k group]
+  int b = (int)blockIdx.x - a.M;
+  const int kc = b % a.sblocks;
+  b /= a.sblocks;
+  const int chunks = a.Np / 128;
+  const int nc = b % chunks, g = b / chunks;
+  for (int i = t; i < 128 * 64; i += 256) {
+    const int n = 128 * nc + (i >> 6), k = 64 * kc + (i & 63);
+    tile[i >> 6][i & 63] = (n < a.N && k < a.Kg) ? a.s[((size_t)g * a.N + n) * a.Kg + k] : (uint16_t)0;
+  }
+  __syncthreads();
+  for (int i = t; i < 64 * 16; i += 256) {   // 8 n of one k group each
+    const int kk = i >> 4, k = 64 * kc + kk, n = 8 * (i & 15);
+    if (k >= a.Kg) continue;
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = (uint32_t)tile[n + j][kk] | ((uint32_t)tile[n + j + 4][kk] << 16);
+    *reinterpret_cast<u32x4*>(a.st + ((size_t)g * a.Kg + k) * a.Np + 128 * nc + n) = u32x4{o[0], o[1], o[2], o[3]};
+  }
+  if (t < 64 && 64 * kc + t < a.Kg) {
+    uint32_t top = 0;
+    for (int n = 0; n < 128; ++n) {
+      const uint32_t v = tile[n][t] & 0x7FFFu;
+      if (v < 0x7F80u) top = max(top, v);
+    }
+    a.tops[((size_t)g * chunks + nc) * a.Kg + 64 * kc + t] = (uint16_t)top;
+  }
+}
+
+// ---------------------------------------------------------------- tile kernel
+// One workgroup of 8 waves (WM x WN) per BM x 256 tile of dX; a stage is 64 n:
+// dY in fp16 [BM rows, 128 B], the packed weights [64 rows, 128 B], which a
+// transposing LDS read turns into 16 n of one column per lane, and the tile's
+// NG groups of scales, s and -24 s in fp16 (a nibble reads as 16 + q: (16 + q) s
+// - 24 s = s (q - 8), one exact packed FMA for two weights).
+struct GradArgs {
+  const uint16_t* h;       // [M, Np] fp16
+  const int* up;           // [M]
+  const uint8_t* w;        // [G, N, K / 2]
+  const uint16_t* st;      // [G, Kg, Np]
+  const uint16_t* tops;    // [G, Np / 128, Kg]
+  uint16_t* dx;            // [M, K]
+  float* part;             // [SK, M, K] or nullptr
+  const int32_t* m_sizes;
+  int M, N, Np, K, G;
+  int sps;                 // stages per slice
+  int mtiles, otiles;
+};
+
+template <int BM, int GS>
+struct GradStage {
+  static constexpr int NG = kBN / GS;               // scale groups of a tile
+  static constexpr int kA = BM * 2 * kSt;
+  static constexpr int kW = kSt * kBN / 2;
+  static constexpr int kS = NG * kSt * 2;           // s, and as many bytes for -24 s
+  static constexpr int kBytes = kA + kW + 2 * kS;
+};
+
+template <int BM, int WM, int NS, int GS>
+__global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
+  using ST = GradStage<BM, GS>;
+  constexpr int WN = kNW / WM;
+  constexpr int TM = BM / WM, TN = kBN / WN;
+  constexpr int MS = TM / 16, SN = TN / 16;
+  constexpr int NG = ST::NG;
+  constexpr int NQA = BM / 8, QA = (NQA + kNW - 1) / kNW;
+  constexpr int SPT = NG * kSt / 2;               // scale pairs per stage
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ int gup[NG];                         // the power of two of each scale group
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wv / WN, wn = wv % WN;
+  const int r16 = lane & 15, q4 = lane >> 4;
+
+  int mt, ot;
+  TileRows tr;
+  if (a.m_sizes != nullptr) {
+    const GroupScan gs(a.m_sizes, a.G, a.M, BM);
+    const int nblocks = gs.tiles * a.otiles;
+    if ((int)blockIdx.x >= nblocks) return;
+    tile_coords(blockIdx.x, nblocks, gs.tiles, a.otiles, &mt, &ot);
+    tr = gs.find(mt);
+  } else {
+    tile_coords(blockIdx.x, (int)gridDim.x, a.mtiles, a.otiles, &mt, &ot);
+    tr = TileRows{0, mt * BM, min(BM, a.M - mt * BM)};
+  }
+  if (tr.rows <= 0) return;
+
+  const int K = a.K, Kg = K / GS, Np = a.Np, chunks = Np / 128;
+  const uint32_t K2 = (uint32_t)K / 2u;
+  const int o0 = ot * kBN, g0 = o0 / GS;
+  const int s0 = blockIdx.y * a.sps;
+  const int ns_ = min(Np / kSt, s0 + a.sps) - s0;   // stages
+
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.h + (size_t)tr.row0 * Np, (uint32_t)tr.rows * (uint32_t)Np * 2u);
+  const __amdgpu_buffer_rsrc_t rw =
+      make_rsrc(a.w + (size_t)tr.wg * a.N * K2 + (uint32_t)o0 / 2u, (uint32_t)a.N * K2 - (uint32_t)o0 / 2u);
+  // groups past the last column read zeros
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.st + ((size_t)tr.wg * Kg + g0) * Np, (uint32_t)(Kg - g0) * (uint32_t)Np * 2u);
+
+  auto issue = [&](int s, int stage) {
+    uint8_t* base = lds + stage * ST::kBytes;
+    const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)s * (2u * kSt));
+#pragma unroll
+    for (int i = 0; i < QA; ++i) {
+      const int q = wv + kNW * i;
+      const int row = 8 * q + (lane >> 3);
+      if (NQA % kNW == 0 || q < NQA)
+        dma16(ra, base + 1024 * q, (uint32_t)row * (uint32_t)Np * 2u + 16u * (uint32_t)((lane & 7) ^ ((row >> 1) & 7)),
+              so);
+    }
+    const int row = 8 * wv + (lane >> 3);
+    // (rows past N end past the extent, which checks the vector offset only)
+    dma16(rw, base + ST::kA + 1024 * wv,
+          ((uint32_t)s * kSt + (uint32_t)row) * K2 + 16u * (uint32_t)((lane & 7) ^ ((row >> 1) & 7)), 0u);
+  };
+  // scale pair p of a stage: group p / 32, n pair p % 32
+  auto scale_word = [&](int s) {
+    return tid < SPT ? ld32(rs, ((uint32_t)(tid >> 5) * (uint32_t)Np + (uint32_t)s * kSt) * 2u + 4u * (uint32_t)(tid & 31))
+                     : 0u;
+  };
+  auto put_scales = [&](int stage, uint32_t v, int e) {
+    if (tid < SPT) {
+      uint8_t* p = lds + stage * ST::kBytes + ST::kA + ST::kW + 4 * tid;
+      const uint32_t h = f16_pair(bf16lo(v), bf16hi(v), e);
+      const f16x2 m24 = {(_Float16)-24.0f, (_Float16)-24.0f};
+      const f16x2 c = __builtin_bit_cast(f16x2, h) * m24;
+      *reinterpret_cast<uint32_t*>(p) = h;
+      *reinterpret_cast<uint32_t*>(p + ST::kS) = __builtin_bit_cast(uint32_t, c);
+    }
+  };
+
+  // largest scale of each of the tile's groups over all n
+  for (int g = wv; g < NG; g += kNW) {
+    uint32_t top = 0;
+    if (g0 + g < Kg)
+      for (int c = lane; c < chunks; c += 64) top = max(top, (uint32_t)a.tops[((size_t)tr.wg * chunks + c) * Kg + g0 + g]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if (lane == 0) gup[g] = up_by(top, 10);
+  }
+  __syncthreads();
+  const int sup = tid < SPT ? gup[tid >> 5] : 0;
+
+  f32x4 acc[MS][SN];
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) acc[ms][ns] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto compute = [&](int stage) {
+    const uint8_t* base = lds + stage * ST::kBytes;
+    f16x8 wf[SN][2];
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) {
+      const int row = 16 * q4 + r16, ct = (TN * wn) / 16 + ns;   // 8 bytes: 16 columns
+      const uint32_t off =
+          (uint32_t)row * (kBN / 2) + 16u * (uint32_t)((ct >> 1) ^ ((row >> 1) & 7)) + 8u * (uint32_t)(ct & 1);
+      const i32x2 d = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+          (__attribute__((address_space(3))) i32x2*)(base + ST::kA + off));
+      const int grp = (TN * wn + 16 * ns) / GS;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const uint8_t* sp = base + ST::kA + ST::kW + (grp * kSt + 16 * q4 + 8 * st) * 2;
+        const u32x4 s = *reinterpret_cast<const u32x4*>(sp);
+        const u32x4 c = *reinterpret_cast<const u32x4*>(sp + ST::kS);
+        const uint32_t v = (uint32_t)(st == 0 ? d.x : d.y);
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // nibbles j and j + 4 to mantissa bits 6 .. 9 of the two halves of 16 + q
+          const uint32_t sh = j == 0 ? v << 6 : j == 1 ? v << 2 : j == 2 ? v >> 2 : v >> 6;
+          const uint32_t u = (sh & 0x03C003C0u) | 0x4C004C00u;
+          const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u), __builtin_bit_cast(f16x2, (uint32_t)s[j]),
+                                                    __builtin_bit_cast(f16x2, (uint32_t)c[j]));
+          o[j] = __builtin_bit_cast(uint32_t, r);
+        }
+        wf[ns][st] = __builtin_bit_cast(f16x8, o);
+      }
+    }
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms) {
+      const int row = TM * wm + 16 * ms + r16;
+      const uint8_t* p = base + row * (2 * kSt);
+      const int sz = (row >> 1) & 7;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const f16x8 xf = *reinterpret_cast<const f16x8*>(p + 16 * ((2 * q4 + st) ^ sz));
+#pragma unroll
+        for (int ns = 0; ns < SN; ++ns)
+          acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[ns][st], xf, acc[ms][ns], 0, 0, 0);
+      }
+    }
+  };
+
+  if (ns_ > 0) {
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      if (s < ns_) {
+        issue(s0 + s, s);
+        put_scales(s, scale_word(s0 + s), sup);
+      }
+    }
+    for (int j = 0; j < ns_; ++j) {
+      wait_vm_barrier<0>();
+      const bool ahead = j + NS - 1 < ns_;
+      uint32_t sv = 0;
+      if (ahead) {
+        sv = scale_word(s0 + j + NS - 1);
+        issue(s0 + j + NS - 1, (j + NS - 1) % NS);
+      }
+      compute(j % NS);
+      if (ahead) put_scales((j + NS - 1) % NS, sv, sup);
+    }
+  }
+
+  // ---- epilogue: lane holds row 16 ms + r16, columns 16 ns + 4 q4 + 0..3
+  const size_t part0 = ((size_t)blockIdx.y * a.M + tr.row0) * K;
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms) {
+    const int row = TM * wm + 16 * ms + r16;
+    if (row >= tr.rows) continue;
+    const int down = -a.up[tr.row0 + row];
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) {
+      const int c = o0 + TN * wn + 16 * ns + 4 * q4;
+      if (c >= K) continue;
+      const int e = down - gup[(TN * wn + 16 * ns) / GS];
+      const f32x4 v = {ldexpf(acc[ms][ns].x, e), ldexpf(acc[ms][ns].y, e), ldexpf(acc[ms][ns].z, e),
+                       ldexpf(acc[ms][ns].w, e)};
+      if (a.part != nullptr)
+        *reinterpret_cast<f32x4*>(a.part + part0 + (size_t)row * K + c) = v;
+      else
+        *reinterpret_cast<u32x2*>(a.dx + (size_t)(tr.row0 + row) * K + c) =
+            u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+    }
+  }
+}
+
+template <int BM, int WM, int NS, int GS>
+static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
+  constexpr int lds_bytes = NS * GradStage<BM, GS>::kBytes;
+  static_assert(lds_bytes <= 159 * 1024, "LDS");
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t ea =
+      ensure_dyn_lds(reinterpret_cast<const void*>(&w4_grad_kernel<BM, WM, NS, GS>), lds_bytes, lds_set);
+  if (ea != hipSuccess) return ea;
+  a.mtiles = (a.M + BM - 1) / BM + (a.m_sizes != nullptr ? a.G : 0);
+  a.otiles = (a.K + kBN - 1) / kBN;
+  const long long blocks = (long long)a.mtiles * a.otiles;
+  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((w4_grad_kernel<BM, WM, NS, GS>), dim3((unsigned)blocks, sk), dim3(64 * kNW), lds_bytes, stream,
+                     a);
+  return hipGetLastError();
+}
+
+template <int GS>
+static hipError_t launch_w4_grad_gs(const GradArgs& a, int sk, int bm, hipStream_t stream) {
+  switch (bm) {
+    case 256: return launch_w4_grad_t<256, 2, 3, GS>(a, sk, stream);
+    case 128: return launch_w4_grad_t<128, 2, 4, GS>(a, sk, stream);
+    case 64: return launch_w4_grad_t<64, 1, 4, GS>(a, sk, stream);
+    case 16: return launch_w4_grad_t<16, 1, 4, GS>(a, sk, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* s, uint16_t* dx, const int32_t* m_sizes,
+                          int M, int N, int K, int G, int gsize, const W4GradPlan& p, uint8_t* ws, hipStream_t stream) {
+  const int Np = (int)w4_grad_padded(N), Kg = K / gsize;
+  GradPrep pr;
+  pr.dy = dy; pr.s = s;
+  pr.h = reinterpret_cast<uint16_t*>(ws + p.h);
+  pr.up = reinterpret_cast<int*>(ws + p.up);
+  pr.st = reinterpret_cast<uint16_t*>(ws + p.st);
+  pr.tops = reinterpret_cast<uint16_t*>(ws + p.tops);
+  pr.M = M; pr.N = N; pr.Np = Np; pr.Kg = Kg; pr.G = G;
+  pr.sblocks = (Kg + 63) / 64;
+  const long long blocks = (long long)M + (long long)G * (Np / 128) * pr.sblocks;
+  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(grad_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, pr);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  GradArgs a;
+  a.h = pr.h; a.up = pr.up; a.w = w; a.st = pr.st; a.tops = pr.tops; a.dx = dx;
+  a.part = p.sk > 1 ? reinterpret_cast<float*>(ws + p.part) : nullptr;
+  a.m_sizes = m_sizes; a.M = M; a.N = N; a.Np = Np; a.K = K; a.G = G;
+  a.sps = (Np / kSt + p.sk - 1) / p.sk;
+  a.mtiles = a.otiles = 0;
+  const hipError_t el = gsize == 32 ? launch_w4_grad_gs<32>(a, p.sk, p.bm, stream)
+                                    : launch_w4_grad_gs<128>(a, p.sk, p.bm, stream);
+  if (el != hipSuccess || p.sk == 1) return el;
+  return launch_splitk_reduce(a.part, dx, (uint64_t)M * (uint64_t)K, p.sk, stream);
+}
+
+}  // namespace w4a16

@@ -381,6 +381,108 @@ w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z,
                                        int32_t k, int64_t rows, int64_t width,
                                        void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit products with a scale for each block of 128.
+ *
+ * Values are e4m3 (OCP: largest finite 448, one NaN), one byte each; scales
+ * are fp32, 4-byte aligned, and may be any finite number.
+ *
+ * w4a16_fp8_quantize: blocks of block_rows x 128 of a bf16 matrix,
+ *   top = max(largest magnitude of the block, 2^-100)
+ *   scales[r / block_rows, k / 128] = top / 448
+ *   q[r, k] = e4m3(x[r, k] * (448 / top))     (fp32, rounded to nearest even)
+ * A block with an infinity or a NaN has the scale NaN (and values of zero), so
+ * that every product with it is NaN.
+ *   x : [M, K] bf16, device;  q : [M, K] e4m3, device, written
+ *   scales : [ceil(M / block_rows), K / 128] fp32, device, written
+ *   block_rows 1 (activations, output gradients) or 128 (weights; the last
+ *   block may have fewer rows); M >= 0 (0: nothing enqueued), K >= 128,
+ *   K % 128 == 0, M * K < 2^37. x and q may be larger than 2^32 bytes.
+ */
+w4a16_status w4a16_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales,
+                                int64_t M, int64_t K, int32_t block_rows,
+                                void* stream);
+
+/*
+ * w4a16_fp8_gemm:
+ *   Y[m, n] = sum_b x_scales[m, b] w_scales[n / 128, b]
+ *                   sum_{k in block b of 128} X[m, k] W[n, k]
+ * summed in fp32 and rounded once to bf16.
+ *   x        : [M, K] e4m3;  x_scales : [M, K / 128] fp32, device
+ *   w        : [N, K] e4m3;  w_scales : [ceil(N / 128), K / 128] fp32, device
+ *   y        : [M, N] bf16, device, written
+ *   M >= 0 (0: nothing enqueued), N >= 1, K >= 128, K % 128 == 0.
+ *   workspace: fp32 device scratch, overwritten, at least
+ *   w4a16_fp8_gemm_workspace_bytes (0, and NULL allowed, for most shapes).
+ * No atomics: bitwise reproducible for a given shape.
+ */
+size_t w4a16_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+w4a16_status w4a16_fp8_gemm(const uint8_t* x, const float* x_scales,
+                            const uint8_t* w, const float* w_scales,
+                            uint16_t* y, int64_t M, int64_t N, int64_t K,
+                            float* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * w4a16_fp8_gemm_grouped: the same for rows grouped by expert, in one launch;
+ * rows, m_sizes and their preconditions as for w4a16_gemm_grouped.
+ *   x : [M_total, K];  x_scales : [M_total, K / 128];  w : [G, N, K];
+ *   w_scales : [G, ceil(N / 128), K / 128];  y : [M_total, N], written
+ */
+w4a16_status w4a16_fp8_gemm_grouped(const uint8_t* x, const float* x_scales,
+                                    const uint8_t* w, const float* w_scales,
+                                    const int32_t* m_sizes, uint16_t* y,
+                                    int32_t G, int64_t M_total, int64_t N,
+                                    int64_t K, void* stream);
+
+/*
+ * w4a16_fp8_gemm_grad: the gradient of both with respect to X, from dY
+ * quantised in blocks of 1 x 128 along N:
+ *   dX[m, k] = sum_b dy_scales[m, b] sum_{n in block b of 128} dY[m, n]
+ *              w_scales[b, k / 128] W[n, k]
+ * summed in fp32 and rounded once to bf16 (the quantisation of X counts as the
+ * identity; gradients of W are not computed).
+ *   dy : [M, N] e4m3;  dy_scales : [M, N / 128] fp32;  w, w_scales: as above
+ *   dx : [M, K] bf16, device, written
+ *   m_sizes : NULL (with G == 1), or the [G] sizes of the grouped product
+ *   N >= 128, N % 128 == 0; M, K and the workspace as for w4a16_fp8_gemm (the
+ *   workspace is used without m_sizes only).
+ */
+size_t w4a16_fp8_gemm_grad_workspace_bytes(int64_t M, int64_t N, int64_t K);
+w4a16_status w4a16_fp8_gemm_grad(const uint8_t* dy, const float* dy_scales,
+                                 const uint8_t* w, const float* w_scales,
+                                 const int32_t* m_sizes, uint16_t* dx,
+                                 int32_t G, int64_t M, int64_t N, int64_t K,
+                                 float* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * w4a16_gemm_grad: the gradient of w4a16_gemm and w4a16_gemm_grouped with
+ * respect to X (training what stands around frozen 4-bit weights):
+ *   dX[m, k] = sum_n dY[m, n] S[n, k / group_size] (q[n, k] - 8)
+ * with fp32 sums, rounded once to bf16.
+ *   dy : [M, N] bf16, device;  w_packed, scales, group_size: as for the product
+ *   dx : [M, K] bf16, device, written
+ *   m_sizes : NULL (with G == 1), or the [G] sizes of the grouped product
+ *   M >= 0 (0: nothing enqueued), N >= 8, N % 8 == 0, K >= 128, K % 128 == 0.
+ *   workspace: device scratch, overwritten, never NULL when M > 0: at least
+ *   w4a16_gemm_grad_workspace_bytes (dY and the scales in fp16, the partial
+ *   sums of a split contraction), 16-byte aligned.
+ * Numerics: S (q - 8) is exact in fp16, so no weight is rounded; dY and S enter
+ * in fp16, scaled by powers of two (dY by one per row, S by one per weight
+ * group and column group), which loses nothing of a value down to 2^-29 (dY)
+ * and 2^-28 (S) of the largest finite one in its row or column group; smaller
+ * values are rounded to 2^-40 (dY) and 2^-35 (S) of it. A non-finite value of
+ * dY reaches its row only, a non-finite scale its column group only, as NaN.
+ */
+size_t w4a16_gemm_grad_workspace_bytes(int32_t G, int64_t M, int64_t N,
+                                       int64_t K, int32_t group_size);
+w4a16_status w4a16_gemm_grad(const uint16_t* dy, const uint8_t* w_packed,
+                             const uint16_t* scales, const int32_t* m_sizes,
+                             uint16_t* dx, int32_t G, int64_t M, int64_t N,
+                             int64_t K, int32_t group_size, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

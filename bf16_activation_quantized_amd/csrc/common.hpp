@@ -82,6 +82,17 @@ __device__ __forceinline__ uint32_t xswz(int r) {
   return (uint32_t)((r & 3) | ((r >> 1) & 4) | ((((r >> 2) ^ (r >> 3)) & 1) << 3));
 }
 
+// The same for operand rows of 128 B (8 chunks; two rows span the banks): chunk
+// c of the row pair p = 0..7 (of 16 rows) sits in slot c ^ pair_swz(p). In a
+// wave's 16-byte reads, lane (row r, quarter q) at chunk 2 q or 2 q + 1, each
+// LDS cycle serves row pairs 0, 1, 6, 7 of one quarter and 2 .. 5 of its
+// neighbour (2 chunks on): the map sends the first four to slots 0 .. 3 and the
+// others to 4 .. 7, both closed under that step. XOR by p itself measured 8
+// cycles per read instead of 4.
+__device__ __forceinline__ uint32_t pair_swz(int p) {
+  return (uint32_t)((p & 1) | ((p >> 1) & 2) | (((p << 1) ^ p) & 4));
+}
+
 // ---------------------------------------------------------------- bf16
 __device__ __forceinline__ float bf16lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }

@@ -196,7 +196,7 @@ struct Fp8Args {
 constexpr int kBN = 256;      // output columns per tile
 
 template <int BM>
-constexpr int fp8_stage_bytes() { return BM * kBlk + kBN * kBlk + BM * 4; }
+constexpr int fp8_stage_bytes() { return BM * kBlk + kBN * kBlk + BM * 4 + 128; }
 
 template <int BM, int WM, int NS, bool GRAD>
 __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
@@ -238,16 +238,18 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
   const uint8_t* wg = a.w + (size_t)tr.wg * a.N * a.K;
   const __amdgpu_buffer_rsrc_t rw = GRAD ? make_rsrc(wg + o0, (uint32_t)a.N * wk - (uint32_t)o0)
                                          : make_rsrc(wg + (size_t)o0 * a.K, (uint32_t)min(kBN, O - o0) * wk);
-  // the wave's columns' scale of each contraction block (a wave past the last
-  // column takes the last block's: its outputs are not stored)
-  const int ob = min((o0 + TN * wn) / kBlk, (GRAD ? KB : NB) - 1);
-  const float* sw = a.ws + (size_t)tr.wg * NB * KB + (GRAD ? (size_t)ob : (size_t)ob * KB);
-  const int sw_step = GRAD ? KB : 1;
+  // scales of the tile's two column blocks: for contraction block b, one dword
+  // each at ((first block) + i) * sw_col + b * sw_step (the second block of a last
+  // tile may be past the end: it reads zero, and its outputs are not stored)
+  const int sw_col = GRAD ? 1 : KB, sw_step = GRAD ? KB : 1;
+  const size_t sw0 = (size_t)tr.wg * NB * KB;
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.ws + sw0, (uint32_t)NB * (uint32_t)KB * 4u);
 
   const int cb0 = blockIdx.y * a.cps;
   const int nc = min(Cb, cb0 + a.cps) - cb0;
 
-  // 16-byte chunk c of an LDS row of X lies in slot c ^ ((row >> 1) & 7)
+  // 16-byte chunks of an LDS row lie in slots by pair_swz of the row pair that a
+  // fragment read sees (W: rows 4 SN (r >> 2) + (r & 3) are one read's)
   auto issue = [&](int cb, int stage) {
     uint8_t* base = lds + stage * kStage;
     const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)cb * kBlk);
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
         const int q = wv + kNW * i;
         const int row = 8 * q + rr;
         if (NQX % kNW == 0 || q < NQX)
-          dma16(rx, base + 1024 * q, (uint32_t)row * (uint32_t)C + 16u * (uint32_t)((lane & 7) ^ ((row >> 1) & 7)), so);
+          dma16(rx, base + 1024 * q, (uint32_t)row * (uint32_t)C + 16u * ((uint32_t)(lane & 7) ^ pair_swz((row >> 1) & 7)), so);
       }
     }
 #pragma unroll
@@ -270,12 +272,17 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
         dma16(rw, base + kX + 1024 * q, ((uint32_t)cb * kBlk + (uint32_t)row) * wk + 16u * (uint32_t)sl, 0u);
       } else {
         const int row = 8 * q + (lane >> 3);
-        const int sl = (lane & 7) ^ (((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1);
-        dma16(rw, base + kX + 1024 * q, (uint32_t)row * wk + 16u * (uint32_t)sl, so);
+        const uint32_t sl = (uint32_t)(lane & 7) ^ pair_swz(((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1);
+        dma16(rw, base + kX + 1024 * q, (uint32_t)row * wk + 16u * sl, so);
       }
     }
-    const int srow = 64 * wv + lane;
-    if (srow < BM) dma4(rxs, base + kX + kW + 256 * wv, (uint32_t)srow * (uint32_t)Cb * 4u, (uint32_t)cb * 4u);
+    const uint32_t sb = __builtin_amdgcn_readfirstlane((uint32_t)cb * 4u);
+    if (wv < (BM + 63) / 64) {
+      if (BM % 64 == 0 || 64 * wv + lane < BM)
+        dma4(rxs, base + kX + kW + 256 * wv, (uint32_t)(64 * wv + lane) * (uint32_t)Cb * 4u, sb);
+    }
+    if (wv == kNW - 1 && lane < kBN / kBlk)
+      dma4(rws, base + kX + kW + 4 * BM, ((uint32_t)(o0 / kBlk + lane) * (uint32_t)sw_col + (uint32_t)cb * (uint32_t)sw_step) * 4u, 0u);
   };
 
   f32x4 acc[MS][SN];
@@ -284,69 +291,79 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) acc[ms][ns] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto compute = [&](int stage, float sc) {
+  // ---- LDS operand offsets within a stage
+  // X: row TM wm + 16 ms + r16, chunks 2 q4 and 2 q4 + 1
+  const uint32_t xo = (uint32_t)(TM * wm + r16) * kBlk + 16u * ((uint32_t)(2 * q4) ^ pair_swz(r16 >> 1));
+  // W: MFMA row r of column tile ns is column 4 SN (r >> 2) + 4 ns + (r & 3) of the
+  // wave's, so that a lane's outputs are 4 SN consecutive columns
+  const uint32_t wo = kX + (uint32_t)(TN * wn + 4 * SN * (r16 >> 2) + (r16 & 3)) * kBlk +
+                      16u * ((uint32_t)(2 * q4) ^ pair_swz(r16 >> 1));
+  // gradient: 8 rows x 16 columns are transposed by each group of 16 lanes: lanes
+  // 2 j and 2 j + 1 point at row j's two 8-byte halves, lane c receives column c
+  const uint32_t go = kX + (uint32_t)(32 * q4 + (r16 >> 1)) * kBN + 8u * (uint32_t)(r16 & 1) +
+                      16u * (uint32_t)((TN * wn / 16) ^ ((r16 >> 1) | (q4 & 1) << 3));
+  const uint32_t so_x = kX + kW + 4u * (uint32_t)(TM * wm + r16);
+  const uint32_t so_w = kX + kW + 4u * (uint32_t)BM + 4u * (uint32_t)(TN * wn / kBlk);
+
+  auto compute = [&](int stage) {
     const uint8_t* base = lds + stage * kStage;
-    i32x8 wf[SN];
+    i32x8 wf[SN], xf[2];
+    float sx[2];
+    auto read_x = [&](int ms) {
+      const uint8_t* p = base + 16 * kBlk * ms;
+      xf[ms & 1] = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
+      sx[ms & 1] = *reinterpret_cast<const float*>(base + so_x + 64 * ms);
+    };
+    const float sc = *reinterpret_cast<const float*>(base + so_w);
+    read_x(0);
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) {
       if constexpr (GRAD) {
-        // 8 rows x 16 columns transposed by each group of 16 lanes: lane 2 j, 2 j + 1
-        // point at row j's two 8-byte halves, lane c receives column c
         u32x4 h[2];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int row = 32 * q4 + 8 * t + (r16 >> 1);
-          const int chunk = (TN * wn) / 16 + ns;
-          const uint32_t off = (uint32_t)row * kBN + 16u * (uint32_t)(chunk ^ ((row & 7) | ((row >> 2) & 8))) +
-                               8u * (uint32_t)(r16 & 1);
           const i32x2 d = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (__attribute__((address_space(3))) i32x2*)(base + kX + off));
+              (__attribute__((address_space(3))) i32x2*)(base + (go ^ (16u * ns)) + 8 * kBN * t));
           h[t >> 1][2 * (t & 1)] = (uint32_t)d.x;
           h[t >> 1][2 * (t & 1) + 1] = (uint32_t)d.y;
         }
         wf[ns] = frag(h[0], h[1]);
       } else {
-        // MFMA row r of column tile ns is column 4 SN (r >> 2) + 4 ns + (r & 3): a
-        // lane's outputs are then 4 SN consecutive columns
-        const int row = TN * wn + 4 * SN * (r16 >> 2) + 4 * ns + (r16 & 3);
-        const int sz = ((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1;
-        const uint8_t* p = base + kX + row * kBlk;
-        wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4) ^ sz)),
-                      *reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4 + 1) ^ sz)));
+        const uint8_t* p = base + 4 * kBlk * ns;
+        wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + wo), *reinterpret_cast<const u32x4*>(p + (wo ^ 16u)));
       }
     }
+    // row tile ms + 1 is read and row tile ms - 1 scaled and added while the
+    // products of row tile ms are formed
+    f32x4 t[2][SN];
+    float sp = 0.0f;
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
-      const int row = TM * wm + 16 * ms + r16;
-      const uint8_t* p = base + row * kBlk;
-      const int sz = (row >> 1) & 7;
-      const i32x8 xf = frag(*reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4) ^ sz)),
-                            *reinterpret_cast<const u32x4*>(p + 16 * ((2 * q4 + 1) ^ sz)));
-      const float s = sc * *reinterpret_cast<const float*>(base + kX + kW + 4 * row);
-      f32x4 t[SN];
+      if (ms + 1 < MS) read_x(ms + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      const float s = sc * sx[ms & 1];
 #pragma unroll
-      for (int ns = 0; ns < SN; ++ns) t[ns] = block_product(wf[ns], xf);
+      for (int ns = 0; ns < SN; ++ns) t[ms & 1][ns] = block_product(wf[ns], xf[ms & 1]);
+      if (ms > 0) {
 #pragma unroll
-      for (int ns = 0; ns < SN; ++ns) add_scaled(acc[ms][ns], s, t[ns]);
+        for (int ns = 0; ns < SN; ++ns) add_scaled(acc[ms - 1][ns], sp, t[(ms - 1) & 1][ns]);
+      }
+      sp = s;
     }
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) add_scaled(acc[MS - 1][ns], sp, t[(MS - 1) & 1][ns]);
   };
 
   // stages j + 1 .. j + NS - 2 stay in flight over the wait for stage j
   constexpr int kPer = QW + NQX / kNW;   // loads of a stage, by any wave at least
-  auto sw_at = [&](int j) { return sw[(size_t)(cb0 + min(j, nc - 1)) * sw_step]; };
-  if (nc > 0) {
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s)
-      if (s < nc) issue(cb0 + s, s);
-    float sc = sw_at(0);
-    for (int j = 0; j < nc; ++j) {
-      if (j + NS - 2 < nc) wait_vm_barrier<(NS - 2) * kPer>();
-      else wait_vm_barrier<0>();
-      if (j + NS - 1 < nc) issue(cb0 + j + NS - 1, (j + NS - 1) % NS);
-      const float sn = sw_at(j + 1);
-      compute(j % NS, sc);
-      sc = sn;
-    }
+  for (int s = 0; s < NS - 1; ++s)
+    if (s < nc) issue(cb0 + s, s);
+  for (int j = 0; j < nc; ++j) {
+    if (j + NS - 2 < nc) wait_vm_barrier<(NS - 2) * kPer>();
+    else wait_vm_barrier<0>();
+    if (j + NS - 1 < nc) issue(cb0 + j + NS - 1, (j + NS - 1) % NS);
+    compute(j % NS);
   }
 
   // ---- epilogue

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
       const int q = wv + kNW * i;
       const int row = 8 * q + (lane >> 3);
       if (NQA % kNW == 0 || q < NQA)
-        dma16(ra, base + 1024 * q, (uint32_t)row * (uint32_t)Np * 2u + 16u * (uint32_t)((lane & 7) ^ ((row >> 1) & 7)),
+        dma16(ra, base + 1024 * q, (uint32_t)row * (uint32_t)Np * 2u + 16u * ((uint32_t)(lane & 7) ^ pair_swz((row >> 1) & 7)),
               so);
     }
     const int row = 8 * wv + (lane >> 3);
@@ -249,6 +249,8 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) acc[ms][ns] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // dY: row TM wm + 16 ms + r16, chunk 2 q4 + st
+  const uint32_t ao = (uint32_t)(TM * wm + r16) * (2 * kSt) + 16u * ((uint32_t)(2 * q4) ^ pair_swz(r16 >> 1));
   auto compute = [&](int stage) {
     const uint8_t* base = lds + stage * ST::kBytes;
     f16x8 wf[SN][2];
@@ -281,12 +283,10 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
     }
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
-      const int row = TM * wm + 16 * ms + r16;
-      const uint8_t* p = base + row * (2 * kSt);
-      const int sz = (row >> 1) & 7;
+      const uint8_t* p = base + 16 * 2 * kSt * ms;
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        const f16x8 xf = *reinterpret_cast<const f16x8*>(p + 16 * ((2 * q4 + st) ^ sz));
+        const f16x8 xf = *reinterpret_cast<const f16x8*>(p + (ao ^ (16u * (uint32_t)st)));
 #pragma unroll
         for (int ns = 0; ns < SN; ++ns)
           acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[ns][st], xf, acc[ms][ns], 0, 0, 0);

@@ -13,6 +13,8 @@
 // output columns of each tile: one product of scales per row tile and block
 // serves all of a wave's column tiles, and the outputs of a lane are
 // contiguous.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "tilemap.hpp"
@@ -196,7 +198,7 @@ struct Fp8Args {
 constexpr int kBN = 256;      // output columns per tile
 
 template <int BM>
-constexpr int fp8_stage_bytes() { return BM * kBlk + kBN * kBlk + BM * 4 + 128; }
+constexpr int fp8_stage_bytes() { return BM * kBlk + kBN * kBlk + ((BM + 63) / 64 + 1) * 256; }
 
 template <int BM, int WM, int NS, bool GRAD>
 __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
@@ -205,9 +207,10 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
   constexpr int MS = TM / 16, SN = TN / 16;
   constexpr int kX = BM * kBlk, kW = kBN * kBlk, kStage = fp8_stage_bytes<BM>();
   constexpr int NQX = BM / 8;                  // 1 KiB loads of X per stage
+  constexpr int kSX = (BM + 63) / 64;          // waves that load row scales
   constexpr int QX = (NQX + kNW - 1) / kNW;
   constexpr int QW = kBN / 8 / kNW;            // of W per wave
-  static_assert(TN <= kBlk && MS >= 1 && SN >= 1, "a wave's columns lie in one block");
+  static_assert(kSX < kNW && TN <= kBlk && MS >= 1 && SN >= 1, "a wave's columns lie in one block");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
   const int lane = threadIdx.x & 63;
@@ -233,56 +236,71 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
   const int Cb = C / kBlk, KB = a.K / kBlk, NB = (a.N + kBlk - 1) / kBlk;
   const int o0 = ot * kBN;
   const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tr.row0 * C, (uint32_t)tr.rows * (uint32_t)C);
-  const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.xs + (size_t)tr.row0 * Cb, (uint32_t)tr.rows * (uint32_t)Cb * 4u);
   const uint32_t wk = (uint32_t)a.K;
   const uint8_t* wg = a.w + (size_t)tr.wg * a.N * a.K;
   const __amdgpu_buffer_rsrc_t rw = GRAD ? make_rsrc(wg + o0, (uint32_t)a.N * wk - (uint32_t)o0)
                                          : make_rsrc(wg + (size_t)o0 * a.K, (uint32_t)min(kBN, O - o0) * wk);
-  // scales of the tile's two column blocks: for contraction block b, one dword
-  // each at ((first block) + i) * sw_col + b * sw_step (the second block of a last
-  // tile may be past the end: it reads zero, and its outputs are not stored)
-  const int sw_col = GRAD ? 1 : KB, sw_step = GRAD ? KB : 1;
-  const size_t sw0 = (size_t)tr.wg * NB * KB;
-  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.ws + sw0, (uint32_t)NB * (uint32_t)KB * 4u);
-
   const int cb0 = blockIdx.y * a.cps;
   const int nc = min(Cb, cb0 + a.cps) - cb0;
 
   // 16-byte chunks of an LDS row lie in slots by pair_swz of the row pair that a
   // fragment read sees (W: rows 4 SN (r >> 2) + (r & 3) are one read's)
-  auto issue = [&](int cb, int stage) {
+  // Part i of the loads of block cb: QX of X, QW of W, and the scales' own. Wave wv's load i
+  // fills the 1 KiB block wv + 8 i of X (8 rows each) and of W (8 columns; gradient:
+  // 4 rows): the lane offsets are those of i = 0 plus whole rows, added at each
+  // load (the opaque copies keep the sums from being held in registers).
+  constexpr int kParts = QX + QW;
+  uint32_t xb = (uint32_t)(8 * wv + (lane >> 3)) * (uint32_t)C +
+                16u * ((uint32_t)(lane & 7) ^ pair_swz((4 * (wv & 1)) | (lane >> 4)));
+  uint32_t wb, wb2 = 0;
+  if constexpr (GRAD) {
+    // slot of chunk c of row r: c ^ (r & 7 | (r & 32) / 4)
+    const uint32_t row = (uint32_t)(4 * wv + (lane >> 4)), c = (uint32_t)(lane & 15) ^ (row & 7u);
+    wb = row * wk + 16u * c;
+    wb2 = row * wk + 16u * (c ^ 8u);   // odd i: r & 32 set
+  } else {
+    const int row = 8 * wv + (lane >> 3);
+    wb = (uint32_t)row * wk +
+         16u * ((uint32_t)(lane & 7) ^ pair_swz(((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1));
+  }
+  static_assert(GRAD || (64 / (4 * SN)) % 4 == 0, "the slots of a wave's columns repeat every 64");
+  auto issue = [&](int cb, int stage, int i) {
     uint8_t* base = lds + stage * kStage;
     const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)cb * kBlk);
-    {
-      const int rr = lane >> 3;
-#pragma unroll
-      for (int i = 0; i < QX; ++i) {
-        const int q = wv + kNW * i;
-        const int row = 8 * q + rr;
-        if (NQX % kNW == 0 || q < NQX)
-          dma16(rx, base + 1024 * q, (uint32_t)row * (uint32_t)C + 16u * ((uint32_t)(lane & 7) ^ pair_swz((row >> 1) & 7)), so);
+    if (i < QX) {
+      if (NQX % kNW == 0 || wv + kNW * i < NQX) {
+        asm volatile("" : "+v"(xb));
+        dma16(rx, base + 1024 * (wv + kNW * i), xb + (uint32_t)(64 * i) * (uint32_t)C, so);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < QW; ++i) {
-      const int q = wv + kNW * i;
+    } else {
+      const int k = i - QX;
+      uint8_t* dst = base + kX + 1024 * (wv + kNW * k);
       if constexpr (GRAD) {
-        const int row = 4 * q + (lane >> 4);
-        const int sl = (lane & 15) ^ ((row & 7) | ((row >> 2) & 8));
-        dma16(rw, base + kX + 1024 * q, ((uint32_t)cb * kBlk + (uint32_t)row) * wk + 16u * (uint32_t)sl, 0u);
+        uint32_t& o = k & 1 ? wb2 : wb;
+        asm volatile("" : "+v"(o));
+        // (the whole offset is checked against the extent: the last row's end)
+        dma16(rw, dst, o + __builtin_amdgcn_readfirstlane(((uint32_t)cb * kBlk + 32u * (uint32_t)k) * wk), 0u);
       } else {
-        const int row = 8 * q + (lane >> 3);
-        const uint32_t sl = (uint32_t)(lane & 7) ^ pair_swz(((row >> 1) & 1) | ((row / (4 * SN)) & 3) << 1);
-        dma16(rw, base + kX + 1024 * q, (uint32_t)row * wk + 16u * sl, so);
+        asm volatile("" : "+v"(wb));
+        dma16(rw, dst, wb + (uint32_t)(64 * k) * wk, so);
       }
     }
-    const uint32_t sb = __builtin_amdgcn_readfirstlane((uint32_t)cb * 4u);
-    if (wv < (BM + 63) / 64) {
-      if (BM % 64 == 0 || 64 * wv + lane < BM)
-        dma4(rxs, base + kX + kW + 256 * wv, (uint32_t)(64 * wv + lane) * (uint32_t)Cb * 4u, sb);
-    }
-    if (wv == kNW - 1 && lane < kBN / kBlk)
-      dma4(rws, base + kX + kW + 4 * BM, ((uint32_t)(o0 / kBlk + lane) * (uint32_t)sw_col + (uint32_t)cb * (uint32_t)sw_step) * 4u, 0u);
+  };
+  // The scales: one dword per lane and wave. Waves below BM / 64 (at least one)
+  // take the row scales, the others all the same two column scales (lanes 0 and
+  // 1; an offset past every extent reads zero).
+  const bool sxw = wv < kSX;
+  const __amdgpu_buffer_rsrc_t rsc =
+      make_rsrc(sxw ? a.xs + (size_t)tr.row0 * Cb : a.ws + (size_t)tr.wg * NB * KB,
+                sxw ? (uint32_t)tr.rows * (uint32_t)Cb * 4u : (uint32_t)NB * (uint32_t)KB * 4u);
+  const int ob = o0 / kBlk + lane;
+  const uint32_t sv = sxw ? (uint32_t)(64 * wv + lane) * (uint32_t)Cb * 4u
+                          : (lane < kBN / kBlk && ob < (GRAD ? KB : NB)) ? (uint32_t)ob * (GRAD ? 4u : (uint32_t)KB * 4u)
+                                                                        : 0xFFFFFFF0u;
+  const uint32_t sstep = GRAD && !sxw ? (uint32_t)KB * 4u : 4u;
+  const uint32_t sdst = kX + kW + 256u * (uint32_t)min(wv, kSX);
+  auto issue_scales = [&](int cb, int stage) {
+    dma4(rsc, lds + stage * kStage + sdst, sv, __builtin_amdgcn_readfirstlane((uint32_t)cb * sstep));
   };
 
   f32x4 acc[MS][SN];
@@ -303,43 +321,54 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
   const uint32_t go = kX + (uint32_t)(32 * q4 + (r16 >> 1)) * kBN + 8u * (uint32_t)(r16 & 1) +
                       16u * (uint32_t)((TN * wn / 16) ^ ((r16 >> 1) | (q4 & 1) << 3));
   const uint32_t so_x = kX + kW + 4u * (uint32_t)(TM * wm + r16);
-  const uint32_t so_w = kX + kW + 4u * (uint32_t)BM + 4u * (uint32_t)(TN * wn / kBlk);
+  const uint32_t so_w = kX + kW + 256u * kSX + 4u * (uint32_t)(TN * wn / kBlk);
 
-  auto compute = [&](int stage) {
+  i32x8 wf[SN], xf[2];
+  float sx[2], sc = 0.0f;
+  auto read_x = [&](int stage, int ms) {
     const uint8_t* base = lds + stage * kStage;
-    i32x8 wf[SN], xf[2];
-    float sx[2];
-    auto read_x = [&](int ms) {
-      const uint8_t* p = base + 16 * kBlk * ms;
-      xf[ms & 1] = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
-      sx[ms & 1] = *reinterpret_cast<const float*>(base + so_x + 64 * ms);
-    };
-    const float sc = *reinterpret_cast<const float*>(base + so_w);
-    read_x(0);
+    const uint8_t* p = base + 16 * kBlk * ms;
+    xf[ms & 1] = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
+    sx[ms & 1] = *reinterpret_cast<const float*>(base + so_x + 64 * ms);
+  };
+  auto read_w = [&](int stage, int ns) {
+    const uint8_t* base = lds + stage * kStage;
+    if constexpr (GRAD) {
+      u32x4 h[2];
 #pragma unroll
-    for (int ns = 0; ns < SN; ++ns) {
-      if constexpr (GRAD) {
-        u32x4 h[2];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const i32x2 d = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (__attribute__((address_space(3))) i32x2*)(base + (go ^ (16u * ns)) + 8 * kBN * t));
-          h[t >> 1][2 * (t & 1)] = (uint32_t)d.x;
-          h[t >> 1][2 * (t & 1) + 1] = (uint32_t)d.y;
-        }
-        wf[ns] = frag(h[0], h[1]);
-      } else {
-        const uint8_t* p = base + 4 * kBlk * ns;
-        wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + wo), *reinterpret_cast<const u32x4*>(p + (wo ^ 16u)));
+      for (int t = 0; t < 4; ++t) {
+        const i32x2 d = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2*)(base + (go ^ (16u * ns)) + 8 * kBN * t));
+        h[t >> 1][2 * (t & 1)] = (uint32_t)d.x;
+        h[t >> 1][2 * (t & 1) + 1] = (uint32_t)d.y;
       }
+      wf[ns] = frag(h[0], h[1]);
+    } else {
+      const uint8_t* p = base + 4 * kBlk * ns;
+      wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + wo), *reinterpret_cast<const u32x4*>(p + (wo ^ 16u)));
     }
-    // row tile ms + 1 is read and row tile ms - 1 scaled and added while the
-    // products of row tile ms are formed
+  };
+
+  // One block. Row tile ms + 1 is read and row tile ms - 1 scaled and added while
+  // the products of row tile ms are formed. With AHEAD, block next is loaded into
+  // stage nstage, a few loads at each row tile: all of them at once would hold the
+  // waves up in the memory pipeline's queue before their first product.
+  constexpr int kPer = QW + NQX / kNW + 1;  // loads of a stage, by any wave at least
+  auto body = [&](auto AHEAD, int stage, int next, int nstage) {
     f32x4 t[2][SN];
     float sp = 0.0f;
+    if constexpr (AHEAD.value) issue_scales(next, nstage);
+    sc = *reinterpret_cast<const float*>(lds + stage * kStage + so_w);
+    read_x(stage, 0);
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) read_w(stage, ns);
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
-      if (ms + 1 < MS) read_x(ms + 1);
+      if (ms + 1 < MS) read_x(stage, ms + 1);
+      if constexpr (AHEAD.value) {
+#pragma unroll
+        for (int i = ms * kParts / MS; i < (ms + 1) * kParts / MS; ++i) issue(next, nstage, i);
+      }
       __builtin_amdgcn_sched_barrier(0);
       const float s = sc * sx[ms & 1];
 #pragma unroll
@@ -354,19 +383,56 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
     for (int ns = 0; ns < SN; ++ns) add_scaled(acc[MS - 1][ns], sp, t[(MS - 1) & 1][ns]);
   };
 
-  // stages j + 1 .. j + NS - 2 stay in flight over the wait for stage j
-  constexpr int kPer = QW + NQX / kNW;   // loads of a stage, by any wave at least
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s)
-    if (s < nc) issue(cb0 + s, s);
-  for (int j = 0; j < nc; ++j) {
-    if (j + NS - 2 < nc) wait_vm_barrier<(NS - 2) * kPer>();
-    else wait_vm_barrier<0>();
-    if (j + NS - 1 < nc) issue(cb0 + j + NS - 1, (j + NS - 1) % NS);
-    compute(j % NS);
+    if (s < nc) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) issue(cb0 + s, s, i);
+      issue_scales(cb0 + s, s);
+    }
+  int j = 0;
+  for (; j < nc - (NS - 1); ++j) {
+    wait_vm_barrier<(NS - 2) * kPer>();
+    body(std::true_type{}, j % NS, cb0 + j + NS - 1, (j + NS - 1) % NS);
+  }
+  for (; j < nc; ++j) {
+    wait_vm_barrier<0>();
+    body(std::false_type{}, j % NS, 0, 0);
   }
 
-  // ---- epilogue
+  // ---- epilogue: lane holds row 16 ms + r16 of the wave's, columns col(ns) .. + 3
+  auto col = [&](int ns) { return GRAD ? 16 * ns + 4 * q4 : 4 * SN * q4 + 4 * ns; };
+  const int ow = o0 + TN * wn;   // the wave's first column
+  if (a.part == nullptr && O % 8 == 0) {
+    // through LDS (free behind the barrier), so that whole runs of the output's
+    // rows are stored, 16 bytes per lane; 16-byte chunk c of a row lies in slot
+    // c ^ (row & mask)
+    constexpr int RB = TN * 2, NCH = RB / 16;   // bytes and chunks of a wave's row
+    static_assert(kNW * TM * RB <= NS * kStage, "the outputs fit the stages");
+    __syncthreads();
+    uint8_t* reg = lds + wv * (TM * RB);
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+      for (int ns = 0; ns < SN; ++ns) {
+        const int b = 2 * col(ns);
+        *reinterpret_cast<u32x2*>(reg + (16 * ms + r16) * RB + 16 * ((b >> 4) ^ (r16 & (NCH - 1))) + (b & 8)) =
+            u32x2{pack_bf16x2(acc[ms][ns].x, acc[ms][ns].y), pack_bf16x2(acc[ms][ns].z, acc[ms][ns].w)};
+      }
+    wave_lds_exchange();   // the rows below were written by other lanes
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + (size_t)tr.row0 * O, (uint32_t)tr.rows * (uint32_t)O * 2u);
+    constexpr int RI = 64 / NCH;   // rows per store
+    const int rr = lane / NCH, cc = lane % NCH;
+    const bool in = ow + 8 * cc < O;
+#pragma unroll
+    for (int i = 0; i < TM / RI; ++i) {
+      const int row = RI * i + rr;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(reg + row * RB + 16 * (cc ^ (row & (NCH - 1))));
+      // rows past the tile's last are past the extent (dropped)
+      if (in) st128(v, ry, ((uint32_t)(TM * wm + row) * (uint32_t)O + (uint32_t)(ow + 8 * cc)) * 2u);
+    }
+    return;
+  }
   const size_t part0 = ((size_t)blockIdx.y * a.M + tr.row0) * O;
 #pragma unroll
   for (int ms = 0; ms < MS; ++ms) {
@@ -376,23 +442,16 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
     float* pr = a.part == nullptr ? nullptr : a.part + part0 + (size_t)row * O;
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) {
-      const int c = o0 + TN * wn + (GRAD ? 16 * ns + 4 * q4 : 4 * SN * q4 + 4 * ns);
-      if (a.part != nullptr) {
-        if (O % 4 == 0 && c < O) {
-          *reinterpret_cast<f32x4*>(pr + c) = acc[ms][ns];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c + i < O) pr[c + i] = acc[ms][ns][i];
-        }
-      } else if (O % 4 == 0) {
-        if (c < O)
-          *reinterpret_cast<u32x2*>(yr + c) =
-              u32x2{pack_bf16x2(acc[ms][ns].x, acc[ms][ns].y), pack_bf16x2(acc[ms][ns].z, acc[ms][ns].w)};
+      const int c = ow + col(ns);
+      if (a.part != nullptr && O % 4 == 0) {
+        if (c < O) *reinterpret_cast<f32x4*>(pr + c) = acc[ms][ns];
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (c + i < O) yr[c + i] = to_bf16(acc[ms][ns][i]);
+          if (c + i < O) {
+            if (a.part != nullptr) pr[c + i] = acc[ms][ns][i];
+            else yr[c + i] = to_bf16(acc[ms][ns][i]);
+          }
       }
     }
   }

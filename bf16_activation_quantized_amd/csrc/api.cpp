@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include <stddef.h>
@@ -551,24 +552,68 @@ struct RowsPlan {
   int32_t sk;   // slices of the contraction
 };
 
-// Slices of the contraction (cb steps) where fewer than half of the compute
-// units have a tile: as far as one round of workgroups goes, while a slice
-// keeps at least four steps.
+// Estimated time of the tile kernels in us: `tiles` workgroups (one per compute
+// unit at a time) of `steps` contraction steps of `step_us`, and what a workgroup
+// costs besides (first loads, outputs). Past one round the last, partly filled
+// one counts in part: workgroups do not end together (1322 x 19456 x 2560: 2.08
+// rounds of 192 rows run like 2.4, 3.3 of 128 like 3.5).
+double rounds_us(double tiles, double steps, double step_us, double extra_us) {
+  const double r = tiles / device_cus();
+  const double eff = r <= 1.0 ? 1.0 : 0.4 * r + 0.6 * std::ceil(r);
+  return eff * (extra_us + steps * step_us);
+}
+
+// Partial sums of a split contraction, written and read, and the launch of the
+// reduce (777 x 9728 x 2560: 8, 10, 13 us for 2, 3, 4 slices of 8 MB).
+double split_us(int32_t sk, double outputs) { return sk > 1 ? 2.5 + 8.0 * sk * outputs / 6.0e6 : 0.0; }
+
+struct TileTime {
+  int bm;
+  double us;   // of one contraction step
+};
+
+// Least estimated time over the tile heights and (without groups) the splits
+// whose workgroups fit one round; `forced` > 0 fixes the height.
+template <size_t NT>
+RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
+                    int forced, int64_t min_steps) {
+  RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
+  double least = -1.0;
+  const int64_t ot = ceil_div(O, 256);
+  for (const TileTime& c : cands) {
+    if (forced > 0 && c.bm != forced) continue;
+    // grouped: each group's last tile is half full on average
+    const double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
+    for (int32_t sk = 1; sk <= 16; ++sk) {
+      if (sk > 1 && (G > 0 || mt * (double)(ot * sk) > device_cus() || ceil_div(steps, sk) < min_steps)) break;
+      const double us =
+          rounds_us(mt * (double)(ot * sk), (double)ceil_div(steps, sk), c.us, extra_us) + split_us(sk, (double)M * (double)O);
+      if (least < 0.0 || us < least * (1.0 - 1e-9)) {
+        least = us;
+        best = {c.bm, sk};
+      }
+    }
+  }
+  return best;
+}
+
+// One block of 128 of the 8-bit tile kernel by height, between what it takes
+// alone and with every compute unit busy (lower clocks): at 777 x 9728 x 2560 and
+// 8192^3 256 rows 1.42 and 1.78 us, 128 rows 0.93 and 1.04, 64 rows 0.70 and 0.63.
+constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.50}, {192, 1.33}, {160, 1.15}, {128, 0.99}, {96, 0.82}, {64, 0.66}};
+constexpr double kFp8ExtraUs = 6.0;
+
+// M rows of G groups (0: plain), O output columns, cb contraction blocks
+RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
+  const int64_t per = G > 0 ? ceil_div(M, G) : M;
+  if (forced == 16 || (forced == 0 && per <= 16 && !grad)) return {16, 1};
+  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4);
+}
+
 int32_t fill_split(int64_t tiles, int64_t cb) {
   int32_t sk = 1;
   while (sk < 16 && tiles * sk * 2 <= device_cus() && cb >= 8 * (int64_t)sk) sk <<= 1;
   return sk;
-}
-
-// M rows of G groups (0: plain), O output columns, cb contraction blocks
-RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb) {
-  const int64_t per = G > 0 ? ceil_div(M, G) : M;
-  RowsPlan p = {256, 1};
-  if (per <= 16 && !grad) p.bm = 16;
-  else if (per <= 64) p.bm = 64;
-  else if (per <= 128) p.bm = 128;
-  if (G == 0 && p.bm != 16) p.sk = fill_split(ceil_div(M, p.bm) * ceil_div(O, 256), cb);
-  return p;
 }
 
 w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
@@ -585,12 +630,10 @@ w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N,
 w4a16_status make_fp8_plan(bool grad, int64_t G, int64_t M, int64_t N, int64_t K, int32_t bm, int32_t sk, RowsPlan* p,
                            uint64_t* bytes) {
   const int64_t O = grad ? K : N, cb = (grad ? N : K) / kGroup;
-  *p = fp8_plan(grad, G, M, O, cb);
   if (bm != 0) {
-    if (bm != 64 && bm != 128 && bm != 256 && (bm != 16 || grad)) return W4A16_ERR_SHAPE;
-    p->bm = bm;
-    p->sk = 1;
+    if (!(bm == 64 || (bm >= 96 && bm <= 256 && bm % 32 == 0)) && (bm != 16 || grad)) return W4A16_ERR_SHAPE;
   }
+  *p = fp8_plan(grad, G, M, O, cb, bm);
   if (sk != 0) {
     if (sk < 1 || sk > 16 || (sk > 1 && (G > 0 || p->bm == 16))) return W4A16_ERR_SPLIT_K;
     p->sk = sk;

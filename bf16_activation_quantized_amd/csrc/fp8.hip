@@ -18,6 +18,7 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "tilemap.hpp"
+#include "tilestore.hpp"
 
 namespace w4a16 {
 
@@ -404,33 +405,10 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
   auto col = [&](int ns) { return GRAD ? 16 * ns + 4 * q4 : 4 * SN * q4 + 4 * ns; };
   const int ow = o0 + TN * wn;   // the wave's first column
   if (a.part == nullptr && O % 8 == 0) {
-    // through LDS (free behind the barrier), so that whole runs of the output's
-    // rows are stored, 16 bytes per lane; 16-byte chunk c of a row lies in slot
-    // c ^ (row & mask)
-    constexpr int RB = TN * 2, NCH = RB / 16;   // bytes and chunks of a wave's row
-    static_assert(kNW * TM * RB <= NS * kStage, "the outputs fit the stages");
+    static_assert(kNW * TM * TN * 2 <= NS * kStage, "the outputs fit the stages");
     __syncthreads();
-    uint8_t* reg = lds + wv * (TM * RB);
-#pragma unroll
-    for (int ms = 0; ms < MS; ++ms)
-#pragma unroll
-      for (int ns = 0; ns < SN; ++ns) {
-        const int b = 2 * col(ns);
-        *reinterpret_cast<u32x2*>(reg + (16 * ms + r16) * RB + 16 * ((b >> 4) ^ (r16 & (NCH - 1))) + (b & 8)) =
-            u32x2{pack_bf16x2(acc[ms][ns].x, acc[ms][ns].y), pack_bf16x2(acc[ms][ns].z, acc[ms][ns].w)};
-      }
-    wave_lds_exchange();   // the rows below were written by other lanes
     const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + (size_t)tr.row0 * O, (uint32_t)tr.rows * (uint32_t)O * 2u);
-    constexpr int RI = 64 / NCH;   // rows per store
-    const int rr = lane / NCH, cc = lane % NCH;
-    const bool in = ow + 8 * cc < O;
-#pragma unroll
-    for (int i = 0; i < TM / RI; ++i) {
-      const int row = RI * i + rr;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(reg + row * RB + 16 * (cc ^ (row & (NCH - 1))));
-      // rows past the tile's last are past the extent (dropped)
-      if (in) st128(v, ry, ((uint32_t)(TM * wm + row) * (uint32_t)O + (uint32_t)(ow + 8 * cc)) * 2u);
-    }
+    store_tile_bf16<TM, TN>(lds + wv * (TM * TN * 2), acc, col, ry, TM * wm, ow, O, lane);
     return;
   }
   const size_t part0 = ((size_t)blockIdx.y * a.M + tr.row0) * O;
@@ -565,25 +543,27 @@ static hipError_t launch_fp8_rows_t(Fp8Args a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// stages: three where they fit LDS, else two
+template <bool GRAD>
+static hipError_t launch_fp8_tile_bm(const Fp8Args& a, int sk, int bm, hipStream_t stream) {
+  switch (bm) {
+    case 256: return launch_fp8_tile_t<256, 2, 2, GRAD>(a, sk, stream);
+    case 224: return launch_fp8_tile_t<224, 2, 2, GRAD>(a, sk, stream);
+    case 192: return launch_fp8_tile_t<192, 2, 2, GRAD>(a, sk, stream);
+    case 160: return launch_fp8_tile_t<160, 2, 3, GRAD>(a, sk, stream);
+    case 128: return launch_fp8_tile_t<128, 2, 3, GRAD>(a, sk, stream);
+    case 96: return launch_fp8_tile_t<96, 2, 3, GRAD>(a, sk, stream);
+    case 64: return launch_fp8_tile_t<64, 1, 3, GRAD>(a, sk, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
 hipError_t launch_fp8_gemm(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, uint16_t* y,
                            float* part, const int32_t* m_sizes, int M, int N, int K, int G, bool grad, int cps, int sk,
                            int bm, hipStream_t stream) {
   const Fp8Args a = {x, xs, w, ws, y, part, m_sizes, M, N, K, G, cps, 0, 0};
   if (bm == 16 && !grad && sk == 1) return launch_fp8_rows_t<2>(a, stream);
-  if (grad) {
-    switch (bm) {
-      case 256: return launch_fp8_tile_t<256, 2, 2, true>(a, sk, stream);
-      case 128: return launch_fp8_tile_t<128, 2, 3, true>(a, sk, stream);
-      case 64: return launch_fp8_tile_t<64, 1, 3, true>(a, sk, stream);
-      default: return hipErrorInvalidValue;
-    }
-  }
-  switch (bm) {
-    case 256: return launch_fp8_tile_t<256, 2, 2, false>(a, sk, stream);
-    case 128: return launch_fp8_tile_t<128, 2, 3, false>(a, sk, stream);
-    case 64: return launch_fp8_tile_t<64, 1, 3, false>(a, sk, stream);
-    default: return hipErrorInvalidValue;
-  }
+  return grad ? launch_fp8_tile_bm<true>(a, sk, bm, stream) : launch_fp8_tile_bm<false>(a, sk, bm, stream);
 }
 
 }  // namespace w4a16

@@ -15,9 +15,13 @@
 // A prepass writes dY in fp16, the scales transposed to [k group, n] and their
 // largest magnitudes per 128 n; both are ordered (0 4 1 5 2 6 3 7) within 8 n,
 // the order in which a word of 8 nibbles unpacks into pairs.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "tilemap.hpp"
+#include "tilestore.hpp"
 
 namespace w4a16 {
 
@@ -199,36 +203,41 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
   // groups past the last column read zeros
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.st + ((size_t)tr.wg * Kg + g0) * Np, (uint32_t)(Kg - g0) * (uint32_t)Np * 2u);
 
-  auto issue = [&](int s, int stage) {
+  // Part i of the loads of stage s: QA of dY, one of the weights. Wave wv's load i
+  // fills the 1 KiB block wv + 8 i of dY (8 rows each) and block wv of the weights
+  // (8 n each); the opaque copies keep the sums from being held in registers.
+  // 16-byte chunks lie in the slots of pair_swz (dY) and of the row pair (weights).
+  constexpr int kParts = QA + 1;
+  const uint32_t AB = (uint32_t)Np * 2u;
+  uint32_t ab = (uint32_t)(8 * wv + (lane >> 3)) * AB + 16u * ((uint32_t)(lane & 7) ^ pair_swz((4 * (wv & 1)) | (lane >> 4)));
+  uint32_t wb = (uint32_t)(8 * wv + (lane >> 3)) * K2 +
+                16u * ((uint32_t)(lane & 7) ^ (uint32_t)((4 * (wv & 1)) | (lane >> 4)));
+  auto issue = [&](int s, int stage, int i) {
     uint8_t* base = lds + stage * ST::kBytes;
-    const uint32_t so = __builtin_amdgcn_readfirstlane((uint32_t)s * (2u * kSt));
-#pragma unroll
-    for (int i = 0; i < QA; ++i) {
-      const int q = wv + kNW * i;
-      const int row = 8 * q + (lane >> 3);
-      if (NQA % kNW == 0 || q < NQA)
-        dma16(ra, base + 1024 * q, (uint32_t)row * (uint32_t)Np * 2u + 16u * ((uint32_t)(lane & 7) ^ pair_swz((row >> 1) & 7)),
-              so);
+    if (i < QA) {
+      if (NQA % kNW == 0 || wv + kNW * i < NQA) {
+        asm volatile("" : "+v"(ab));
+        dma16(ra, base + 1024 * (wv + kNW * i), ab + (uint32_t)(64 * i) * AB,
+              __builtin_amdgcn_readfirstlane((uint32_t)s * (2u * kSt)));
+      }
+    } else {
+      asm volatile("" : "+v"(wb));
+      // (rows past N end past the extent, which checks the vector offset only)
+      dma16(rw, base + ST::kA + 1024 * wv, wb + __builtin_amdgcn_readfirstlane((uint32_t)s * kSt * K2), 0u);
     }
-    const int row = 8 * wv + (lane >> 3);
-    // (rows past N end past the extent, which checks the vector offset only)
-    dma16(rw, base + ST::kA + 1024 * wv,
-          ((uint32_t)s * kSt + (uint32_t)row) * K2 + 16u * (uint32_t)((lane & 7) ^ ((row >> 1) & 7)), 0u);
   };
-  // scale pair p of a stage: group p / 32, n pair p % 32
-  auto scale_word = [&](int s) {
-    return tid < SPT ? ld32(rs, ((uint32_t)(tid >> 5) * (uint32_t)Np + (uint32_t)s * kSt) * 2u + 4u * (uint32_t)(tid & 31))
-                     : 0u;
-  };
+  // Scales: pair p of a stage is n pair p % 32 of group p / 32; every thread takes
+  // pair tid % SPT (the same words several times rather than a branch).
+  const int sp = tid % SPT;
+  const uint32_t sb = ((uint32_t)(sp >> 5) * (uint32_t)Np + 2u * (uint32_t)(sp & 31)) * 2u;
+  auto scale_word = [&](int s) { return ld32(rs, sb, __builtin_amdgcn_readfirstlane((uint32_t)s * (2u * kSt))); };
   auto put_scales = [&](int stage, uint32_t v, int e) {
-    if (tid < SPT) {
-      uint8_t* p = lds + stage * ST::kBytes + ST::kA + ST::kW + 4 * tid;
-      const uint32_t h = f16_pair(bf16lo(v), bf16hi(v), e);
-      const f16x2 m24 = {(_Float16)-24.0f, (_Float16)-24.0f};
-      const f16x2 c = __builtin_bit_cast(f16x2, h) * m24;
-      *reinterpret_cast<uint32_t*>(p) = h;
-      *reinterpret_cast<uint32_t*>(p + ST::kS) = __builtin_bit_cast(uint32_t, c);
-    }
+    uint8_t* p = lds + stage * ST::kBytes + ST::kA + ST::kW + 4 * sp;
+    const uint32_t h = f16_pair(bf16lo(v), bf16hi(v), e);
+    const f16x2 m24 = {(_Float16)-24.0f, (_Float16)-24.0f};
+    const f16x2 c = __builtin_bit_cast(f16x2, h) * m24;
+    *reinterpret_cast<uint32_t*>(p) = h;
+    *reinterpret_cast<uint32_t*>(p + ST::kS) = __builtin_bit_cast(uint32_t, c);
   };
 
   // largest scale of each of the tile's groups over all n
@@ -241,7 +250,7 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
     if (lane == 0) gup[g] = up_by(top, 10);
   }
   __syncthreads();
-  const int sup = tid < SPT ? gup[tid >> 5] : 0;
+  const int sup = gup[sp >> 5];
 
   f32x4 acc[MS][SN];
 #pragma unroll
@@ -249,98 +258,146 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) acc[ms][ns] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  // ---- LDS operand offsets within a stage
   // dY: row TM wm + 16 ms + r16, chunk 2 q4 + st
   const uint32_t ao = (uint32_t)(TM * wm + r16) * (2 * kSt) + 16u * ((uint32_t)(2 * q4) ^ pair_swz(r16 >> 1));
-  auto compute = [&](int stage) {
-    const uint8_t* base = lds + stage * ST::kBytes;
-    f16x8 wf[SN][2];
+  // weights: lane r of a group of 16 points at 8 bytes (16 columns) of row 16 q4 +
+  // r and receives column r's 16 n
+  const uint32_t wo = ST::kA + (uint32_t)(16 * q4 + r16) * (kBN / 2);
+  // scales of n 16 q4 + 8 st .. + 7
+  const uint32_t so = ST::kA + ST::kW + 32u * (uint32_t)q4;
+
+  const uint32_t magic = vgpr_const(0x4C004C00u);   // a pair of 16
+  const uint32_t mask = __builtin_amdgcn_readfirstlane(vgpr_const(0x03C003C0u));
+  constexpr int NF = 2 * SN;    // weight fragments of a stage: st = f / SN, ns = f % SN
+  f16x8 wf[2][NF];              // of this stage and the next
+  i32x2 raw[SN];
+  u32x4 sc, cc;
+  f16x8 xf[2][2];
+  auto read_x = [&](int stage, int ms) {
+    const uint8_t* p = lds + stage * ST::kBytes + 16 * 2 * kSt * ms;
+    xf[ms & 1][0] = *reinterpret_cast<const f16x8*>(p + ao);
+    xf[ms & 1][1] = *reinterpret_cast<const f16x8*>(p + (ao ^ 16u));
+  };
+  auto read_raw = [&](int stage) {
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) {
-      const int row = 16 * q4 + r16, ct = (TN * wn) / 16 + ns;   // 8 bytes: 16 columns
-      const uint32_t off =
-          (uint32_t)row * (kBN / 2) + 16u * (uint32_t)((ct >> 1) ^ ((row >> 1) & 7)) + 8u * (uint32_t)(ct & 1);
-      const i32x2 d = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-          (__attribute__((address_space(3))) i32x2*)(base + ST::kA + off));
-      const int grp = (TN * wn + 16 * ns) / GS;
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const uint8_t* sp = base + ST::kA + ST::kW + (grp * kSt + 16 * q4 + 8 * st) * 2;
-        const u32x4 s = *reinterpret_cast<const u32x4*>(sp);
-        const u32x4 c = *reinterpret_cast<const u32x4*>(sp + ST::kS);
-        const uint32_t v = (uint32_t)(st == 0 ? d.x : d.y);
-        u32x4 o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // nibbles j and j + 4 to mantissa bits 6 .. 9 of the two halves of 16 + q
-          const uint32_t sh = j == 0 ? v << 6 : j == 1 ? v << 2 : j == 2 ? v >> 2 : v >> 6;
-          const uint32_t u = (sh & 0x03C003C0u) | 0x4C004C00u;
-          const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u), __builtin_bit_cast(f16x2, (uint32_t)s[j]),
-                                                    __builtin_bit_cast(f16x2, (uint32_t)c[j]));
-          o[j] = __builtin_bit_cast(uint32_t, r);
-        }
-        wf[ns][st] = __builtin_bit_cast(f16x8, o);
-      }
-    }
-#pragma unroll
-    for (int ms = 0; ms < MS; ++ms) {
-      const uint8_t* p = base + 16 * 2 * kSt * ms;
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        const f16x8 xf = *reinterpret_cast<const f16x8*>(p + (ao ^ (16u * (uint32_t)st)));
-#pragma unroll
-        for (int ns = 0; ns < SN; ++ns)
-          acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[ns][st], xf, acc[ms][ns], 0, 0, 0);
-      }
+      const int ct = (TN * wn) / 16 + ns;
+      raw[ns] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+          (__attribute__((address_space(3))) i32x2*)(lds + stage * ST::kBytes + wo +
+                                                     16u * (uint32_t)((ct >> 1) ^ (r16 >> 1)) + 8u * (uint32_t)(ct & 1)));
     }
   };
-
-  if (ns_ > 0) {
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) {
-      if (s < ns_) {
-        issue(s0 + s, s);
-        put_scales(s, scale_word(s0 + s), sup);
-      }
+  // fragment f of the raw weights: nibbles j and j + 4 of a word go to mantissa
+  // bits 6 .. 9 of the two halves of 16 + q
+  auto unpack = [&](int stage, int f, f16x8& out) {
+    const int st = f / SN, ns = f % SN;
+    if ((16 * ns) % GS == 0) {
+      const uint8_t* p = lds + stage * ST::kBytes + so + (TN * wn + 16 * ns) / GS * (2 * kSt) + 16 * st;
+      sc = *reinterpret_cast<const u32x4*>(p);
+      cc = *reinterpret_cast<const u32x4*>(p + ST::kS);
     }
-    for (int j = 0; j < ns_; ++j) {
-      wait_vm_barrier<0>();
-      const bool ahead = j + NS - 1 < ns_;
-      uint32_t sv = 0;
-      if (ahead) {
-        sv = scale_word(s0 + j + NS - 1);
-        issue(s0 + j + NS - 1, (j + NS - 1) % NS);
-      }
-      compute(j % NS);
-      if (ahead) put_scales((j + NS - 1) % NS, sv, sup);
+    const uint32_t v = (uint32_t)(st == 0 ? raw[ns].x : raw[ns].y);
+    u32x4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = and_or_sv(j == 0 ? v << 6 : j == 1 ? v << 2 : j == 2 ? v >> 2 : v >> 6, mask, magic);
+      const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u), __builtin_bit_cast(f16x2, (uint32_t)sc[j]),
+                                                __builtin_bit_cast(f16x2, (uint32_t)cc[j]));
+      o[j] = __builtin_bit_cast(uint32_t, r);
+    }
+    out = __builtin_bit_cast(f16x8, o);
+  };
+
+  // One stage: its products, from weights that are in registers, while the next
+  // stage's weights are unpacked, a fragment at each row tile, and the stage
+  // after that is loaded, a few loads at each row tile. Past the last stage the
+  // last one's loads are repeated, unused: one form of the loop keeps the
+  // registers where they are.
+  auto body = [&](auto P, int stage, int after, int next, int nstage) {
+    constexpr int p = P.value;
+    const uint32_t sv = scale_word(next);
+    read_raw(after);
+    read_x(stage, 0);
+#pragma unroll
+    for (int ms = 0; ms < MS; ++ms) {
+      if (ms + 1 < MS) read_x(stage, ms + 1);
+#pragma unroll
+      for (int i = ms * kParts / MS; i < (ms + 1) * kParts / MS; ++i) issue(next, nstage, i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int ns = 0; ns < SN; ++ns)
+          acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[p][st * SN + ns], xf[ms & 1][st], acc[ms][ns], 0, 0, 0);
+#pragma unroll
+      for (int f = ms * NF / MS; f < (ms + 1) * NF / MS; ++f) unpack(after, f, wf[1 - p][f]);
+    }
+    put_scales(nstage, sv, sup);
+    wait_vm_barrier<0>();
+  };
+
+  static_assert(NS == 3, "stages j, j + 1 (whose weights are unpacked) and j + 2 (being loaded)");
+  if (ns_ > 0) {
+    auto at = [&](int j) { return s0 + min(j, ns_ - 1); };
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t sv = scale_word(at(s));
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) issue(at(s), s, i);
+      put_scales(s, sv, sup);
+    }
+    wait_vm_barrier<0>();
+    read_raw(0);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) unpack(0, f, wf[0][f]);
+    int st = 0;   // the stage of j: j % 3
+    for (int j = 0; j < ns_; j += 2) {
+      const int a1 = st == 2 ? 0 : st + 1, a2 = a1 == 2 ? 0 : a1 + 1;
+      body(std::integral_constant<int, 0>{}, st, a1, at(j + 2), a2);
+      if (j + 1 >= ns_) break;
+      body(std::integral_constant<int, 1>{}, a1, a2, at(j + 3), st);
+      st = a2;
     }
   }
 
-  // ---- epilogue: lane holds row 16 ms + r16, columns 16 ns + 4 q4 + 0..3
+  // ---- epilogue: lane holds row 16 ms + r16 of the wave's, columns 16 ns + 4 q4 .. + 3
+  const int ow = o0 + TN * wn;
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms) {
+    const int row = TM * wm + 16 * ms + r16;
+    const int down = row < tr.rows ? -a.up[tr.row0 + row] : 0;
+#pragma unroll
+    for (int ns = 0; ns < SN; ++ns) {
+      const int e = down - gup[(TN * wn + 16 * ns) / GS];
+      acc[ms][ns] = f32x4{ldexpf(acc[ms][ns].x, e), ldexpf(acc[ms][ns].y, e), ldexpf(acc[ms][ns].z, e),
+                          ldexpf(acc[ms][ns].w, e)};
+    }
+  }
+  if (a.part == nullptr) {
+    __syncthreads();
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.dx + (size_t)tr.row0 * K, (uint32_t)tr.rows * (uint32_t)K * 2u);
+    store_tile_bf16<TM, TN>(lds + wv * (TM * TN * 2), acc, [&](int ns) { return 16 * ns + 4 * q4; }, ry, TM * wm, ow, K,
+                            lane);
+    return;
+  }
   const size_t part0 = ((size_t)blockIdx.y * a.M + tr.row0) * K;
 #pragma unroll
   for (int ms = 0; ms < MS; ++ms) {
     const int row = TM * wm + 16 * ms + r16;
     if (row >= tr.rows) continue;
-    const int down = -a.up[tr.row0 + row];
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) {
-      const int c = o0 + TN * wn + 16 * ns + 4 * q4;
-      if (c >= K) continue;
-      const int e = down - gup[(TN * wn + 16 * ns) / GS];
-      const f32x4 v = {ldexpf(acc[ms][ns].x, e), ldexpf(acc[ms][ns].y, e), ldexpf(acc[ms][ns].z, e),
-                       ldexpf(acc[ms][ns].w, e)};
-      if (a.part != nullptr)
-        *reinterpret_cast<f32x4*>(a.part + part0 + (size_t)row * K + c) = v;
-      else
-        *reinterpret_cast<u32x2*>(a.dx + (size_t)(tr.row0 + row) * K + c) =
-            u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)};
+      const int c = ow + 16 * ns + 4 * q4;
+      if (c < K) *reinterpret_cast<f32x4*>(a.part + part0 + (size_t)row * K + c) = acc[ms][ns];
     }
   }
 }
 
 template <int BM, int WM, int NS, int GS>
 static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
-  constexpr int lds_bytes = NS * GradStage<BM, GS>::kBytes;
+  // the stages, afterwards the outputs
+  constexpr int lds_bytes = std::max(NS * GradStage<BM, GS>::kBytes, BM * kBN * 2);
   static_assert(lds_bytes <= 159 * 1024, "LDS");
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t ea =
@@ -359,9 +416,9 @@ template <int GS>
 static hipError_t launch_w4_grad_gs(const GradArgs& a, int sk, int bm, hipStream_t stream) {
   switch (bm) {
     case 256: return launch_w4_grad_t<256, 2, 3, GS>(a, sk, stream);
-    case 128: return launch_w4_grad_t<128, 2, 4, GS>(a, sk, stream);
-    case 64: return launch_w4_grad_t<64, 1, 4, GS>(a, sk, stream);
-    case 16: return launch_w4_grad_t<16, 1, 4, GS>(a, sk, stream);
+    case 128: return launch_w4_grad_t<128, 2, 3, GS>(a, sk, stream);
+    case 64: return launch_w4_grad_t<64, 1, 3, GS>(a, sk, stream);
+    case 16: return launch_w4_grad_t<16, 1, 3, GS>(a, sk, stream);
     default: return hipErrorInvalidValue;
   }
 }

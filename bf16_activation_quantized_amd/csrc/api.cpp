@@ -694,7 +694,7 @@ w4a16_status make_w4_grad_plan(bool grouped, int32_t G, int64_t M, int64_t N, in
   const int64_t per = grouped ? ceil_div(M, G) : M;
   p->bm = per <= 16 ? 16 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
   if (bm != 0) {
-    if (bm != 16 && bm != 64 && bm != 128 && bm != 256) return W4A16_ERR_SHAPE;
+    if (bm != 16 && bm != 64 && !(bm >= 96 && bm <= 256 && bm % 32 == 0)) return W4A16_ERR_SHAPE;
     p->bm = bm;
   }
   p->sk = grouped ? 1 : fill_split(ceil_div(M, p->bm) * ceil_div(K, 256), (int64_t)np / 64);

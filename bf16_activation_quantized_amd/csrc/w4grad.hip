@@ -65,69 +65,99 @@ struct GradPrep {
   uint16_t* st;         // [G, Kg, Np] bf16 scales, zero past N
   uint16_t* tops;       // [G, Np / 128, Kg] bf16 bits of the largest finite magnitudes
   int M, N, Np, Kg, G;
-  int sblocks;          // workgroups per group of 128 n: ceil(Kg / 64)
+  int sblocks;          // workgroups per 128 n of the scales
 };
 
-// Workgroups 0 .. M - 1: a row of dY each; the others: 128 n x 64 k groups of
-// the scales of one expert.
-__global__ __launch_bounds__(256) void grad_prep_kernel(const GradPrep a) {
+// Workgroups 0 .. M - 1: a row of dY each, held in registers between its largest
+// magnitude and its conversion up to kPrepRegs x 4096 elements (read again past
+// that). The others: 128 n of the scales of one expert each; up to kPrepWide
+// groups they are one run of memory, read in 16-byte pieces, past that 64 groups
+// at a time are read by rows.
+constexpr int kPrepThreads = 512;
+constexpr int kPrepRegs = 5;
+constexpr int kPrepWide = 128;
+
+__global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep a) {
+  __shared__ __attribute__((aligned(16))) uint16_t tile[128 * kPrepWide];   // [n][k group]
   const int t = threadIdx.x;
   if ((int)blockIdx.x < a.M) {
-    __shared__ uint32_t part[4];
+    uint32_t* part = reinterpret_cast<uint32_t*>(tile);
     const int m = blockIdx.x;
     const u32x4* src = reinterpret_cast<const u32x4*>(a.dy + (size_t)m * a.N);
-    const int n8 = a.N / 8;
+    const int n8 = a.N / 8, p8 = a.Np / 8;
     uint32_t top = 0;
-    auto take = [&](uint32_t v) {
-      v &= 0x7FFFu;
-      if (v < 0x7F80u) top = max(top, v);
+    auto take = [&](u32x4 v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = v[i] & 0x7FFFu, hi = (v[i] >> 16) & 0x7FFFu;
+        top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      }
     };
-    for (int i = t; i < n8; i += 256) {
-      const u32x4 v = src[i];
-      take(v.x); take(v.x >> 16); take(v.y); take(v.y >> 16);
-      take(v.z); take(v.z >> 16); take(v.w); take(v.w >> 16);
+    u32x4 held[kPrepRegs];
+#pragma unroll
+    for (int i = 0; i < kPrepRegs; ++i) {
+      const int at = t + kPrepThreads * i;
+      held[i] = at < n8 ? src[at] : u32x4{0u, 0u, 0u, 0u};
     }
+#pragma unroll
+    for (int i = 0; i < kPrepRegs; ++i) take(held[i]);
+    for (int at = t + kPrepThreads * kPrepRegs; at < n8; at += kPrepThreads) take(src[at]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
     if ((t & 63) == 0) part[t >> 6] = top;
     __syncthreads();
-    top = max(max(part[0], part[1]), max(part[2], part[3]));
+#pragma unroll
+    for (int i = 0; i < kPrepThreads / 64; ++i) top = max(top, part[i]);
     const int e = up_by(top, 14);
     u32x4* dst = reinterpret_cast<u32x4*>(a.h + (size_t)m * a.Np);
-    for (int i = t; i < a.Np / 8; i += 256) {
-      const u32x4 v = i < n8 ? src[i] : u32x4{0u, 0u, 0u, 0u};
-      dst[i] = u32x4{f16_pair(bf16lo(v.x), bf16lo(v.z), e), f16_pair(bf16hi(v.x), bf16hi(v.z), e),
-                     f16_pair(bf16lo(v.y), bf16lo(v.w), e), f16_pair(bf16hi(v.y), bf16hi(v.w), e)};
+    auto put = [&](int at, u32x4 v) {
+      dst[at] = u32x4{f16_pair(bf16lo(v.x), bf16lo(v.z), e), f16_pair(bf16hi(v.x), bf16hi(v.z), e),
+                      f16_pair(bf16lo(v.y), bf16lo(v.w), e), f16_pair(bf16hi(v.y), bf16hi(v.w), e)};
+    };
+#pragma unroll
+    for (int i = 0; i < kPrepRegs; ++i) {
+      const int at = t + kPrepThreads * i;
+      if (at < p8) put(at, held[i]);
     }
+    for (int at = t + kPrepThreads * kPrepRegs; at < p8; at += kPrepThreads)
+      put(at, at < n8 ? src[at] : u32x4{0u, 0u, 0u, 0u});
     if (t == 0) a.up[m] = e;
     return;
   }
-  __shared__ uint16_t tile[128][65];   // [n][k group]
   int b = (int)blockIdx.x - a.M;
   const int kc = b % a.sblocks;
   b /= a.sblocks;
   const int chunks = a.Np / 128;
   const int nc = b % chunks, g = b / chunks;
-  for (int i = t; i < 128 * 64; i += 256) {
-    const int n = 128 * nc + (i >> 6), k = 64 * kc + (i & 63);
-    tile[i >> 6][i & 63] = (n < a.N && k < a.Kg) ? a.s[((size_t)g * a.N + n) * a.Kg + k] : (uint16_t)0;
+  const int n0 = 128 * nc, rows = min(128, a.N - n0);
+  const bool wide = a.Kg <= kPrepWide;
+  const int k0 = wide ? 0 : 64 * kc, kn = wide ? a.Kg : min(64, a.Kg - k0);   // groups of this workgroup
+  const uint16_t* src = a.s + ((size_t)g * a.N + n0) * a.Kg + k0;
+  if (wide) {
+    // (rows is a multiple of 8, so the run is one of 16 bytes and 16-byte aligned)
+    for (int i = t; i < rows * kn / 8; i += kPrepThreads)
+      reinterpret_cast<u32x4*>(tile)[i] = reinterpret_cast<const u32x4*>(src)[i];
+  } else {
+    for (int i = t; i < rows * 64; i += kPrepThreads)
+      if ((i & 63) < kn) tile[(i >> 6) * kn + (i & 63)] = src[(size_t)(i >> 6) * a.Kg + (i & 63)];
   }
   __syncthreads();
-  for (int i = t; i < 64 * 16; i += 256) {   // 8 n of one k group each
-    const int kk = i >> 4, k = 64 * kc + kk, n = 8 * (i & 15);
-    if (k >= a.Kg) continue;
-    uint32_t o[4];
+  for (int i = t; i < kn * 16; i += kPrepThreads) {   // 8 n of one group each; the group's 16 threads are neighbours
+    const int kk = i >> 4, n = 8 * (i & 15);
+    uint32_t o[4] = {0u, 0u, 0u, 0u}, top = 0;
+    if (n < rows) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = (uint32_t)tile[n + j][kk] | ((uint32_t)tile[n + j + 4][kk] << 16);
-    *reinterpret_cast<u32x4*>(a.st + ((size_t)g * a.Kg + k) * a.Np + 128 * nc + n) = u32x4{o[0], o[1], o[2], o[3]};
-  }
-  if (t < 64 && 64 * kc + t < a.Kg) {
-    uint32_t top = 0;
-    for (int n = 0; n < 128; ++n) {
-      const uint32_t v = tile[n][t] & 0x7FFFu;
-      if (v < 0x7F80u) top = max(top, v);
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = tile[(n + j) * kn + kk], hi = tile[(n + j + 4) * kn + kk];
+        o[j] = lo | (hi << 16);
+        const uint32_t ml = lo & 0x7FFFu, mh = hi & 0x7FFFu;
+        top = max(top, max(ml < 0x7F80u ? ml : 0u, mh < 0x7F80u ? mh : 0u));
+      }
     }
-    a.tops[((size_t)g * chunks + nc) * a.Kg + 64 * kc + t] = (uint16_t)top;
+    *reinterpret_cast<u32x4*>(a.st + ((size_t)g * a.Kg + k0 + kk) * a.Np + n0 + n) = u32x4{o[0], o[1], o[2], o[3]};
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if ((i & 15) == 0) a.tops[((size_t)g * chunks + nc) * a.Kg + k0 + kk] = (uint16_t)top;
   }
 }
 
@@ -416,6 +446,10 @@ template <int GS>
 static hipError_t launch_w4_grad_gs(const GradArgs& a, int sk, int bm, hipStream_t stream) {
   switch (bm) {
     case 256: return launch_w4_grad_t<256, 2, 3, GS>(a, sk, stream);
+    case 224: return launch_w4_grad_t<224, 2, 3, GS>(a, sk, stream);
+    case 192: return launch_w4_grad_t<192, 2, 3, GS>(a, sk, stream);
+    case 160: return launch_w4_grad_t<160, 2, 3, GS>(a, sk, stream);
+    case 96: return launch_w4_grad_t<96, 2, 3, GS>(a, sk, stream);
     case 128: return launch_w4_grad_t<128, 2, 3, GS>(a, sk, stream);
     case 64: return launch_w4_grad_t<64, 1, 3, GS>(a, sk, stream);
     case 16: return launch_w4_grad_t<16, 1, 3, GS>(a, sk, stream);
@@ -433,10 +467,10 @@ hipError_t launch_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* 
   pr.st = reinterpret_cast<uint16_t*>(ws + p.st);
   pr.tops = reinterpret_cast<uint16_t*>(ws + p.tops);
   pr.M = M; pr.N = N; pr.Np = Np; pr.Kg = Kg; pr.G = G;
-  pr.sblocks = (Kg + 63) / 64;
+  pr.sblocks = Kg <= kPrepWide ? 1 : (Kg + 63) / 64;
   const long long blocks = (long long)M + (long long)G * (Np / 128) * pr.sblocks;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(grad_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, pr);
+  hipLaunchKernelGGL(grad_prep_kernel, dim3((unsigned)blocks), dim3(kPrepThreads), 0, stream, pr);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   GradArgs a;

@@ -93,6 +93,45 @@ __device__ __forceinline__ uint32_t pair_swz(int p) {
   return (uint32_t)((p & 1) | ((p >> 1) & 2) | (((p << 1) ^ p) & 4));
 }
 
+// Transposing LDS reads. The builtins make the compiler wait for every LDS DMA in
+// flight before each read (it does not for ordinary reads of an LDS array), which
+// would end the overlap of loads and products, so these are written out, each
+// with its own wait: the outputs are complete when the block ends.
+__device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
+// 8-bit: each group of 16 lanes reads 8 rows of 16 bytes (lanes 2 j and 2 j + 1 at
+// the two halves of row j); lane c receives byte c of the 8 rows. Rows + 8 t of
+// 256 bytes for t = 0 .. 3, at two addresses.
+__device__ __forceinline__ void lds_tr8_rows(uint32_t a0, uint32_t a1, u32x2 (&d0)[4], u32x2 (&d1)[4]) {
+  asm volatile(
+      "ds_read_b64_tr_b8 %0, %8\n\tds_read_b64_tr_b8 %1, %8 offset:2048\n\t"
+      "ds_read_b64_tr_b8 %2, %8 offset:4096\n\tds_read_b64_tr_b8 %3, %8 offset:6144\n\t"
+      "ds_read_b64_tr_b8 %4, %9\n\tds_read_b64_tr_b8 %5, %9 offset:2048\n\t"
+      "ds_read_b64_tr_b8 %6, %9 offset:4096\n\tds_read_b64_tr_b8 %7, %9 offset:6144\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(d0[0]), "=&v"(d0[1]), "=&v"(d0[2]), "=&v"(d0[3]), "=&v"(d1[0]), "=&v"(d1[1]), "=&v"(d1[2]), "=&v"(d1[3])
+      : "v"(a0), "v"(a1)
+      : "memory");
+}
+// 4-bit: each group of 16 lanes reads 16 rows of 8 bytes, lane c receives nibble c
+// of the 16 rows. Two neighbouring pieces of 8 bytes.
+__device__ __forceinline__ void lds_tr4_pair(uint32_t a, u32x2& d0, u32x2& d1) {
+  asm volatile(
+      "ds_read_b64_tr_b4 %0, %2\n\tds_read_b64_tr_b4 %1, %2 offset:8\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(d0), "=&v"(d1)
+      : "v"(a)
+      : "memory");
+}
+__device__ __forceinline__ void lds_tr4_pairs(uint32_t a, uint32_t b, u32x2& d0, u32x2& d1, u32x2& d2, u32x2& d3) {
+  asm volatile(
+      "ds_read_b64_tr_b4 %0, %4\n\tds_read_b64_tr_b4 %1, %4 offset:8\n\t"
+      "ds_read_b64_tr_b4 %2, %5\n\tds_read_b64_tr_b4 %3, %5 offset:8\n\ts_waitcnt lgkmcnt(0)"
+      : "=&v"(d0), "=&v"(d1), "=&v"(d2), "=&v"(d3)
+      : "v"(a), "v"(b)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- bf16
 __device__ __forceinline__ float bf16lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }

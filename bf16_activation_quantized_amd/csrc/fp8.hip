@@ -332,21 +332,25 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
     xf[ms & 1] = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
     sx[ms & 1] = *reinterpret_cast<const float*>(base + so_x + 64 * ms);
   };
-  auto read_w = [&](int stage, int ns) {
+  auto read_w = [&](int stage) {
     const uint8_t* base = lds + stage * kStage;
     if constexpr (GRAD) {
-      u32x4 h[2];
+      static_assert(!GRAD || SN % 2 == 0, "column tiles are read by twos");
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const i32x2 d = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2*)(base + (go ^ (16u * ns)) + 8 * kBN * t));
-        h[t >> 1][2 * (t & 1)] = (uint32_t)d.x;
-        h[t >> 1][2 * (t & 1) + 1] = (uint32_t)d.y;
+      for (int ns = 0; ns < SN; ns += 2) {
+        u32x2 d[2][4];
+        lds_tr8_rows(lds_offset(base) + (go ^ (16u * ns)), lds_offset(base) + (go ^ (16u * ns + 16u)), d[0], d[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          wf[ns + i] = i32x8{(int)d[i][0].x, (int)d[i][0].y, (int)d[i][1].x, (int)d[i][1].y,
+                             (int)d[i][2].x, (int)d[i][2].y, (int)d[i][3].x, (int)d[i][3].y};
       }
-      wf[ns] = frag(h[0], h[1]);
     } else {
-      const uint8_t* p = base + 4 * kBlk * ns;
-      wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + wo), *reinterpret_cast<const u32x4*>(p + (wo ^ 16u)));
+#pragma unroll
+      for (int ns = 0; ns < SN; ++ns) {
+        const uint8_t* p = base + 4 * kBlk * ns;
+        wf[ns] = frag(*reinterpret_cast<const u32x4*>(p + wo), *reinterpret_cast<const u32x4*>(p + (wo ^ 16u)));
+      }
     }
   };
 
@@ -361,8 +365,7 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
     if constexpr (AHEAD.value) issue_scales(next, nstage);
     sc = *reinterpret_cast<const float*>(lds + stage * kStage + so_w);
     read_x(stage, 0);
-#pragma unroll
-    for (int ns = 0; ns < SN; ++ns) read_w(stage, ns);
+    read_w(stage);
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
       if (ms + 1 < MS) read_x(stage, ms + 1);

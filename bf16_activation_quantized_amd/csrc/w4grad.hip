@@ -27,7 +27,6 @@ namespace w4a16 {
 
 namespace {
 
-typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -301,7 +300,7 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
   const uint32_t mask = __builtin_amdgcn_readfirstlane(vgpr_const(0x03C003C0u));
   constexpr int NF = 2 * SN;    // weight fragments of a stage: st = f / SN, ns = f % SN
   f16x8 wf[2][NF];              // of this stage and the next
-  i32x2 raw[SN];
+  u32x2 raw[SN];
   u32x4 sc, cc;
   f16x8 xf[2][2];
   auto read_x = [&](int stage, int ms) {
@@ -310,13 +309,13 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
     xf[ms & 1][1] = *reinterpret_cast<const f16x8*>(p + (ao ^ 16u));
   };
   auto read_raw = [&](int stage) {
-#pragma unroll
-    for (int ns = 0; ns < SN; ++ns) {
-      const int ct = (TN * wn) / 16 + ns;
-      raw[ns] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-          (__attribute__((address_space(3))) i32x2*)(lds + stage * ST::kBytes + wo +
-                                                     16u * (uint32_t)((ct >> 1) ^ (r16 >> 1)) + 8u * (uint32_t)(ct & 1)));
-    }
+    static_assert(SN == 2 || SN == 4, "column tiles are read by twos");
+    constexpr int kPairs = SN / 2;
+    const uint32_t at = lds_offset(lds) + (uint32_t)(stage * ST::kBytes) + wo;
+    // 16-byte chunk TN wn / 32 + i of the row, slot chunk ^ (row pair)
+    const uint32_t slot = 16u * ((uint32_t)(TN * wn / 32) ^ (uint32_t)(r16 >> 1));
+    if constexpr (kPairs == 2) lds_tr4_pairs(at + slot, at + (slot ^ 16u), raw[0], raw[1], raw[2], raw[3]);
+    else lds_tr4_pair(at + slot, raw[0], raw[1]);
   };
   // fragment f of the raw weights: nibbles j and j + 4 of a word go to mantissa
   // bits 6 .. 9 of the two halves of 16 + q
@@ -327,7 +326,7 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
       sc = *reinterpret_cast<const u32x4*>(p);
       cc = *reinterpret_cast<const u32x4*>(p + ST::kS);
     }
-    const uint32_t v = (uint32_t)(st == 0 ? raw[ns].x : raw[ns].y);
+    const uint32_t v = st == 0 ? raw[ns].x : raw[ns].y;
     u32x4 o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -339,15 +338,20 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
     out = __builtin_bit_cast(f16x8, o);
   };
 
-  // One stage: its products, from weights that are in registers, while the next
-  // stage's weights are unpacked, a fragment at each row tile, and the stage
-  // after that is loaded, a few loads at each row tile. Past the last stage the
+  // One stage j: its products, from weights that are in registers, while stage j +
+  // 1's weights are unpacked, a fragment at each row tile, and stage j + NS - 1 is
+  // loaded, a few loads at each row tile. Its scales were requested kAhead stages
+  // earlier: waiting for a load waits for all that was issued before it, which
+  // should be no more than the barrier waits for anyway. Past the last stage the
   // last one's loads are repeated, unused: one form of the loop keeps the
   // registers where they are.
-  auto body = [&](auto P, int stage, int after, int next, int nstage) {
-    constexpr int p = P.value;
-    const uint32_t sv = scale_word(next);
-    read_raw(after);
+  constexpr int kPer = NQA / kNW + 2;   // loads issued per stage, by any wave at least
+  // (kAhead stages are unrolled: a register with a load in flight cannot be moved)
+  constexpr int kAhead = NS > 5 ? 4 : 2;
+  static_assert(kAhead >= NS - 4, "stages in flight");
+  uint32_t sv[kAhead];                  // the scales of stages j + NS - 1 .. j + NS + kAhead - 2
+  auto body = [&](auto P, int stage, int after, int next, int word, int nstage) {
+    constexpr int p = P.value & 1;
     read_x(stage, 0);
 #pragma unroll
     for (int ms = 0; ms < MS; ++ms) {
@@ -360,35 +364,50 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
 #pragma unroll
         for (int ns = 0; ns < SN; ++ns)
           acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[p][st * SN + ns], xf[ms & 1][st], acc[ms][ns], 0, 0, 0);
+      if (ms == 0) read_raw(after);   // (it waits, behind the first products)
 #pragma unroll
       for (int f = ms * NF / MS; f < (ms + 1) * NF / MS; ++f) unpack(after, f, wf[1 - p][f]);
     }
-    put_scales(nstage, sv, sup);
-    wait_vm_barrier<0>();
+    put_scales(nstage, sv[P.value], sup);
+    sv[P.value] = scale_word(word);
+    wait_vm_barrier<(NS - 3) * kPer>();   // stage j + 2 has landed
   };
 
-  static_assert(NS == 3, "stages j, j + 1 (whose weights are unpacked) and j + 2 (being loaded)");
+  static_assert(NS >= 3, "stages j, j + 1 (whose weights are unpacked) and j + 2 (being loaded)");
   if (ns_ > 0) {
     auto at = [&](int j) { return s0 + min(j, ns_ - 1); };
+    uint32_t first[NS - 1];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const uint32_t sv = scale_word(at(s));
+    for (int s = 0; s < NS - 1; ++s) first[s] = scale_word(at(s));
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) sv[i] = scale_word(at(NS - 1 + i));
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) issue(at(s), s, i);
-      put_scales(s, sv, sup);
     }
-    wait_vm_barrier<0>();
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) put_scales(s, first[s], sup);
+    wait_vm_barrier<(NS - 3) * (kPer - 1)>();
     read_raw(0);
 #pragma unroll
     for (int f = 0; f < NF; ++f) unpack(0, f, wf[0][f]);
-    int st = 0;   // the stage of j: j % 3
-    for (int j = 0; j < ns_; j += 2) {
-      const int a1 = st == 2 ? 0 : st + 1, a2 = a1 == 2 ? 0 : a1 + 1;
-      body(std::integral_constant<int, 0>{}, st, a1, at(j + 2), a2);
-      if (j + 1 >= ns_) break;
-      body(std::integral_constant<int, 1>{}, a1, a2, at(j + 3), st);
-      st = a2;
+    auto inc = [](int s, int by) { return s + by >= NS ? s + by - NS : s + by; };
+    int st = 0, j = 0;   // st = j % NS
+    auto step = [&](auto P) {
+      body(P, st, inc(st, 1), at(j + NS - 1), at(j + NS - 1 + kAhead), inc(st, NS - 1));
+      st = inc(st, 1);
+      return ++j >= ns_;
+    };
+    for (;;) {
+      if (step(std::integral_constant<int, 0>{})) break;
+      if (step(std::integral_constant<int, 1>{})) break;
+      if constexpr (kAhead == 4) {
+        if (step(std::integral_constant<int, 2>{})) break;
+        if (step(std::integral_constant<int, 3>{})) break;
+      }
     }
+    wait_vm_barrier<0>();   // the repeated loads: LDS is used again below
   }
 
   // ---- epilogue: lane holds row 16 ms + r16 of the wave's, columns 16 ns + 4 q4 .. + 3
@@ -442,17 +461,18 @@ static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// stages: as many as LDS takes, up to 8
 template <int GS>
 static hipError_t launch_w4_grad_gs(const GradArgs& a, int sk, int bm, hipStream_t stream) {
   switch (bm) {
     case 256: return launch_w4_grad_t<256, 2, 3, GS>(a, sk, stream);
-    case 224: return launch_w4_grad_t<224, 2, 3, GS>(a, sk, stream);
-    case 192: return launch_w4_grad_t<192, 2, 3, GS>(a, sk, stream);
-    case 160: return launch_w4_grad_t<160, 2, 3, GS>(a, sk, stream);
-    case 96: return launch_w4_grad_t<96, 2, 3, GS>(a, sk, stream);
-    case 128: return launch_w4_grad_t<128, 2, 3, GS>(a, sk, stream);
-    case 64: return launch_w4_grad_t<64, 1, 3, GS>(a, sk, stream);
-    case 16: return launch_w4_grad_t<16, 1, 3, GS>(a, sk, stream);
+    case 224: return launch_w4_grad_t<224, 2, 4, GS>(a, sk, stream);
+    case 192: return launch_w4_grad_t<192, 2, 4, GS>(a, sk, stream);
+    case 160: return launch_w4_grad_t<160, 2, 5, GS>(a, sk, stream);
+    case 128: return launch_w4_grad_t<128, 2, 6, GS>(a, sk, stream);
+    case 96: return launch_w4_grad_t<96, 2, 6, GS>(a, sk, stream);
+    case 64: return launch_w4_grad_t<64, 1, 8, GS>(a, sk, stream);
+    case 16: return launch_w4_grad_t<16, 1, 8, GS>(a, sk, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -610,12 +610,6 @@ RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int fo
   return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4);
 }
 
-int32_t fill_split(int64_t tiles, int64_t cb) {
-  int32_t sk = 1;
-  while (sk < 16 && tiles * sk * 2 <= device_cus() && cb >= 8 * (int64_t)sk) sk <<= 1;
-  return sk;
-}
-
 w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
   if (G < 1 || (!grouped && G != 1)) return W4A16_ERR_SHAPE;
   if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return W4A16_ERR_SHAPE;
@@ -631,7 +625,9 @@ w4a16_status make_fp8_plan(bool grad, int64_t G, int64_t M, int64_t N, int64_t K
                            uint64_t* bytes) {
   const int64_t O = grad ? K : N, cb = (grad ? N : K) / kGroup;
   if (bm != 0) {
-    if (!(bm == 64 || (bm >= 96 && bm <= 256 && bm % 32 == 0)) && (bm != 16 || grad)) return W4A16_ERR_SHAPE;
+    bool built = bm == 16 && !grad;
+    for (const TileTime& c : kFp8Times) built = built || c.bm == bm;
+    if (!built) return W4A16_ERR_SHAPE;
   }
   *p = fp8_plan(grad, G, M, O, cb, bm);
   if (sk != 0) {
@@ -676,6 +672,13 @@ w4a16_status run_fp8(bool grad, const uint8_t* x, const float* xs, const uint8_t
 }
 
 // ---- input gradient of the 4-bit products
+// One stage of 64 n by height, as for the 8-bit tiles (at 8192^3: 256 rows 1.66
+// us, 192 rows 1.29, 128 rows 0.87, 64 rows 0.56; below that each stage's chain of
+// LDS reads and its barrier).
+constexpr TileTime kW4GradTimes[] = {{256, 1.62}, {224, 1.43}, {192, 1.22}, {160, 1.05}, {128, 0.85},
+                                     {96, 0.70},  {64, 0.55},  {32, 0.50},  {16, 0.46}};
+constexpr double kW4GradExtraUs = 6.0;
+
 w4a16_status check_w4_grad(bool grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size) {
   if (G < 1 || (!grouped && G != 1)) return W4A16_ERR_SHAPE;
   const w4a16_status st = check_dims(M, N, K, group_size);
@@ -691,13 +694,14 @@ w4a16_status check_w4_grad(bool grouped, int32_t G, int64_t M, int64_t N, int64_
 w4a16_status make_w4_grad_plan(bool grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size,
                                int32_t bm, int32_t sk, w4a16::W4GradPlan* p) {
   const uint64_t np = (uint64_t)w4a16::w4_grad_padded(N), kg = (uint64_t)(K / group_size);
-  const int64_t per = grouped ? ceil_div(M, G) : M;
-  p->bm = per <= 16 ? 16 : per <= 64 ? 64 : per <= 128 ? 128 : 256;
   if (bm != 0) {
-    if (bm != 16 && bm != 64 && !(bm >= 96 && bm <= 256 && bm % 32 == 0)) return W4A16_ERR_SHAPE;
-    p->bm = bm;
+    bool built = false;
+    for (const TileTime& c : kW4GradTimes) built = built || c.bm == bm;
+    if (!built) return W4A16_ERR_SHAPE;
   }
-  p->sk = grouped ? 1 : fill_split(ceil_div(M, p->bm) * ceil_div(K, 256), (int64_t)np / 64);
+  const RowsPlan r = plan_tiles(kW4GradTimes, kW4GradExtraUs, grouped ? G : 0, M, K, (int64_t)np / 64, bm, 8);
+  p->bm = r.bm;
+  p->sk = r.sk;
   if (sk != 0) {
     if (sk < 1 || sk > 16 || (sk > 1 && grouped)) return W4A16_ERR_SPLIT_K;
     p->sk = sk;

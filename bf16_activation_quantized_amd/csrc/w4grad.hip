@@ -461,17 +461,22 @@ static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// stages: as many as LDS takes, up to 8
+// Stages: as many as LDS takes, up to 8. One row of waves (each unpacks the
+// weights of its own 32 columns only) against two: 128 rows 986 against 1090 us at
+// 8192^3, 192 rows 970 against 997; at 256 rows, where each wave then reads every
+// row of dY, 946 against 924 (group 32, where two rows of waves leave registers
+// short, 959 against 956).
 template <int GS>
 static hipError_t launch_w4_grad_gs(const GradArgs& a, int sk, int bm, hipStream_t stream) {
   switch (bm) {
-    case 256: return launch_w4_grad_t<256, 2, 3, GS>(a, sk, stream);
-    case 224: return launch_w4_grad_t<224, 2, 4, GS>(a, sk, stream);
-    case 192: return launch_w4_grad_t<192, 2, 4, GS>(a, sk, stream);
-    case 160: return launch_w4_grad_t<160, 2, 5, GS>(a, sk, stream);
-    case 128: return launch_w4_grad_t<128, 2, 6, GS>(a, sk, stream);
-    case 96: return launch_w4_grad_t<96, 2, 6, GS>(a, sk, stream);
+    case 256: return launch_w4_grad_t<256, GS == 128 ? 2 : 1, 3, GS>(a, sk, stream);
+    case 224: return launch_w4_grad_t<224, 1, 4, GS>(a, sk, stream);
+    case 192: return launch_w4_grad_t<192, 1, 4, GS>(a, sk, stream);
+    case 160: return launch_w4_grad_t<160, 1, 5, GS>(a, sk, stream);
+    case 128: return launch_w4_grad_t<128, 1, 6, GS>(a, sk, stream);
+    case 96: return launch_w4_grad_t<96, 1, 6, GS>(a, sk, stream);
     case 64: return launch_w4_grad_t<64, 1, 8, GS>(a, sk, stream);
+    case 32: return launch_w4_grad_t<32, 1, 8, GS>(a, sk, stream);
     case 16: return launch_w4_grad_t<16, 1, 8, GS>(a, sk, stream);
     default: return hipErrorInvalidValue;
   }

@@ -666,7 +666,7 @@ w4a16_status run_fp8(bool grad, const uint8_t* x, const float* xs, const uint8_t
   hipStream_t strm = reinterpret_cast<hipStream_t>(stream);
   const hipError_t e =
       w4a16::launch_fp8_gemm(x, xs, w, ws, y, p.sk > 1 ? workspace : nullptr, m_sizes, (int)M, (int)N, (int)K, G,
-                             grad, (int)ceil_div(cb, p.sk), p.sk, p.bm, strm);
+                             grad, (int)ceil_div(cb, p.sk), p.sk, p.bm, device_cus(), strm);
   if (e != hipSuccess || p.sk == 1) return launched(e);
   return launched(w4a16::launch_splitk_reduce(workspace, y, (uint64_t)M * (uint64_t)O, p.sk, strm));
 }

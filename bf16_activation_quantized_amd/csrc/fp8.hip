@@ -439,82 +439,166 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 16 rows (of one expert): the weights stream from memory straight into
-// the MFMA's operand registers, each once; the 8 waves of a workgroup take
-// every eighth contraction block of the same 16 NT columns and add their sums
-// through LDS, in wave order.
+// Up to 16 rows: the weights stream from memory straight into the MFMA's operand
+// registers, each once; the 8 waves of a workgroup take every eighth contraction
+// block of the same 16 NT columns and add their sums through LDS, in wave order. A
+// workgroup takes column tiles gridDim.x apart, and each wave's blocks of all of
+// them are one sequence, with U blocks in flight throughout. XL: the rows and
+// their scales lie in LDS, loaded once per workgroup (from L2 they would cost as
+// much traffic as the weights, and every workgroup asks for the same lines).
 template <int NT>
+constexpr int kRowsSums = 2 * kNW * NT * 256 * 4;   // bytes of the sums, two buffers
+
+// bytes of R rows in LDS, in whole loads of 1 KiB
+__host__ __device__ constexpr uint32_t rows_xl_bytes(int R, int K) {
+  return ((uint32_t)R * (uint32_t)K + 1023u) & ~1023u;
+}
+
+template <int NT, int U, bool GROUPED, bool XL>
 __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
-  constexpr int U = 4;   // blocks in flight
-  __shared__ __attribute__((aligned(16))) float sums[kNW][NT][256];
+  constexpr int TC = 16 * NT;
+  constexpr int kSum = NT * 256;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  float* const sums = reinterpret_cast<float*>(lds);                       // [2][kNW][kSum]
+  uint8_t* const xl = lds + kRowsSums<NT>;                                 // [KB][R][128 B]
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
 
-  int mt, ot;
-  TileRows tr;
-  if (a.m_sizes != nullptr) {
+  TileRows tr{0, 16 * (int)blockIdx.y, min(16, a.M - 16 * (int)blockIdx.y)};
+  int first = blockIdx.x, step = gridDim.x, end = a.otiles;
+  if constexpr (GROUPED) {
     const GroupScan gs(a.m_sizes, a.G, a.M, 16);
     const int nblocks = gs.tiles * a.otiles;
     if ((int)blockIdx.x >= nblocks) return;
+    int mt, ot;
     tile_coords(blockIdx.x, nblocks, gs.tiles, a.otiles, &mt, &ot);
     tr = gs.find(mt);
-  } else {
-    ot = blockIdx.x % a.otiles;
-    mt = blockIdx.x / a.otiles;
-    tr = TileRows{0, mt * 16, min(16, a.M - mt * 16)};
+    if (tr.rows <= 0) return;
+    first = ot;
+    step = a.otiles;   // one tile
   }
-  if (tr.rows <= 0) return;
   const int K = a.K, KB = K / kBlk, NB = (a.N + kBlk - 1) / kBlk;
-  const int o0 = ot * 16 * NT;
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tr.row0 * K, (uint32_t)tr.rows * (uint32_t)K);
+  const uint8_t* wg = a.w + (size_t)tr.wg * a.N * K;
   const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.xs + (size_t)tr.row0 * KB, (uint32_t)tr.rows * (uint32_t)KB * 4u);
-  const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(a.w + ((size_t)tr.wg * a.N + o0) * K, (uint32_t)min(16 * NT, a.N - o0) * (uint32_t)K);
-  // 16 NT divides 128: the columns lie in one block
-  const float* sw = a.ws + ((size_t)tr.wg * NB + o0 / kBlk) * KB;
+  const __amdgpu_buffer_rsrc_t rws = make_rsrc(a.ws + (size_t)tr.wg * NB * KB, (uint32_t)NB * (uint32_t)KB * 4u);
   const uint32_t roff = (uint32_t)r16 * (uint32_t)K + 32u * (uint32_t)q4;
+
+  const int nb = (KB + kNW - 1) / kNW;                      // blocks of a wave and tile
+  const int tiles = first < end ? (end - first + step - 1) / step : 0;
+  const int total = tiles * nb;
+
+  const int R = tr.rows;
+  float* const sl = reinterpret_cast<float*>(xl + rows_xl_bytes(R, K));     // [KB][R] row scales
+  if constexpr (XL) {
+    // row r of block b: 16-byte chunk c in slot c ^ pair_swz(r / 2). The workgroups
+    // of an XCD begin at different places: all read the same lines.
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tr.row0 * K, (uint32_t)R * (uint32_t)K);
+    const int chunks = R * KB * 8, n = (chunks + 64 * kNW - 1) / (64 * kNW);
+    int at = (int)(blockIdx.x / kNumXcd) % n;
+    for (int k = 0; k < n; ++k) {
+      const int i0 = 64 * (kNW * at + wv), i = i0 + lane;
+      const int row = (i >> 3) % R, b = (i >> 3) / R;
+      const uint32_t c = (uint32_t)(i & 7) ^ pair_swz(row >> 1);
+      if (i0 < chunks)
+        dma16(rx, xl + 16 * i0, i < chunks ? (uint32_t)row * (uint32_t)K + (uint32_t)b * kBlk + 16u * c : 0xFFFFFFF0u,
+              0u);
+      if (++at == n) at = 0;
+    }
+    for (int i = threadIdx.x; i < R * KB; i += 64 * kNW) sl[i] = a.xs[(size_t)(tr.row0 + i % R) * KB + i / R];
+  }
+
+  u32x4 wr[U][NT][2], xr[XL ? 1 : U][2];
+  uint32_t sx[XL ? 1 : U], sc[U];
+  // the next block to load: tile lt, block lu of it
+  int lt = first, lu = 0;
+  auto load = [&](int u) {
+    const int b = wv + kNW * lu;
+    // a wave's last block may be past the end: extents of zero, so that nothing is
+    // read and the products are zero
+    const bool in = b < KB && lt < end;
+    const int o0 = lt * TC;
+    const __amdgpu_buffer_rsrc_t rw =
+        make_rsrc(wg + (size_t)o0 * K, in ? (uint32_t)min(TC, a.N - o0) * (uint32_t)K : 0u);
+    const uint32_t so = (uint32_t)b * kBlk;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      wr[u][t][0] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K, so);
+      wr[u][t][1] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K + 16u, so);
+    }
+    if constexpr (!XL) {
+      const __amdgpu_buffer_rsrc_t rx =
+          make_rsrc(a.x + (size_t)tr.row0 * K, in ? (uint32_t)tr.rows * (uint32_t)K : 0u);
+      xr[u][0] = ld128(rx, roff, so);
+      xr[u][1] = ld128(rx, roff + 16u, so);
+      sx[u] = ld32(rxs, (uint32_t)r16 * (uint32_t)KB * 4u, (uint32_t)min(b, KB - 1) * 4u);
+    }
+    // TC divides 128: the tile's columns lie in one block
+    sc[u] = ld32(rws, 0u, __builtin_amdgcn_readfirstlane(((uint32_t)(o0 / kBlk) * (uint32_t)KB + (uint32_t)b) * 4u));
+    if (++lu == nb) {
+      lu = 0;
+      lt += step;
+    }
+  };
 
   f32x4 acc[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b0 = wv; b0 < KB; b0 += kNW * U) {
-    u32x4 wr[U][NT][2], xr[U][2];
-    float sx[U], sc[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) load(u);
+  if constexpr (XL) wait_vm_barrier<U * (2 * NT + 1)>();
+  const int xrow = min(r16, R - 1);   // (rows past the last repeat it: not stored)
+  const uint32_t xo = (uint32_t)xrow * kBlk + 16u * ((uint32_t)(2 * q4) ^ pair_swz(xrow >> 1));
+  int ct = first, cu = 0, buf = 0;   // the block to compute
+  for (int s = 0; s < total; s += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int b = b0 + kNW * u;
-      if (b >= KB) break;
-      const uint32_t so = (uint32_t)b * kBlk;
+      if (s + u >= total) break;
+      const int b = wv + kNW * cu;
+      i32x8 xf;
+      float f;
+      if constexpr (XL) {
+        const int bx = min(b, KB - 1);
+        const uint8_t* p = xl + bx * R * kBlk;
+        xf = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
+        f = sl[bx * R + xrow];
+      } else {
+        xf = frag(xr[u][0], xr[u][1]);
+        f = __uint_as_float(sx[u]);
+      }
+      // (a block past the end: its weights read zero)
+      f = b < KB ? f * __uint_as_float(sc[u]) : 0.0f;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        wr[u][t][0] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K, so);
-        wr[u][t][1] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K + 16u, so);
+        const f32x4 p = block_product(frag(wr[u][t][0], wr[u][t][1]), xf);
+        if (b < KB) add_scaled(acc[t], f, p);
       }
-      xr[u][0] = ld128(rx, roff, so);
-      xr[u][1] = ld128(rx, roff + 16u, so);
-      sx[u] = __uint_as_float(ld32(rxs, (uint32_t)r16 * (uint32_t)KB * 4u, (uint32_t)b * 4u));
-      sc[u] = sw[b];
+      load(u);
+      if (++cu == nb) {
+        // ---- the tile's sums
+        float* sm = sums + buf * kNW * kSum;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          *reinterpret_cast<f32x4*>(sm + wv * kSum + t * 256 + r16 * 16 + 4 * q4) = acc[t];
+          acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        // (the loads in flight are not waited for; the other buffer's readers are
+        // past this barrier before it is written again)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const int o0 = ct * TC;
+        for (int e = threadIdx.x; e < kSum; e += 64 * kNW) {
+          const int row = e / TC, c = e % TC;
+          const int at = (c >> 4) * 256 + row * 16 + (c & 15);
+          float v = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kNW; ++w) v += sm[w * kSum + at];
+          if (row < tr.rows && o0 + c < a.N) a.y[(size_t)(tr.row0 + row) * a.N + o0 + c] = to_bf16(v);
+        }
+        buf ^= 1;
+        cu = 0;
+        ct += step;
+      }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (b0 + kNW * u >= KB) break;
-      const i32x8 xf = frag(xr[u][0], xr[u][1]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        add_scaled(acc[t], sx[u] * sc[u], block_product(frag(wr[u][t][0], wr[u][t][1]), xf));
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(&sums[wv][t][r16 * 16 + 4 * q4]) = acc[t];
-  __syncthreads();
-  // element e: row e / 16 NT, column e % 16 NT
-  for (int e = threadIdx.x; e < 256 * NT; e += 64 * kNW) {
-    const int row = e / (16 * NT), c = e % (16 * NT);
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kNW; ++w) s += sums[w][c >> 4][row * 16 + (c & 15)];
-    if (row < tr.rows && o0 + c < a.N) a.y[(size_t)(tr.row0 + row) * a.N + o0 + c] = to_bf16(s);
   }
 }
 
@@ -536,14 +620,47 @@ static hipError_t launch_fp8_tile_t(Fp8Args a, int sk, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int NT>
-static hipError_t launch_fp8_rows_t(Fp8Args a, hipStream_t stream) {
-  a.mtiles = (a.M + 15) / 16 + (a.m_sizes != nullptr ? a.G : 0);
+template <int NT, int U, bool XL>
+static hipError_t launch_fp8_rows_t(Fp8Args a, int lds_bytes, int grid, hipStream_t stream) {
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t ea =
+      ensure_dyn_lds(reinterpret_cast<const void*>(&fp8_rows_kernel<NT, U, false, XL>), 160 * 1024, lds_set);
+  if (ea != hipSuccess) return ea;
   a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
-  const long long blocks = (long long)a.mtiles * a.otiles;
-  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_rows_kernel<NT>), dim3((unsigned)blocks), dim3(64 * kNW), 0, stream, a);
+  hipLaunchKernelGGL((fp8_rows_kernel<NT, U, false, XL>), dim3((unsigned)min(grid, a.otiles), (unsigned)((a.M + 15) / 16)),
+                     dim3(64 * kNW), lds_bytes, stream, a);
   return hipGetLastError();
+}
+
+template <int NT, int U>
+static hipError_t launch_fp8_rows_grouped_t(Fp8Args a, hipStream_t stream) {
+  a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
+  const long long blocks = (long long)((a.M + 15) / 16 + a.G) * a.otiles;
+  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp8_rows_kernel<NT, U, true, false>), dim3((unsigned)blocks), dim3(64 * kNW), kRowsSums<NT>, stream,
+                     a);
+  return hipGetLastError();
+}
+
+// Plain: 16 columns at a time by workgroups that stay (one per compute unit, two
+// where their rows fit LDS twice), the rows in LDS where they fit (1 x 17408 x
+// 5120 24.3 us with the rows from L2, 18.6 from LDS; 16 rows 32.2 and 21.6).
+// By expert: a workgroup per tile, of 64 columns while that leaves two tiles per
+// compute unit, else of 32 or 16 (96 rows of 64 experts, 2048 x 4096: 77.4 us
+// with 64 columns, 88.7 with 32, 118 with 16).
+static hipError_t launch_fp8_rows(const Fp8Args& a, int cus, hipStream_t stream) {
+  if (a.m_sizes != nullptr) {
+    const int tiles = min(a.G, a.M);   // at least so many with rows, if rows are spread
+    if ((long long)tiles * ((a.N + 63) / 64) >= 2 * cus) return launch_fp8_rows_grouped_t<4, 2>(a, stream);
+    if ((long long)tiles * ((a.N + 31) / 32) >= 2 * cus) return launch_fp8_rows_grouped_t<2, 4>(a, stream);
+    return launch_fp8_rows_grouped_t<1, 4>(a, stream);
+  }
+  const int R = min(16, a.M);
+  const long long with_x =
+      kRowsSums<1> + (((long long)R * a.K + 1023) & ~1023LL) + (long long)R * (a.K / kBlk) * 4;
+  if (with_x <= 160 * 1024)
+    return launch_fp8_rows_t<1, 4, true>(a, (int)with_x, with_x <= 80 * 1024 ? 2 * cus : cus, stream);
+  return launch_fp8_rows_t<1, 4, false>(a, kRowsSums<1>, cus, stream);
 }
 
 // stages: three where they fit LDS, else two
@@ -563,9 +680,9 @@ static hipError_t launch_fp8_tile_bm(const Fp8Args& a, int sk, int bm, hipStream
 
 hipError_t launch_fp8_gemm(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, uint16_t* y,
                            float* part, const int32_t* m_sizes, int M, int N, int K, int G, bool grad, int cps, int sk,
-                           int bm, hipStream_t stream) {
+                           int bm, int cus, hipStream_t stream) {
   const Fp8Args a = {x, xs, w, ws, y, part, m_sizes, M, N, K, G, cps, 0, 0};
-  if (bm == 16 && !grad && sk == 1) return launch_fp8_rows_t<2>(a, stream);
+  if (bm == 16) return grad || sk != 1 ? hipErrorInvalidValue : launch_fp8_rows(a, cus, stream);
   return grad ? launch_fp8_tile_bm<true>(a, sk, bm, stream) : launch_fp8_tile_bm<false>(a, sk, bm, stream);
 }
 

@@ -102,10 +102,10 @@ hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int
 // grad: the input gradient (x: dY, contraction over N). bm: rows per tile (16:
 // the kernel for few rows, whole contractions of the products only). With
 // part != nullptr slice s of sk, cps contraction blocks, writes fp32
-// partials part[s, :, :].
+// partials part[s, :, :]. cus: compute units of the device.
 hipError_t launch_fp8_gemm(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws, uint16_t* y,
                            float* part, const int32_t* m_sizes, int M, int N, int K, int G, bool grad, int cps, int sk,
-                           int bm, hipStream_t stream);
+                           int bm, int cus, hipStream_t stream);
 
 // ---- input gradient of the 4-bit products (w4grad.hip)
 constexpr int64_t w4_grad_padded(int64_t N) { return (N + 127) / 128 * 128; }

@@ -557,8 +557,8 @@ struct RowsPlan {
 // costs besides (first loads, outputs). Past one round the last, partly filled
 // one counts in part: workgroups do not end together (1322 x 19456 x 2560: 2.08
 // rounds of 192 rows run like 2.4, 3.3 of 128 like 3.5).
-double rounds_us(double tiles, double steps, double step_us, double extra_us) {
-  const double r = tiles / device_cus();
+double rounds_us(double tiles, double steps, double step_us, double extra_us, double cus) {
+  const double r = tiles / cus;
   const double eff = r <= 1.0 ? 1.0 : 0.4 * r + 0.6 * std::ceil(r);
   return eff * (extra_us + steps * step_us);
 }
@@ -580,14 +580,17 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
   RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
   double least = -1.0;
   const int64_t ot = ceil_div(O, 256);
+  const double cus = device_cus();
   for (const TileTime& c : cands) {
     if (forced > 0 && c.bm != forced) continue;
     // grouped: each group's last tile is half full on average
     const double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
-    for (int32_t sk = 1; sk <= 16; ++sk) {
-      if (sk > 1 && (G > 0 || mt * (double)(ot * sk) > device_cus() || ceil_div(steps, sk) < min_steps)) break;
+    const double tiles = mt * (double)ot;
+    for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
+      const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
+      if (sk > 1 && (G > 0 || tiles * sk > cus || part < min_steps)) break;
       const double us =
-          rounds_us(mt * (double)(ot * sk), (double)ceil_div(steps, sk), c.us, extra_us) + split_us(sk, (double)M * (double)O);
+          rounds_us(tiles * sk, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
       if (least < 0.0 || us < least * (1.0 - 1e-9)) {
         least = us;
         best = {c.bm, sk};

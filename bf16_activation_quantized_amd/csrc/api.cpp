@@ -572,11 +572,13 @@ struct TileTime {
   double us;   // of one contraction step
 };
 
+// half_tiles: a plain problem's last row tile of at most half the height counts as
+// a half.
 // Least estimated time over the tile heights and (without groups) the splits
 // whose workgroups fit one round; `forced` > 0 fixes the height.
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
-                    int forced, int64_t min_steps) {
+                    int forced, int64_t min_steps, bool half_tiles) {
   RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
   double least = -1.0;
   const int64_t ot = ceil_div(O, 256);
@@ -584,7 +586,8 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
   for (const TileTime& c : cands) {
     if (forced > 0 && c.bm != forced) continue;
     // grouped: each group's last tile is half full on average
-    const double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
+    double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
+    if (half_tiles && G == 0 && mt > 1.0 && M % c.bm != 0 && M % c.bm <= c.bm / 2) mt -= 0.5;
     const double tiles = mt * (double)ot;
     for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
       const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
@@ -603,14 +606,14 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
 // One block of 128 of the 8-bit tile kernel by height, between what it takes
 // alone and with every compute unit busy (lower clocks): at 777 x 9728 x 2560 and
 // 8192^3 256 rows 1.42 and 1.78 us, 128 rows 0.93 and 1.04, 64 rows 0.70 and 0.63.
-constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.50}, {192, 1.33}, {160, 1.15}, {128, 0.99}, {96, 0.82}, {64, 0.66}};
+constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1.15}, {128, 0.99}, {96, 0.82}, {64, 0.66}};
 constexpr double kFp8ExtraUs = 6.0;
 
 // M rows of G groups (0: plain), O output columns, cb contraction blocks
 RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
   if (forced == 16 || (forced == 0 && per <= 16 && !grad)) return {16, 1};
-  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4);
+  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true);
 }
 
 w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
@@ -702,7 +705,7 @@ w4a16_status make_w4_grad_plan(bool grouped, int32_t G, int64_t M, int64_t N, in
     for (const TileTime& c : kW4GradTimes) built = built || c.bm == bm;
     if (!built) return W4A16_ERR_SHAPE;
   }
-  const RowsPlan r = plan_tiles(kW4GradTimes, kW4GradExtraUs, grouped ? G : 0, M, K, (int64_t)np / 64, bm, 8);
+  const RowsPlan r = plan_tiles(kW4GradTimes, kW4GradExtraUs, grouped ? G : 0, M, K, (int64_t)np / 64, bm, 8, false);
   p->bm = r.bm;
   p->sk = r.sk;
   if (sk != 0) {

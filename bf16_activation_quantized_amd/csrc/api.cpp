@@ -572,9 +572,8 @@ struct TileTime {
   double us;   // of one contraction step
 };
 
-// half_tiles: a plain problem's last row tile of at most half the height counts as
-// a half.
-// Least estimated time over the tile heights and (without groups) the splits
+// half_tiles: past one round a plain problem's last row tile counts as a half if it
+// has at most half the height's rows. Least estimated time over the tile heights and (without groups) the splits
 // whose workgroups fit one round; `forced` > 0 fixes the height.
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
@@ -586,14 +585,14 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
   for (const TileTime& c : cands) {
     if (forced > 0 && c.bm != forced) continue;
     // grouped: each group's last tile is half full on average
-    double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
-    if (half_tiles && G == 0 && mt > 1.0 && M % c.bm != 0 && M % c.bm <= c.bm / 2) mt -= 0.5;
+    const double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
     const double tiles = mt * (double)ot;
+    const bool half = half_tiles && G == 0 && tiles > cus && M % c.bm != 0 && M % c.bm <= c.bm / 2;
     for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
       const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
       if (sk > 1 && (G > 0 || tiles * sk > cus || part < min_steps)) break;
       const double us =
-          rounds_us(tiles * sk, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
+          rounds_us(half ? tiles - 0.5 * (double)ot : tiles * sk, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
       if (least < 0.0 || us < least * (1.0 - 1e-9)) {
         least = us;
         best = {c.bm, sk};

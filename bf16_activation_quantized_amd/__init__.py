@@ -13,6 +13,7 @@ torch.int32.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -548,6 +549,13 @@ def w4a16_fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales
     return q, scales
 
 
+@functools.lru_cache(maxsize=4096)
+def _bytes_of(name: str, dev: int, *args) -> int:
+    """A workspace size, which depends on the sizes and the device's compute
+    units only: kept, since asking takes a good part of a short call."""
+    return int(_on(dev, getattr(_lib_handle or _lib(), name), *args))
+
+
 def w4a16_fp8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(_lib().w4a16_fp8_gemm_workspace_bytes(M, N, K))
 
@@ -576,17 +584,16 @@ def _fp8(name: str, grad: bool, x, x_scales, w, w_scales, m_sizes, y, workspace,
     pws = _in(w_scales, "w_scales", f32, (*lead, -(-N // 128), K // 128), dev)
     pm = None if m_sizes is None else _in(m_sizes, "m_sizes", torch.int32, (G,), dev)
     y, py = _out(y, ny, torch.bfloat16, (M, outer), x, dev, stream)
-    L = _lib_handle or _lib()
     if tile is not None:
-        need = 0 if pm else _on(dev, L.w4a16_fp8_gemm_workspace_bytes_ex, int(grad), M, N, K, *tile)
+        need = 0 if pm else _bytes_of("w4a16_fp8_gemm_workspace_bytes_ex", dev, int(grad), M, N, K, *tile)
         workspace, pk, nk = _given_workspace(workspace, f32, need, x, dev, stream)
         _run("w4a16_fp8_gemm_ex", dev, stream, int(grad), px, pxs, pw, pws, pm, py, G, M, N, K, *tile, pk, nk)
     elif grad:
-        need = 0 if pm else _on(dev, L.w4a16_fp8_gemm_grad_workspace_bytes, M, N, K)
+        need = 0 if pm else _bytes_of("w4a16_fp8_gemm_grad_workspace_bytes", dev, M, N, K)
         workspace, pk, nk = _given_workspace(workspace, f32, need, x, dev, stream)
         _run(name, dev, stream, px, pxs, pw, pws, pm, py, G, M, N, K, pk, nk)
     elif pm is None:
-        need = _on(dev, L.w4a16_fp8_gemm_workspace_bytes, M, N, K)
+        need = _bytes_of("w4a16_fp8_gemm_workspace_bytes", dev, M, N, K)
         workspace, pk, nk = _given_workspace(workspace, f32, need, x, dev, stream)
         _run(name, dev, stream, px, pxs, pw, pws, py, M, N, K, pk, nk)
     else:
@@ -646,13 +653,12 @@ def w4a16_gemm_grad(dy: torch.Tensor, w_packed: torch.Tensor, scales: torch.Tens
     ps = _in(scales, "scales", bf16, (*lead, N, K // group_size), dev)
     pm = None if m_sizes is None else _in(m_sizes, "m_sizes", torch.int32, (G,), dev)
     dx, px = _out(dx, "dx", bf16, (M, K), dy, dev, stream)
-    L = _lib_handle or _lib()
     if tile is None:
-        need = 0 if workspace is not None else _on(dev, L.w4a16_gemm_grad_workspace_bytes, G, M, N, K, group_size)
+        need = _bytes_of("w4a16_gemm_grad_workspace_bytes", dev, G, M, N, K, group_size)
         workspace, pk, nk = _given_workspace(workspace, u8, need, dy, dev, stream)
         _run("w4a16_gemm_grad", dev, stream, pd, pw, ps, pm, px, G, M, N, K, group_size, pk, nk)
     else:
-        need = _on(dev, L.w4a16_gemm_grad_workspace_bytes_ex, G, M, N, K, group_size, *tile)
+        need = _bytes_of("w4a16_gemm_grad_workspace_bytes_ex", dev, G, M, N, K, group_size, *tile)
         workspace, pk, nk = _given_workspace(workspace, u8, need, dy, dev, stream)
         _run("w4a16_gemm_grad_ex", dev, stream, pd, pw, ps, pm, px, G, M, N, K, group_size, *tile, pk, nk)
     return dx

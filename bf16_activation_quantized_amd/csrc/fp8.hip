@@ -556,6 +556,7 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
   f32x4 acc[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  asm volatile("" ::: "memory");   // the rows' loads come first: only they are waited for below
 #pragma unroll
   for (int u = 0; u < U; ++u) load(u);
   if constexpr (XL) wait_vm_barrier<U * (2 * NT + 1)>();

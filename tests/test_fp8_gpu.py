@@ -17,7 +17,8 @@ from products_ref import E4M3, e4m3_of, fp8_values, grouped_ref, quantize_ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-TILES = [None, (16, 0), (64, 1), (128, 1), (256, 1), (64, 2), (128, 4), (256, 16)]
+TILES = [None, (16, 0), (64, 1), (96, 1), (128, 1), (160, 1), (192, 1), (224, 1), (256, 1), (64, 2), (128, 4), (160, 3),
+         (256, 16)]
 GRAD_TILES = [t for t in TILES if t is None or t[0] != 16]
 
 
@@ -101,7 +102,8 @@ SIZES = [[5], [0, 3], [1, 0, 16, 0, 2], [40, 1, 0, 17, 100], [0, 0, 0, 300, 20, 
          [1] * 70, [2, 0] * 65 + [33]]
 
 
-@pytest.mark.parametrize("tile", [None, (16, 0), (64, 0), (128, 0), (256, 0)], ids=str)
+@pytest.mark.parametrize("tile", [None, (16, 0), (64, 0), (96, 0), (128, 0), (160, 0), (192, 0), (224, 0), (256, 0)],
+                         ids=str)
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{sum(s)}")
 @pytest.mark.parametrize("grad", [False, True])
 def test_grouped_exact(sizes, tile, grad):
@@ -138,6 +140,25 @@ def test_random_values_grouped(grad):
     sizes = [70, 0, 3, 200, 1]
     c = Case(sum(sizes), 384, 512, sizes, grad, exact=False)
     close(c.run(), *c.want(), 4)
+
+
+@pytest.mark.parametrize("M", [1, 2, 5, 8, 15, 16])
+@pytest.mark.parametrize("N,K", [(16, 128), (40, 1024), (4160, 128), (5000, 1152), (300, 8832), (300, 9728), (130, 16384)])
+def test_few_rows(M, N, K):
+    """Every row count of the kernel for few rows, with the rows in LDS and (long ones) from L2, one and more column
+    tiles per workgroup, contractions shorter than its waves."""
+    c = Case(M, N, K)
+    assert same(c.run((16, 0)), c.want()[0])
+
+
+@pytest.mark.parametrize("N,K,G", [(64, 128, 3), (1000, 256, 5), (4096, 128, 20), (2048, 384, 64)])
+def test_few_rows_grouped(N, K, G):
+    """One to 17 rows per expert: tiles of 16, 32 and 64 columns."""
+    g = gen(G)
+    sizes = torch.randint(0, 18, (G,), generator=g).tolist()
+    c = Case(sum(sizes) + 2, N, K, sizes)
+    y = c.run((16, 0))
+    assert same(y[:-2], c.want()[0][:-2])
 
 
 def test_largest_and_smallest_values():
@@ -182,7 +203,7 @@ def test_non_finite_values_stay_in_their_row_and_column(tile):
 
 
 @pytest.mark.parametrize("grad", [False, True])
-@pytest.mark.parametrize("bm", [0, 16, 64, 128, 256])
+@pytest.mark.parametrize("bm", [0, 16, 64, 96, 128, 160, 192, 224, 256])
 def test_other_experts_do_not_reach_a_row(grad, bm):
     """NaN in an expert, in its rows and in the rows behind the last: the others' outputs are the same bits."""
     if grad and bm == 16:

@@ -20,6 +20,7 @@ CALLS = {
 @pytest.mark.parametrize("name", CALLS)
 def test_device_and_stream(on_device_1, name):   # noqa: F811
     f = CALLS[name]
+    w4._bytes_of.cache_clear()
     f()
     assert on_device_1.calls[-1][0] == name and all(d == 1 for _, d, _ in on_device_1.calls)   # sizes too
     assert on_device_1.calls[-1][2][-1] == 0x201 and on_device_1.current == 0
@@ -32,6 +33,7 @@ def test_device_and_stream(on_device_1, name):   # noqa: F811
     assert on_device_1.calls[-1][1] == 1 and on_device_1.calls[-1][2][-1] == own.cuda_stream
     f(stream=0x7000)
     assert on_device_1.calls[-1][2][-1] == 0x7000
+    w4._bytes_of.cache_clear()      # (the stand-in's sizes)
 
 
 def test_wrong_arguments_raise():

@@ -15,7 +15,8 @@ from products_ref import grouped_ref, int4_values
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-TILES = [None, (16, 1), (64, 1), (128, 1), (256, 1), (16, 4), (64, 2), (256, 16)]
+HEIGHTS = (16, 32, 64, 96, 128, 160, 192, 224, 256)
+TILES = [None] + [(h, 1) for h in HEIGHTS] + [(16, 4), (32, 16), (64, 2), (96, 3), (192, 5), (256, 16)]
 
 
 class Case:
@@ -58,7 +59,7 @@ def test_exact(M, N, K, gs, tile):
     assert torch.equal(c.run(tile).cpu(), c.want()[0].bfloat16())
 
 
-@pytest.mark.parametrize("tile", [None, (16, 1), (64, 1), (128, 1), (256, 1)], ids=str)
+@pytest.mark.parametrize("tile", [None] + [(h, 1) for h in HEIGHTS], ids=str)
 @pytest.mark.parametrize("gs", [128, 32])
 @pytest.mark.parametrize("sizes", [[5], [0, 3], [40, 1, 0, 17, 100], [0, 0, 300, 20, 0], [0, 0], [1] * 70],
                          ids=lambda s: f"{len(s)}x{sum(s)}")
@@ -71,7 +72,36 @@ def test_grouped_exact(sizes, gs, tile):
     assert torch.equal(dx[:-5].cpu(), want[:-5].bfloat16()) and (dx[-5:] == 7).all()
 
 
-@pytest.mark.parametrize("tile", [None, (16, 1), (64, 2), (128, 1), (256, 1)], ids=str)
+@pytest.mark.parametrize("gs,K", [(32, 4096), (32, 4224), (32, 8320), (128, 16384), (128, 16512), (128, 24704)])
+def test_wide_rows_of_scales(gs, K):
+    """Up to 128 scale groups the prepass reads them as one run, past that 64 at a time."""
+    for N in (40, 264):
+        c = Case(20, N, K, gs)
+        assert torch.equal(c.run().cpu(), c.want()[0].bfloat16())
+    c = Case(9, 136, K, gs, [3, 0, 4])
+    assert torch.equal(c.run()[:7].cpu(), c.want()[0][:7].bfloat16())
+
+
+@pytest.mark.parametrize("N", [20472, 20480, 20488, 41000])
+def test_long_rows(N):
+    """Rows that the prepass holds in registers, and longer ones, with the largest value in each part."""
+    c = Case(4, N, 128)
+    for m, n in enumerate((0, N - 1, N // 2, 20479 % N)):
+        c.dy[m] = 0
+        c.dy[m, n] = 3.0
+        c.dy[m, (n + 77) % N] = -2.0 ** -10
+    c.dev[0] = c.dy.to(DEV)
+    assert torch.equal(c.run().cpu(), c.want()[0].bfloat16())
+
+
+def test_negative_scales():
+    c = Case(40, 200, 256, 32)
+    c.s[::3] *= -1
+    c.dev[2] = c.s.to(DEV)
+    assert torch.equal(c.run().cpu(), c.want()[0].bfloat16())
+
+
+@pytest.mark.parametrize("tile", [None, (16, 1), (32, 1), (64, 2), (128, 1), (192, 1), (256, 1)], ids=str)
 @pytest.mark.parametrize("M,N,K,gs", [(1, 1000, 256, 128), (40, 2048, 384, 32), (300, 1032, 512, 128),
                                       (300, 1032, 512, 32)])
 def test_random_values(M, N, K, gs, tile):

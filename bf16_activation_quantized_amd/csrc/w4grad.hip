@@ -65,25 +65,28 @@ struct GradPrep {
   uint16_t* tops;       // [G, Np / 128, Kg] bf16 bits of the largest finite magnitudes
   int M, N, Np, Kg, G;
   int sblocks;          // workgroups per 128 n of the scales
+  int stotal;           // workgroups of all scales, the grid's first
+  int per_row;          // threads per row of dY
 };
 
-// Workgroups 0 .. M - 1: a row of dY each, held in registers between its largest
-// magnitude and its conversion up to kPrepRegs x 4096 elements (read again past
-// that). The others: 128 n of the scales of one expert each; up to kPrepWide
-// groups they are one run of memory, read in 16-byte pieces, past that 64 groups
-// at a time are read by rows.
+// The first workgroups take 128 n of the scales of one expert each: up to
+// kPrepWide groups they are one run of memory, read in 16-byte pieces, past that 64
+// groups at a time are read by rows. The others take rows of dY, 64 to 512 threads
+// each, which hold the row in registers between its largest magnitude and its
+// conversion up to kPrepRegs x 8 elements per thread (read again past that).
 constexpr int kPrepThreads = 512;
 constexpr int kPrepRegs = 5;
 constexpr int kPrepWide = 128;
 
 __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep a) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[128 * kPrepWide];   // [n][k group]
+  __shared__ __attribute__((aligned(16))) uint16_t tile[128 * (kPrepWide + 1)];   // [n][k group], odd pitch
   const int t = threadIdx.x;
-  if ((int)blockIdx.x < a.M) {
+  if ((int)blockIdx.x >= a.stotal) {
     uint32_t* part = reinterpret_cast<uint32_t*>(tile);
-    const int m = blockIdx.x;
+    const int T = a.per_row, lt = t & (T - 1);
+    const int m = ((int)blockIdx.x - a.stotal) * (kPrepThreads / T) + t / T;
+    const int n8 = m < a.M ? a.N / 8 : 0, p8 = m < a.M ? a.Np / 8 : 0;
     const u32x4* src = reinterpret_cast<const u32x4*>(a.dy + (size_t)m * a.N);
-    const int n8 = a.N / 8, p8 = a.Np / 8;
     uint32_t top = 0;
     auto take = [&](u32x4 v) {
 #pragma unroll
@@ -95,18 +98,19 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep 
     u32x4 held[kPrepRegs];
 #pragma unroll
     for (int i = 0; i < kPrepRegs; ++i) {
-      const int at = t + kPrepThreads * i;
+      const int at = lt + T * i;
       held[i] = at < n8 ? src[at] : u32x4{0u, 0u, 0u, 0u};
     }
 #pragma unroll
     for (int i = 0; i < kPrepRegs; ++i) take(held[i]);
-    for (int at = t + kPrepThreads * kPrepRegs; at < n8; at += kPrepThreads) take(src[at]);
+    for (int at = lt + T * kPrepRegs; at < n8; at += T) take(src[at]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    if ((t & 63) == 0) part[t >> 6] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPrepThreads / 64; ++i) top = max(top, part[i]);
+    if (T > 64) {
+      if ((t & 63) == 0) part[t >> 6] = top;
+      __syncthreads();
+      for (int i = 0; i < T / 64; ++i) top = max(top, part[t / T * (T / 64) + i]);
+    }
     const int e = up_by(top, 14);
     u32x4* dst = reinterpret_cast<u32x4*>(a.h + (size_t)m * a.Np);
     auto put = [&](int at, u32x4 v) {
@@ -115,15 +119,14 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep 
     };
 #pragma unroll
     for (int i = 0; i < kPrepRegs; ++i) {
-      const int at = t + kPrepThreads * i;
+      const int at = lt + T * i;
       if (at < p8) put(at, held[i]);
     }
-    for (int at = t + kPrepThreads * kPrepRegs; at < p8; at += kPrepThreads)
-      put(at, at < n8 ? src[at] : u32x4{0u, 0u, 0u, 0u});
-    if (t == 0) a.up[m] = e;
+    for (int at = lt + T * kPrepRegs; at < p8; at += T) put(at, at < n8 ? src[at] : u32x4{0u, 0u, 0u, 0u});
+    if (lt == 0 && m < a.M) a.up[m] = e;
     return;
   }
-  int b = (int)blockIdx.x - a.M;
+  int b = blockIdx.x;
   const int kc = b % a.sblocks;
   b /= a.sblocks;
   const int chunks = a.Np / 128;
@@ -131,14 +134,26 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep 
   const int n0 = 128 * nc, rows = min(128, a.N - n0);
   const bool wide = a.Kg <= kPrepWide;
   const int k0 = wide ? 0 : 64 * kc, kn = wide ? a.Kg : min(64, a.Kg - k0);   // groups of this workgroup
+  // the 16 threads of a group read rows 8 apart: with an odd pitch from different banks
+  const int pitch = kn | 1;
   const uint16_t* src = a.s + ((size_t)g * a.N + n0) * a.Kg + k0;
   if (wide) {
     // (rows is a multiple of 8, so the run is one of 16 bytes and 16-byte aligned)
-    for (int i = t; i < rows * kn / 8; i += kPrepThreads)
-      reinterpret_cast<u32x4*>(tile)[i] = reinterpret_cast<const u32x4*>(src)[i];
+    for (int i = t; i < rows * kn / 8; i += kPrepThreads) {
+      const u32x4 v = reinterpret_cast<const u32x4*>(src)[i];
+      int n = 8 * i / kn, k = 8 * i - n * kn;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        tile[n * pitch + k] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+        if (++k == kn) {
+          k = 0;
+          ++n;
+        }
+      }
+    }
   } else {
     for (int i = t; i < rows * 64; i += kPrepThreads)
-      if ((i & 63) < kn) tile[(i >> 6) * kn + (i & 63)] = src[(size_t)(i >> 6) * a.Kg + (i & 63)];
+      if ((i & 63) < kn) tile[(i >> 6) * pitch + (i & 63)] = src[(size_t)(i >> 6) * a.Kg + (i & 63)];
   }
   __syncthreads();
   for (int i = t; i < kn * 16; i += kPrepThreads) {   // 8 n of one group each; the group's 16 threads are neighbours
@@ -147,7 +162,7 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep 
     if (n < rows) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = tile[(n + j) * kn + kk], hi = tile[(n + j + 4) * kn + kk];
+        const uint32_t lo = tile[(n + j) * pitch + kk], hi = tile[(n + j + 4) * pitch + kk];
         o[j] = lo | (hi << 16);
         const uint32_t ml = lo & 0x7FFFu, mh = hi & 0x7FFFu;
         top = max(top, max(ml < 0x7F80u ? ml : 0u, mh < 0x7F80u ? mh : 0u));
@@ -493,8 +508,15 @@ hipError_t launch_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* 
   pr.tops = reinterpret_cast<uint16_t*>(ws + p.tops);
   pr.M = M; pr.N = N; pr.Np = Np; pr.Kg = Kg; pr.G = G;
   pr.sblocks = Kg <= kPrepWide ? 1 : (Kg + 63) / 64;
-  const long long blocks = (long long)M + (long long)G * (Np / 128) * pr.sblocks;
+  // as few threads per row as hold it in registers: a row is a chain of a load, a
+  // reduction and a store (2048 rows of 2048: 15.5 us with 512 threads each, 8 with 64)
+  pr.per_row = 64;
+  while (pr.per_row < kPrepThreads && N > pr.per_row * 8 * kPrepRegs) pr.per_row *= 2;
+  const int rows = kPrepThreads / pr.per_row;
+  const long long sblocks = (long long)G * (Np / 128) * pr.sblocks;
+  const long long blocks = sblocks + (M + rows - 1) / rows;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  pr.stotal = (int)sblocks;
   hipLaunchKernelGGL(grad_prep_kernel, dim3((unsigned)blocks), dim3(kPrepThreads), 0, stream, pr);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

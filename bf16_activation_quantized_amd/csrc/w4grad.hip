@@ -380,11 +380,16 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
         for (int ns = 0; ns < SN; ++ns)
           acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[p][st * SN + ns], xf[ms & 1][st], acc[ms][ns], 0, 0, 0);
       if (ms == 0) read_raw(after);   // (it waits, behind the first products)
+      // (a chain of conversions and a write to LDS: between the products rather than
+      // ahead of the barrier, 957 -> 935 us at 8192^3 and 128 rows, 933 -> 927 at 192;
+      // at 256 rows, with few registers left, 918 ahead of the barrier and 946 here)
+      if (ms == (BM < 256 ? MS / 2 : MS - 1)) {
+        put_scales(nstage, sv[P.value], sup);
+        sv[P.value] = scale_word(word);
+      }
 #pragma unroll
       for (int f = ms * NF / MS; f < (ms + 1) * NF / MS; ++f) unpack(after, f, wf[1 - p][f]);
     }
-    put_scales(nstage, sv[P.value], sup);
-    sv[P.value] = scale_word(word);
     wait_vm_barrier<(NS - 3) * kPer>();   // stage j + 2 has landed
   };
 

@@ -545,8 +545,9 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
       xr[u][1] = ld128(rx, roff + 16u, so);
       sx[u] = ld32(rxs, (uint32_t)r16 * (uint32_t)KB * 4u, (uint32_t)min(b, KB - 1) * 4u);
     }
-    // TC divides 128: the tile's columns lie in one block
-    sc[u] = ld32(rws, 0u, __builtin_amdgcn_readfirstlane(((uint32_t)(o0 / kBlk) * (uint32_t)KB + (uint32_t)b) * 4u));
+    // TC divides 128: the tile's columns lie in one block. (The whole offset is a
+    // vector offset, which the extent checks: past the last tile it lies outside.)
+    sc[u] = ld32(rws, ((uint32_t)(o0 / kBlk) * (uint32_t)KB + (uint32_t)b) * 4u);
     if (++lu == nb) {
       lu = 0;
       lt += step;

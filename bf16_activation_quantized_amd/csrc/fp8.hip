@@ -625,7 +625,7 @@ static hipError_t launch_fp8_tile_t(Fp8Args a, int sk, hipStream_t stream) {
   const hipError_t ea =
       ensure_dyn_lds(reinterpret_cast<const void*>(&fp8_tile_kernel<BM, WM, NS, GRAD>), lds_bytes, lds_set);
   if (ea != hipSuccess) return ea;
-  a.mtiles = (a.M + BM - 1) / BM + (a.m_sizes != nullptr ? a.G : 0);
+  a.mtiles = a.m_sizes != nullptr ? group_tiles_bound(a.M, BM, a.G) : (a.M + BM - 1) / BM;
   a.otiles = ((GRAD ? a.K : a.N) + kBN - 1) / kBN;
   const long long blocks = (long long)a.mtiles * a.otiles;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
@@ -649,7 +649,7 @@ static hipError_t launch_fp8_rows_t(Fp8Args a, int lds_bytes, int grid, hipStrea
 template <int NT, int U>
 static hipError_t launch_fp8_rows_grouped_t(Fp8Args a, hipStream_t stream) {
   a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
-  const long long blocks = (long long)((a.M + 15) / 16 + a.G) * a.otiles;
+  const long long blocks = (long long)group_tiles_bound(a.M, 16, a.G) * a.otiles;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
   hipLaunchKernelGGL((fp8_rows_kernel<NT, U, true, false>), dim3((unsigned)blocks), dim3(64 * kNW), kRowsSums<NT>, stream,
                      a);

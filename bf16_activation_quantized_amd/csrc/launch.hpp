@@ -95,6 +95,12 @@ hipError_t launch_expert_combine_grad(const uint16_t* dy, const uint16_t* z, con
                                       uint16_t* dz, float* dw, int64_t T, int k, int64_t rows, int width,
                                       hipStream_t stream);
 
+// Row tiles of height bm that M rows in G groups take at most: each of the groups
+// that have rows (at most min(G, M)) ends in a tile that may hold a single row.
+inline int group_tiles_bound(int M, int bm, int G) {
+  return (int)(((long long)M + (long long)(bm - 1) * (G < M ? G : M)) / bm);
+}
+
 // ---- 8-bit products with a scale for each block of 128 (fp8.hip)
 // scales of blocks of block_rows (1 or 128) x 128
 hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int64_t M, int K, int block_rows,

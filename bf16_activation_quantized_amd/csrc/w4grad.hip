@@ -472,7 +472,7 @@ static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
   const hipError_t ea =
       ensure_dyn_lds(reinterpret_cast<const void*>(&w4_grad_kernel<BM, WM, NS, GS>), lds_bytes, lds_set);
   if (ea != hipSuccess) return ea;
-  a.mtiles = (a.M + BM - 1) / BM + (a.m_sizes != nullptr ? a.G : 0);
+  a.mtiles = a.m_sizes != nullptr ? group_tiles_bound(a.M, BM, a.G) : (a.M + BM - 1) / BM;
   a.otiles = (a.K + kBN - 1) / kBN;
   const long long blocks = (long long)a.mtiles * a.otiles;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;

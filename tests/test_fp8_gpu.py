@@ -118,6 +118,16 @@ def test_grouped_exact(sizes, tile, grad):
     assert same(y[:-5], want[:-5]) and (y[-5:] == 7).all()
 
 
+@pytest.mark.parametrize("tile", [None, (64, 0), (128, 0), (256, 0)], ids=str)
+@pytest.mark.parametrize("grad", [False, True])
+def test_few_rows_far_apart(grad, tile):
+    """One row of each of a few experts, the first and the last of many among them,
+    so that every tile holds one row; then all rows with the last expert."""
+    for sizes in ([1] + [0] * 198 + [1, 0, 0, 1, 1] + [0] * 95 + [1], [0] * 299 + [40], [40] + [0] * 299):
+        c = Case(sum(sizes), 128, 128, sizes, grad)
+        assert same(c.run(tile), c.want()[0])
+
+
 def close(y, want, size, blocks):
     y = y.double().cpu()
     lim = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -23 * (16 + blocks + 16)) * size

@@ -72,6 +72,15 @@ def test_grouped_exact(sizes, gs, tile):
     assert torch.equal(dx[:-5].cpu(), want[:-5].bfloat16()) and (dx[-5:] == 7).all()
 
 
+@pytest.mark.parametrize("tile", [None, (16, 1), (64, 1), (256, 1)], ids=str)
+def test_few_rows_far_apart(tile):
+    """One row of each of a few experts, the first and the last of many among them,
+    so that every tile holds one row; then all rows with the last expert."""
+    for sizes in ([1] + [0] * 198 + [1, 0, 0, 1, 1] + [0] * 95 + [1], [0] * 299 + [40], [40] + [0] * 299):
+        c = Case(sum(sizes), 64, 128, 128, sizes)
+        assert torch.equal(c.run(tile).cpu(), c.want()[0].bfloat16())
+
+
 @pytest.mark.parametrize("gs,K", [(32, 4096), (32, 4224), (32, 8320), (128, 16384), (128, 16512), (128, 24704)])
 def test_wide_rows_of_scales(gs, K):
     """Up to 128 scale groups the prepass reads them as one run, past that 64 at a time."""

@@ -608,10 +608,15 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
 constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1.15}, {128, 0.99}, {96, 0.82}, {64, 0.66}};
 constexpr double kFp8ExtraUs = 6.0;
 
+// The kernel for few rows holds those of a plain product in LDS.
+bool fp8_rows_built(bool grad, int64_t G, int64_t M, int64_t cb) {
+  return !grad && (G > 0 || w4a16::fp8_rows_lds(M, cb * kGroup) <= w4a16::kRowsLds);
+}
+
 // M rows of G groups (0: plain), O output columns, cb contraction blocks
 RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
-  if (forced == 16 || (forced == 0 && per <= 16 && !grad)) return {16, 1};
+  if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, cb))) return {16, 1};
   return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true);
 }
 
@@ -630,7 +635,7 @@ w4a16_status make_fp8_plan(bool grad, int64_t G, int64_t M, int64_t N, int64_t K
                            uint64_t* bytes) {
   const int64_t O = grad ? K : N, cb = (grad ? N : K) / kGroup;
   if (bm != 0) {
-    bool built = bm == 16 && !grad;
+    bool built = bm == 16 && fp8_rows_built(grad, G, M, cb);
     for (const TileTime& c : kFp8Times) built = built || c.bm == bm;
     if (!built) return W4A16_ERR_SHAPE;
   }

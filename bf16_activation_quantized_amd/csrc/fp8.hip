@@ -455,24 +455,26 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
 // registers, each once; the 8 waves of a workgroup take every eighth contraction
 // block of the same 16 NT columns and add their sums through LDS, in wave order. A
 // workgroup takes column tiles gridDim.x apart, and each wave's blocks of all of
-// them are one sequence, with U blocks in flight throughout. XL: the rows and
-// their scales lie in LDS, loaded once per workgroup (from L2 they would cost as
-// much traffic as the weights, and every workgroup asks for the same lines).
+// them are one sequence, with U blocks in flight throughout. XR > 0: the rows, XR
+// (8 or 16) of them, lie in LDS: from L2 they would cost as much traffic as the
+// weights (16 rows of 17408 x 5120: 32 us against 18.5). A wave reads its own blocks
+// of them only, so it loads them itself, each with the weights of the first tile that
+// it multiplies, and waits for no one (16 x 8192 x 8192 13.3 us; 16.6 with all rows
+// loaded first, by all waves).
+// Bound by the weights' stream: 1 x 17408 x 5120 16.9 us (5.3 TB/s), 16 x 8192 x 8192
+// 13.3 us (5.0 TB/s), 96 rows of 64 experts of 2048 x 4096 77 us (7.0 TB/s, in part
+// from the last-level cache).
 template <int NT>
 constexpr int kRowsSums = 2 * kNW * NT * 256 * 4;   // bytes of the sums, two buffers
 
-// bytes of R rows in LDS, in whole loads of 1 KiB
-__host__ __device__ constexpr uint32_t rows_xl_bytes(int R, int K) {
-  return ((uint32_t)R * (uint32_t)K + 1023u) & ~1023u;
-}
-
-template <int NT, int U, bool GROUPED, bool XL>
+template <int NT, int U, bool GROUPED, int XR>
 __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
   constexpr int TC = 16 * NT;
   constexpr int kSum = NT * 256;
+  constexpr int XB = XR * kBlk;   // bytes of a block of the rows
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   float* const sums = reinterpret_cast<float*>(lds);                       // [2][kNW][kSum]
-  uint8_t* const xl = lds + kRowsSums<NT>;                                 // [KB][R][128 B]
+  uint8_t* const xl = lds + kRowsSums<NT>;                                 // [KB + 1][XR][128 B]
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
@@ -500,28 +502,26 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
   const int tiles = first < end ? (end - first + step - 1) / step : 0;
   const int total = tiles * nb;
 
-  const int R = tr.rows;
-  float* const sl = reinterpret_cast<float*>(xl + rows_xl_bytes(R, K));     // [KB][R] row scales
-  if constexpr (XL) {
-    // row r of block b: 16-byte chunk c in slot c ^ pair_swz(r / 2). The workgroups
-    // of an XCD begin at different places: all read the same lines.
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (size_t)tr.row0 * K, (uint32_t)R * (uint32_t)K);
-    const int chunks = R * KB * 8, n = (chunks + 64 * kNW - 1) / (64 * kNW);
-    int at = (int)(blockIdx.x / kNumXcd) % n;
-    for (int k = 0; k < n; ++k) {
-      const int i0 = 64 * (kNW * at + wv), i = i0 + lane;
-      const int row = (i >> 3) % R, b = (i >> 3) / R;
-      const uint32_t c = (uint32_t)(i & 7) ^ pair_swz(row >> 1);
-      if (i0 < chunks)
-        dma16(rx, xl + 16 * i0, i < chunks ? (uint32_t)row * (uint32_t)K + (uint32_t)b * kBlk + 16u * c : 0xFFFFFFF0u,
-              0u);
-      if (++at == n) at = 0;
+  // row scales in LDS, [KB][XR]: on their way while the first blocks are requested
+  float* const sl = reinterpret_cast<float*>(xl + (KB + 1) * XB);
+  constexpr int kSl = XR > 0 ? (int)((kRowsLds / kBlk + 64 * kNW - 1) / (64 * kNW)) : 1;   // XR KB XB <= kRowsLds
+  uint32_t rs[kSl];
+  if constexpr (XR > 0) {
+#pragma unroll
+    for (int j = 0; j < kSl; ++j) {
+      const int i = (int)threadIdx.x + 64 * kNW * j;   // (rows past the last: zero)
+      rs[j] = ld32(rxs, i < XR * KB ? (uint32_t)((i % XR) * KB + i / XR) * 4u : 0xFFFFFFF0u);
     }
-    for (int i = threadIdx.x; i < R * KB; i += 64 * kNW) sl[i] = a.xs[(size_t)(tr.row0 + i % R) * KB + i / R];
   }
 
-  u32x4 wr[U][NT][2], xr[XL ? 1 : U][2];
-  uint32_t sx[XL ? 1 : U], sc[U];
+  // row r of a block: 16-byte chunk c in slot c ^ pair_swz(r / 2)
+  uint32_t xoff[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+    xoff[d] = (uint32_t)(8 * d + (lane >> 3)) * (uint32_t)K + 16u * ((uint32_t)(lane & 7) ^ pair_swz(4 * d + (lane >> 4)));
+
+  u32x4 wr[U][NT][2], xr[XR > 0 ? 1 : U][2];
+  uint32_t sx[XR > 0 ? 1 : U], sc[U];
   // the next block to load: tile lt, block lu of it
   int lt = first, lu = 0;
   auto load = [&](int u) {
@@ -530,15 +530,24 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
     // read and the products are zero
     const bool in = b < KB && lt < end;
     const int o0 = lt * TC;
+    const uint32_t so = (uint32_t)b * kBlk;
+    if constexpr (XR > 0) {
+      // (past the first tile zeros, to a block that is not read)
+      const bool xin = b < KB && lt == first;
+      const __amdgpu_buffer_rsrc_t rx =
+          make_rsrc(a.x + (size_t)tr.row0 * K, xin ? (uint32_t)tr.rows * (uint32_t)K : 0u);
+      uint8_t* dst = xl + (xin ? b : KB) * XB;
+#pragma unroll
+      for (int d = 0; d < XR / 8; ++d) dma16(rx, dst + 1024 * d, xoff[d], so);
+    }
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(wg + (size_t)o0 * K, in ? (uint32_t)min(TC, a.N - o0) * (uint32_t)K : 0u);
-    const uint32_t so = (uint32_t)b * kBlk;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       wr[u][t][0] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K, so);
       wr[u][t][1] = ld128(rw, roff + (uint32_t)(16 * t) * (uint32_t)K + 16u, so);
     }
-    if constexpr (!XL) {
+    if constexpr (XR == 0) {
       const __amdgpu_buffer_rsrc_t rx =
           make_rsrc(a.x + (size_t)tr.row0 * K, in ? (uint32_t)tr.rows * (uint32_t)K : 0u);
       xr[u][0] = ld128(rx, roff, so);
@@ -548,6 +557,7 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
     // TC divides 128: the tile's columns lie in one block. (The whole offset is a
     // vector offset, which the extent checks: past the last tile it lies outside.)
     sc[u] = ld32(rws, ((uint32_t)(o0 / kBlk) * (uint32_t)KB + (uint32_t)b) * 4u);
+    if constexpr (XR > 0) asm volatile("" ::: "memory");   // the blocks' loads stay apart: one block's are waited for
     if (++lu == nb) {
       lu = 0;
       lt += step;
@@ -557,62 +567,89 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
   f32x4 acc[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  asm volatile("" ::: "memory");   // the rows' loads come first: only they are waited for below
 #pragma unroll
-  for (int u = 0; u < U; ++u) load(u);
-  if constexpr (XL) wait_vm_barrier<U * (2 * NT + 1)>();
-  const int xrow = min(r16, R - 1);   // (rows past the last repeat it: not stored)
+  for (int u = 0; u < U; ++u) {
+    load(u);
+  }
+  if constexpr (XR > 0) {
+#pragma unroll
+    for (int j = 0; j < kSl; ++j) {
+      const int i = (int)threadIdx.x + 64 * kNW * j;
+      if (i < XR * KB) sl[i] = __uint_as_float(rs[j]);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+  const int xrow = XR == 8 ? r16 & 7 : r16;   // (rows past the last are not stored)
   const uint32_t xo = (uint32_t)xrow * kBlk + 16u * ((uint32_t)(2 * q4) ^ pair_swz(xrow >> 1));
   int ct = first, cu = 0, buf = 0;   // the block to compute
-  for (int s = 0; s < total; s += U) {
+  auto compute = [&](auto NEXT, int u) {   // NEXT: another block is requested in its place
+    const int b = wv + kNW * cu;
+    i32x8 xf;
+    float f;
+    if constexpr (XR > 0) {
+      // the rows of this block were requested ahead of its weights: here once those are
+      asm volatile("" : "+v"(wr[u][0][0]) : : "memory");
+      const int bx = min(b, KB - 1);
+      const uint8_t* p = xl + bx * XB;
+      xf = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
+      f = sl[bx * XR + xrow];
+    } else {
+      xf = frag(xr[u][0], xr[u][1]);
+      f = __uint_as_float(sx[u]);
+    }
+    f *= __uint_as_float(sc[u]);
+    if constexpr (XR > 0) asm volatile("" : "+v"(f));   // (not in the branches below, which would hold the reads back)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s + u >= total) break;
-      const int b = wv + kNW * cu;
-      i32x8 xf;
-      float f;
-      if constexpr (XL) {
-        const int bx = min(b, KB - 1);
-        const uint8_t* p = xl + bx * R * kBlk;
-        xf = frag(*reinterpret_cast<const u32x4*>(p + xo), *reinterpret_cast<const u32x4*>(p + (xo ^ 16u)));
-        f = sl[bx * R + xrow];
-      } else {
-        xf = frag(xr[u][0], xr[u][1]);
-        f = __uint_as_float(sx[u]);
-      }
-      // (a block past the end: its weights read zero)
-      f = b < KB ? f * __uint_as_float(sc[u]) : 0.0f;
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 p = block_product(frag(wr[u][t][0], wr[u][t][1]), xf);
+      if (b < KB) add_scaled(acc[t], f, p);
+    }
+    if constexpr (NEXT.value) load(u);
+    if (++cu == nb) {
+      // ---- the tile's sums
+      float* sm = sums + buf * kNW * kSum;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const f32x4 p = block_product(frag(wr[u][t][0], wr[u][t][1]), xf);
-        if (b < KB) add_scaled(acc[t], f, p);
+        *reinterpret_cast<f32x4*>(sm + wv * kSum + t * 256 + r16 * 16 + 4 * q4) = acc[t];
+        acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
-      load(u);
-      if (++cu == nb) {
-        // ---- the tile's sums
-        float* sm = sums + buf * kNW * kSum;
+      // (the loads in flight are not waited for; the other buffer's readers are
+      // past this barrier before it is written again)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      const int o0 = ct * TC;
+      for (int e = threadIdx.x; e < kSum; e += 64 * kNW) {
+        const int row = e / TC, c = e % TC;
+        const int at = (c >> 4) * 256 + row * 16 + (c & 15);
+        float v = 0.0f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          *reinterpret_cast<f32x4*>(sm + wv * kSum + t * 256 + r16 * 16 + 4 * q4) = acc[t];
-          acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        // (the loads in flight are not waited for; the other buffer's readers are
-        // past this barrier before it is written again)
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const int o0 = ct * TC;
-        for (int e = threadIdx.x; e < kSum; e += 64 * kNW) {
-          const int row = e / TC, c = e % TC;
-          const int at = (c >> 4) * 256 + row * 16 + (c & 15);
-          float v = 0.0f;
+        for (int w = 0; w < kNW; ++w) v += sm[w * kSum + at];
+        if (row < tr.rows && o0 + c < a.N) a.y[(size_t)(tr.row0 + row) * a.N + o0 + c] = to_bf16(v);
+      }
+      buf ^= 1;
+      cu = 0;
+      ct += step;
+    }
+  };
+  int s = 0;
+  if constexpr (XR == 0) {
+    for (; s < total; s += U) {
 #pragma unroll
-          for (int w = 0; w < kNW; ++w) v += sm[w * kSum + at];
-          if (row < tr.rows && o0 + c < a.N) a.y[(size_t)(tr.row0 + row) * a.N + o0 + c] = to_bf16(v);
-        }
-        buf ^= 1;
-        cu = 0;
-        ct += step;
+      for (int u = 0; u < U; ++u) {
+        if (s + u >= total) break;
+        compute(std::true_type{}, u);
       }
     }
+  } else {
+    // Whole rounds of U, then the rest: with an exit within the loop the compiler
+    // sees ways round it on which a block was requested last, and waits as if it were
+    // (16 x 8192 x 8192: 13.8 us against 13.3).
+    for (; s + U <= total; s += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) compute(std::true_type{}, u);
+    }
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u)
+      if (s + u < total) compute(std::false_type{}, u);
   }
 }
 
@@ -634,15 +671,15 @@ static hipError_t launch_fp8_tile_t(Fp8Args a, int sk, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int NT, int U, bool XL>
-static hipError_t launch_fp8_rows_t(Fp8Args a, int lds_bytes, int grid, hipStream_t stream) {
+template <int XR>
+static hipError_t launch_fp8_rows_t(Fp8Args a, int grid, hipStream_t stream) {
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t ea =
-      ensure_dyn_lds(reinterpret_cast<const void*>(&fp8_rows_kernel<NT, U, false, XL>), 160 * 1024, lds_set);
+      ensure_dyn_lds(reinterpret_cast<const void*>(&fp8_rows_kernel<1, 4, false, XR>), kRowsLds, lds_set);
   if (ea != hipSuccess) return ea;
-  a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
-  hipLaunchKernelGGL((fp8_rows_kernel<NT, U, false, XL>), dim3((unsigned)min(grid, a.otiles), (unsigned)((a.M + 15) / 16)),
-                     dim3(64 * kNW), lds_bytes, stream, a);
+  a.otiles = (a.N + 15) / 16;
+  hipLaunchKernelGGL((fp8_rows_kernel<1, 4, false, XR>), dim3((unsigned)min(grid, a.otiles), (unsigned)((a.M + 15) / 16)),
+                     dim3(64 * kNW), (unsigned)fp8_rows_lds(a.M, a.K), stream, a);
   return hipGetLastError();
 }
 
@@ -651,17 +688,15 @@ static hipError_t launch_fp8_rows_grouped_t(Fp8Args a, hipStream_t stream) {
   a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
   const long long blocks = (long long)group_tiles_bound(a.M, 16, a.G) * a.otiles;
   if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_rows_kernel<NT, U, true, false>), dim3((unsigned)blocks), dim3(64 * kNW), kRowsSums<NT>, stream,
+  hipLaunchKernelGGL((fp8_rows_kernel<NT, U, true, 0>), dim3((unsigned)blocks), dim3(64 * kNW), kRowsSums<NT>, stream,
                      a);
   return hipGetLastError();
 }
 
-// Plain: 16 columns at a time by workgroups that stay (one per compute unit, two
-// where their rows fit LDS twice), the rows in LDS where they fit (1 x 17408 x
-// 5120 24.3 us with the rows from L2, 18.6 from LDS; 16 rows 32.2 and 21.6).
-// By expert: a workgroup per tile, of 64 columns while that leaves two tiles per
-// compute unit, else of 32 or 16 (96 rows of 64 experts, 2048 x 4096: 77.4 us
-// with 64 columns, 88.7 with 32, 118 with 16).
+// Plain: 16 columns at a time by workgroups that stay, two per compute unit where
+// their LDS allows it. By expert: a workgroup per tile, of 64 columns while that
+// leaves two tiles per compute unit, else of 32 or 16 (96 rows of 64 experts, 2048 x
+// 4096: 77.4 us with 64 columns, 88.7 with 32, 118 with 16).
 static hipError_t launch_fp8_rows(const Fp8Args& a, int cus, hipStream_t stream) {
   if (a.m_sizes != nullptr) {
     const int tiles = min(a.G, a.M);   // at least so many with rows, if rows are spread
@@ -669,12 +704,8 @@ static hipError_t launch_fp8_rows(const Fp8Args& a, int cus, hipStream_t stream)
     if ((long long)tiles * ((a.N + 31) / 32) >= 2 * cus) return launch_fp8_rows_grouped_t<2, 4>(a, stream);
     return launch_fp8_rows_grouped_t<1, 4>(a, stream);
   }
-  const int R = min(16, a.M);
-  const long long with_x =
-      kRowsSums<1> + (((long long)R * a.K + 1023) & ~1023LL) + (long long)R * (a.K / kBlk) * 4;
-  if (with_x <= 160 * 1024)
-    return launch_fp8_rows_t<1, 4, true>(a, (int)with_x, with_x <= 80 * 1024 ? 2 * cus : cus, stream);
-  return launch_fp8_rows_t<1, 4, false>(a, kRowsSums<1>, cus, stream);
+  const int grid = 2 * fp8_rows_lds(a.M, a.K) <= kRowsLds ? 2 * cus : cus;
+  return a.M <= 8 ? launch_fp8_rows_t<8>(a, grid, stream) : launch_fp8_rows_t<16>(a, grid, stream);
 }
 
 // stages: three where they fit LDS, else two

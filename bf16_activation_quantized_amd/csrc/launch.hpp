@@ -105,6 +105,13 @@ inline int group_tiles_bound(int M, int bm, int G) {
 // scales of blocks of block_rows (1 or 128) x 128
 hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int64_t M, int K, int block_rows,
                                hipStream_t stream);
+// LDS of the kernel for few rows: the sums of 16 columns, the rows (8 or 16, one
+// block of them spare) and their scales. It takes rows that fit (kRowsLds).
+constexpr int64_t kRowsLds = 160 * 1024;
+constexpr int64_t fp8_rows_lds(int64_t M, int64_t K) {
+  const int64_t kb = K / 128, r = M <= 8 ? 8 : 16;
+  return 2 * 8 * 256 * 4 + (kb + 1) * r * 128 + kb * r * 4;
+}
 // grad: the input gradient (x: dY, contraction over N). bm: rows per tile (16:
 // the kernel for few rows, whole contractions of the products only). With
 // part != nullptr slice s of sk, cps contraction blocks, writes fp32

@@ -155,10 +155,10 @@ def test_random_values_grouped(grad):
 @pytest.mark.parametrize("M", [1, 2, 5, 8, 15, 16])
 @pytest.mark.parametrize("N,K", [(16, 128), (40, 1024), (4160, 128), (5000, 1152), (300, 8832), (300, 9728), (130, 16384)])
 def test_few_rows(M, N, K):
-    """Every row count of the kernel for few rows, with the rows in LDS and (long ones) from L2, one and more column
-    tiles per workgroup, contractions shorter than its waves."""
+    """Every row count of the kernel for few rows, one and more column tiles per workgroup, contractions shorter than
+    its waves, rows that do not fit its LDS."""
     c = Case(M, N, K)
-    assert same(c.run((16, 0)), c.want()[0])
+    assert same(c.run(), c.want()[0])
 
 
 @pytest.mark.parametrize("N,K,G", [(64, 128, 3), (1000, 256, 5), (4096, 128, 20), (2048, 384, 64)])
@@ -249,15 +249,19 @@ def test_no_rows(grad):
 
 
 def test_weights_past_4_gib():
-    """Experts whose weights lie past 2^32 bytes."""
+    """Experts whose weights lie past 2^32 bytes (whole numbers: every order of summation gives the same bits)."""
     G, N, K = 34, 8192, 16384
-    w = torch.randint(0, 0x70, (G, N, K), dtype=torch.uint8, device=DEV).view(E4M3)
-    ws = torch.rand(G, N // 128, K // 128, device=DEV)
+    table = torch.arange(-4, 5, device=DEV).float().to(E4M3).view(torch.uint8)
+    w = torch.empty(G, N, K, dtype=torch.uint8, device=DEV)
+    for e in range(G):
+        w[e] = table[torch.randint(0, 9, (N, K), device=DEV)]
+    w = w.view(E4M3)
+    ws = torch.ones(G, N // 128, K // 128, device=DEV)
     sizes = [0] * (G - 2) + [3, 20]
-    x, xs = w4.w4a16_fp8_quantize(torch.randn(23, K, device=DEV).bfloat16())
+    x, xs = torch.randint(-4, 5, (23, K), device=DEV).float().to(E4M3), torch.ones(23, K // 128, device=DEV)
     y = w4.w4a16_fp8_gemm_grouped(x, xs, w, ws, torch.tensor(sizes, dtype=torch.int32, device=DEV), tile=(16, 0))
     for e, r in ((G - 2, slice(0, 3)), (G - 1, slice(3, 23))):
-        assert torch.equal(y[r], w4.w4a16_fp8_gemm(x[r].clone(), xs[r].clone(), w[e], ws[e], tile=(16, 0)))
+        assert torch.equal(y[r], w4.w4a16_fp8_gemm(x[r].clone(), xs[r].clone(), w[e], ws[e]))
     dy, dys = w4.w4a16_fp8_quantize(torch.randn(23, N, device=DEV).bfloat16())
     d = w4.w4a16_fp8_gemm_grad(dy, dys, w, ws, m_sizes=torch.tensor(sizes, dtype=torch.int32, device=DEV), tile=(64, 0))
     for e, r in ((G - 2, slice(0, 3)), (G - 1, slice(3, 23))):

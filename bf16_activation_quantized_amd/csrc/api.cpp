@@ -572,9 +572,10 @@ struct TileTime {
   double us;   // of one contraction step
 };
 
-// half_tiles: past one round a plain problem's last row tile counts as a half if it
-// has at most half the height's rows. Least estimated time over the tile heights and (without groups) the splits
-// whose workgroups fit one round; `forced` > 0 fixes the height.
+// Least estimated time over the tile heights and (without groups) the splits whose
+// workgroups fit one round; `forced` > 0 fixes the height. half_tiles: past one
+// round a plain problem's last row tile counts as a half if it has at most half the
+// height's rows (waves without rows only load).
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
                     int forced, int64_t min_steps, bool half_tiles) {
@@ -591,8 +592,8 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
     for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
       const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
       if (sk > 1 && (G > 0 || tiles * sk > cus || part < min_steps)) break;
-      const double us =
-          rounds_us(half ? tiles - 0.5 * (double)ot : tiles * sk, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
+      const double wgs = half ? tiles - 0.5 * (double)ot : tiles * sk;
+      const double us = rounds_us(wgs, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
       if (least < 0.0 || us < least * (1.0 - 1e-9)) {
         least = us;
         best = {c.bm, sk};
@@ -605,7 +606,8 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
 // One block of 128 of the 8-bit tile kernel by height, between what it takes
 // alone and with every compute unit busy (lower clocks): at 777 x 9728 x 2560 and
 // 8192^3 256 rows 1.42 and 1.78 us, 128 rows 0.93 and 1.04, 64 rows 0.70 and 0.63.
-constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1.15}, {128, 0.99}, {96, 0.82}, {64, 0.66}};
+constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1.15},
+                                  {128, 0.99}, {96, 0.82},  {64, 0.66}};
 constexpr double kFp8ExtraUs = 6.0;
 
 // The kernel for few rows holds those of a plain product in LDS.
@@ -682,10 +684,10 @@ w4a16_status run_fp8(bool grad, const uint8_t* x, const float* xs, const uint8_t
 }
 
 // ---- input gradient of the 4-bit products
-// One stage of 64 n by height, as for the 8-bit tiles (at 8192^3: 256 rows 1.66
-// us, 192 rows 1.29, 128 rows 0.87, 64 rows 0.56; below that each stage's chain of
-// LDS reads and its barrier).
-constexpr TileTime kW4GradTimes[] = {{256, 1.62}, {224, 1.43}, {192, 1.22}, {160, 1.05}, {128, 0.85},
+// One stage of 64 n by height, as for the 8-bit tiles (at 8192^3: 256 rows 1.77
+// us, 224 rows 1.40, 192 rows 1.24, 128 rows 0.88, 64 rows 0.56; below that each
+// stage's chain of LDS reads and its barrier).
+constexpr TileTime kW4GradTimes[] = {{256, 1.75}, {224, 1.42}, {192, 1.22}, {160, 1.05}, {128, 0.86},
                                      {96, 0.70},  {64, 0.55},  {32, 0.50},  {16, 0.46}};
 constexpr double kW4GradExtraUs = 6.0;
 

@@ -181,6 +181,14 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep 
 // transposing LDS read turns into 16 n of one column per lane, and the tile's
 // NG groups of scales, s and -24 s in fp16 (a nibble reads as 16 + q: (16 + q) s
 // - 24 s = s (q - 8), one exact packed FMA for two weights).
+// Bound by the products in fp16 (the bf16 library product of 8192^3 reaches 1620
+// TFLOP/s, 1380 with this one's operand order), at the clock that the power limit
+// leaves; below 128 rows by the unpacking, which every tile repeats. Hence tall tiles
+// (1322 x 19456 x 2560 145 us with 224 rows and four slices, 183 with 64 rows), waves
+// side by side so that each unpacks its own columns only, and the next stage's
+// unpacking between the products of this one.
+// 8192^3 900 us (1220 TFLOP/s); 1322 x 19456 x 2560 145 us with its prepass and the
+// reduce; 2048 rows of 8 experts of 2048 x 4096, group 32, 51 us.
 struct GradArgs {
   const uint16_t* h;       // [M, Np] fp16
   const int* up;           // [M]
@@ -245,7 +253,8 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
   const __amdgpu_buffer_rsrc_t rw =
       make_rsrc(a.w + (size_t)tr.wg * a.N * K2 + (uint32_t)o0 / 2u, (uint32_t)a.N * K2 - (uint32_t)o0 / 2u);
   // groups past the last column read zeros
-  const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.st + ((size_t)tr.wg * Kg + g0) * Np, (uint32_t)(Kg - g0) * (uint32_t)Np * 2u);
+  const __amdgpu_buffer_rsrc_t rs =
+      make_rsrc(a.st + ((size_t)tr.wg * Kg + g0) * Np, (uint32_t)(Kg - g0) * (uint32_t)Np * 2u);
 
   // Part i of the loads of stage s: QA of dY, one of the weights. Wave wv's load i
   // fills the 1 KiB block wv + 8 i of dY (8 rows each) and block wv of the weights
@@ -253,7 +262,8 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
   // 16-byte chunks lie in the slots of pair_swz (dY) and of the row pair (weights).
   constexpr int kParts = QA + 1;
   const uint32_t AB = (uint32_t)Np * 2u;
-  uint32_t ab = (uint32_t)(8 * wv + (lane >> 3)) * AB + 16u * ((uint32_t)(lane & 7) ^ pair_swz((4 * (wv & 1)) | (lane >> 4)));
+  uint32_t ab = (uint32_t)(8 * wv + (lane >> 3)) * AB +
+                16u * ((uint32_t)(lane & 7) ^ pair_swz((4 * (wv & 1)) | (lane >> 4)));
   uint32_t wb = (uint32_t)(8 * wv + (lane >> 3)) * K2 +
                 16u * ((uint32_t)(lane & 7) ^ (uint32_t)((4 * (wv & 1)) | (lane >> 4)));
   auto issue = [&](int s, int stage, int i) {
@@ -288,7 +298,8 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
   for (int g = wv; g < NG; g += kNW) {
     uint32_t top = 0;
     if (g0 + g < Kg)
-      for (int c = lane; c < chunks; c += 64) top = max(top, (uint32_t)a.tops[((size_t)tr.wg * chunks + c) * Kg + g0 + g]);
+      for (int c = lane; c < chunks; c += 64)
+        top = max(top, (uint32_t)a.tops[((size_t)tr.wg * chunks + c) * Kg + g0 + g]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
     if (lane == 0) gup[g] = up_by(top, 10);
@@ -346,8 +357,9 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t u = and_or_sv(j == 0 ? v << 6 : j == 1 ? v << 2 : j == 2 ? v >> 2 : v >> 6, mask, magic);
-      const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u), __builtin_bit_cast(f16x2, (uint32_t)sc[j]),
-                                                __builtin_bit_cast(f16x2, (uint32_t)cc[j]));
+      const uint32_t s = sc[j], c = cc[j];
+      const f16x2 r = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, u), __builtin_bit_cast(f16x2, s),
+                                                __builtin_bit_cast(f16x2, c));
       o[j] = __builtin_bit_cast(uint32_t, r);
     }
     out = __builtin_bit_cast(f16x8, o);
@@ -378,7 +390,8 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int ns = 0; ns < SN; ++ns)
-          acc[ms][ns] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[p][st * SN + ns], xf[ms & 1][st], acc[ms][ns], 0, 0, 0);
+          acc[ms][ns] =
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[p][st * SN + ns], xf[ms & 1][st], acc[ms][ns], 0, 0, 0);
       if (ms == 0) read_raw(after);   // (it waits, behind the first products)
       // (a chain of conversions and a write to LDS: between the products rather than
       // ahead of the barrier, 957 -> 935 us at 8192^3 and 128 rows, 933 -> 927 at 192;
@@ -484,8 +497,8 @@ static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
 // Stages: as many as LDS takes, up to 8. One row of waves (each unpacks the
 // weights of its own 32 columns only) against two: 128 rows 986 against 1090 us at
 // 8192^3, 192 rows 970 against 997; at 256 rows, where each wave then reads every
-// row of dY, 946 against 924 (group 32, where two rows of waves leave registers
-// short, 959 against 956).
+// row of dY, 946 against 924 (at group 32, where two rows of waves leave registers
+// short, 956 against 959). (Both sides before the last steps; now 965, 956 and 935.)
 template <int GS>
 static hipError_t launch_w4_grad_gs(const GradArgs& a, int sk, int bm, hipStream_t stream) {
   switch (bm) {

@@ -342,9 +342,9 @@ w4a16_status w4a16_expert_sort(const int32_t* ids, int32_t* order, int32_t* pos,
  * the last kept one) are neither read nor written. Written arrays do not
  * overlap the read ones, except that dz may be z.
  * The two gradients stand on both sides of the grouped product's own: from the
- * dz of combine's to the dxs of gather's the caller brings dXs = dZ .
- * dequant(W_g), which this library does not compute (nor gradients of the
- * packed weights and their scales).
+ * dz of combine's to the dxs of gather's, dXs = dZ . dequant(W_g), leads
+ * w4a16_gemm_grad (or, for 8-bit weights, w4a16_fp8_gemm_grad). Gradients of the
+ * packed weights and their scales are not computed.
  *
  * w4a16_expert_gather: xs[pos[t, j]] = x[t].
  *   x : [T, width] bf16, device;  xs : [rows, width] bf16, device, written
@@ -384,8 +384,17 @@ w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z,
 /* ------------------------------------------------------------------------
  * 8-bit products with a scale for each block of 128.
  *
- * Values are e4m3 (OCP: largest finite 448, one NaN), one byte each; scales
- * are fp32, 4-byte aligned, and may be any finite number.
+ * Values are e4m3 (OCP: largest finite 448, one NaN), one byte each, 16-byte
+ * aligned like the bf16 arrays; scales are fp32, 4-byte aligned. Written arrays
+ * do not overlap the read ones. Sizes whose values (N * K bytes of one weight, M
+ * * K * 2 bytes, M * N * 4 bytes) reach 2^32 are refused (W4A16_ERR_SHAPE);
+ * the weights of all experts together may be larger.
+ * Numerics of the three products: the products of each 8 neighbouring elements
+ * of the contraction are formed exactly, aligned to the largest of the 8 and cut
+ * 13 bits below its leading one; all else is added in fp32. Each block's sum is
+ * multiplied by the product of its two scales, which is formed first, in fp32
+ * (the scales may be any number whose product fp32 holds). A NaN value or a
+ * non-finite scale reaches the outputs that it takes part in, and no others.
  *
  * w4a16_fp8_quantize: blocks of block_rows x 128 of a bf16 matrix,
  *   top = max(largest magnitude of the block, 2^-100)
@@ -473,7 +482,9 @@ w4a16_status w4a16_fp8_gemm_grad(const uint8_t* dy, const float* dy_scales,
  * group and column group), which loses nothing of a value down to 2^-29 (dY)
  * and 2^-28 (S) of the largest finite one in its row or column group; smaller
  * values are rounded to 2^-40 (dY) and 2^-35 (S) of it. A non-finite value of
- * dY reaches its row only, a non-finite scale its column group only, as NaN.
+ * dY reaches its row only; a non-finite scale reaches its expert's column group
+ * only, as NaN. No atomics: bitwise reproducible for a given shape. dX does not
+ * overlap the read arrays; gradients of W and S are not computed.
  */
 size_t w4a16_gemm_grad_workspace_bytes(int32_t G, int64_t M, int64_t N,
                                        int64_t K, int32_t group_size);

@@ -435,32 +435,34 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
   // ---- epilogue: lane holds row 16 ms + r16 of the wave's, columns col(ns) .. + 3
   auto col = [&](int ns) { return GRAD ? 16 * ns + 4 * q4 : 4 * SN * q4 + 4 * ns; };
   const int ow = o0 + TN * wn;   // the wave's first column
-  if (a.part == nullptr && O % 8 == 0) {
+  if (a.part == nullptr) {
     static_assert(kNW * TM * TN * 2 <= NS * kStage, "the outputs fit the stages");
     __syncthreads();
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(a.y + (size_t)tr.row0 * O, (uint32_t)tr.rows * (uint32_t)O * 2u);
-    store_tile_bf16<TM, TN>(lds + wv * (TM * TN * 2), acc, col, ry, TM * wm, ow, O, lane);
+    uint8_t* reg = lds + wv * (TM * TN * 2);
+    uint16_t* y = a.y + (size_t)tr.row0 * O;
+    // (four columns per lane stored one by one: 1322 x 19457 x 2560 143 us, 74 so)
+    if (GRAD || O % 8 == 0)
+      store_tile_bf16<TM, TN>(reg, acc, col, make_rsrc(y, (uint32_t)tr.rows * (uint32_t)O * 2u), TM * wm, ow, O, lane);
+    else
+      store_tile_bf16_odd<TM, TN>(reg, acc, col, y, tr.rows, TM * wm, ow, O, lane);
     return;
   }
-  const size_t part0 = ((size_t)blockIdx.y * a.M + tr.row0) * O;
+  typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+  float* part = a.part + ((size_t)blockIdx.y * a.M + tr.row0) * O;
 #pragma unroll
   for (int ms = 0; ms < MS; ++ms) {
     const int row = TM * wm + 16 * ms + r16;
     if (row >= tr.rows) continue;
-    uint16_t* yr = a.y + (size_t)(tr.row0 + row) * O;
-    float* pr = a.part == nullptr ? nullptr : a.part + part0 + (size_t)row * O;
 #pragma unroll
     for (int ns = 0; ns < SN; ++ns) {
       const int c = ow + col(ns);
-      if (a.part != nullptr && O % 4 == 0) {
-        if (c < O) *reinterpret_cast<f32x4*>(pr + c) = acc[ms][ns];
+      float* p = part + (size_t)row * O + c;
+      if (c + 4 <= O) {
+        *reinterpret_cast<f32x4_a4*>(p) = acc[ms][ns];
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c + i < O) {
-            if (a.part != nullptr) pr[c + i] = acc[ms][ns][i];
-            else yr[c + i] = to_bf16(acc[ms][ns][i]);
-          }
+        for (int i = 0; i < 3; ++i)
+          if (c + i < O) p[i] = acc[ms][ns][i];
       }
     }
   }

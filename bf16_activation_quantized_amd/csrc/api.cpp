@@ -572,13 +572,15 @@ struct TileTime {
   double us;   // of one contraction step
 };
 
-// Least estimated time over the tile heights and (without groups) the splits whose
-// workgroups fit one round; `forced` > 0 fixes the height. half_tiles: past one
-// round a plain problem's last row tile counts as a half if it has at most half the
-// height's rows (waves without rows only load).
+// Least estimated time over the tile heights and (unless `split` is false) the
+// splits whose workgroups, as many as there may be, fit one round (by expert, by the
+// expected number instead: 200 rows of 8 experts of 4096 x 4096 44 -> 56 us); `forced`
+// > 0 fixes the height. half_tiles: past one round a plain problem's last row tile
+// counts as a half if it has at most half the height's rows (waves without rows only
+// load).
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
-                    int forced, int64_t min_steps, bool half_tiles) {
+                    int forced, int64_t min_steps, bool half_tiles, bool split) {
   RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
   double least = -1.0;
   const int64_t ot = ceil_div(O, 256);
@@ -588,10 +590,11 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
     // grouped: each group's last tile is half full on average
     const double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
     const double tiles = mt * (double)ot;
+    const double most = G > 0 ? (double)(ot * w4a16::group_tiles_bound((int)M, c.bm, (int)G)) : tiles;
     const bool half = half_tiles && G == 0 && tiles > cus && M % c.bm != 0 && M % c.bm <= c.bm / 2;
     for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
       const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
-      if (sk > 1 && (G > 0 || tiles * sk > cus || part < min_steps)) break;
+      if (sk > 1 && (!split || most * sk > cus || part < min_steps)) break;
       const double wgs = half ? tiles - 0.5 * (double)ot : tiles * sk;
       const double us = rounds_us(wgs, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
       if (least < 0.0 || us < least * (1.0 - 1e-9)) {
@@ -619,7 +622,7 @@ bool fp8_rows_built(bool grad, int64_t G, int64_t M, int64_t cb) {
 RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
   if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, cb))) return {16, 1};
-  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true);
+  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true, G == 0);
 }
 
 w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
@@ -703,19 +706,20 @@ w4a16_status check_w4_grad(bool grouped, int32_t G, int64_t M, int64_t N, int64_
   return W4A16_OK;
 }
 
-w4a16_status make_w4_grad_plan(bool grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size,
-                               int32_t bm, int32_t sk, w4a16::W4GradPlan* p) {
+w4a16_status make_w4_grad_plan(int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t bm, int32_t sk,
+                               w4a16::W4GradPlan* p) {
   const uint64_t np = (uint64_t)w4a16::w4_grad_padded(N), kg = (uint64_t)(K / group_size);
   if (bm != 0) {
     bool built = false;
     for (const TileTime& c : kW4GradTimes) built = built || c.bm == bm;
     if (!built) return W4A16_ERR_SHAPE;
   }
-  const RowsPlan r = plan_tiles(kW4GradTimes, kW4GradExtraUs, grouped ? G : 0, M, K, (int64_t)np / 64, bm, 8, false);
+  const RowsPlan r =
+      plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, false, true);
   p->bm = r.bm;
   p->sk = r.sk;
   if (sk != 0) {
-    if (sk < 1 || sk > 16 || (sk > 1 && grouped)) return W4A16_ERR_SPLIT_K;
+    if (sk < 1 || sk > 16) return W4A16_ERR_SPLIT_K;
     p->sk = sk;
   }
   p->h = 0;
@@ -736,7 +740,7 @@ w4a16_status run_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* s
   if (st != W4A16_OK || M == 0) return st;
   if (dy == nullptr || w == nullptr || s == nullptr || dx == nullptr) return W4A16_ERR_NULL;
   if (!aligned16(dy) || !aligned16(w) || !aligned16(s) || !aligned16(dx) || !aligned4(m_sizes)) return W4A16_ERR_ALIGN;
-  st = make_w4_grad_plan(m_sizes != nullptr, G, M, N, K, group_size, bm, sk, &p);
+  st = make_w4_grad_plan(G, M, N, K, group_size, bm, sk, &p);
   if (st != W4A16_OK) return st;
   if (workspace == nullptr || workspace_bytes < p.bytes) return W4A16_ERR_WORKSPACE;
   if (!aligned16(workspace)) return W4A16_ERR_ALIGN;
@@ -1100,7 +1104,7 @@ size_t w4a16_gemm_grad_workspace_bytes_ex(int32_t G, int64_t M, int64_t N, int64
                                           int32_t sk) {
   w4a16::W4GradPlan p;
   if (check_w4_grad(true, G, M, N, K, group_size) != W4A16_OK || M == 0) return 0;
-  if (make_w4_grad_plan(G > 1, G, M, N, K, group_size, bm, sk, &p) != W4A16_OK) return 0;
+  if (make_w4_grad_plan(G, M, N, K, group_size, bm, sk, &p) != W4A16_OK) return 0;
   return (size_t)p.bytes;
 }
 
@@ -1129,7 +1133,7 @@ w4a16_status w4a16_gemm_grad_auto(int32_t grouped, int32_t G, int64_t M, int64_t
   const w4a16_status st = check_w4_grad(grouped != 0, G, M, N, K, group_size);
   if (st != W4A16_OK) return st;
   w4a16::W4GradPlan p;
-  const w4a16_status sp = make_w4_grad_plan(grouped != 0, G, M, N, K, group_size, 0, 0, &p);
+  const w4a16_status sp = make_w4_grad_plan(G, M, N, K, group_size, 0, 0, &p);
   *bm_out = p.bm;
   *sk_out = p.sk;
   return sp;

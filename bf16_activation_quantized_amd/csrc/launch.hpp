@@ -120,6 +120,11 @@ hipError_t launch_fp8_gemm(const uint8_t* x, const float* xs, const uint8_t* w, 
                            float* part, const int32_t* m_sizes, int M, int N, int K, int G, bool grad, int cps, int sk,
                            int bm, int cus, hipStream_t stream);
 
+// The split-K reduce of the rows that m_sizes names: those behind the last group's
+// are left as they were. K a multiple of 8.
+hipError_t launch_splitk_reduce_rows(const float* ws, uint16_t* y, const int32_t* m_sizes, int G, int M, int K, int sk,
+                                     hipStream_t stream);
+
 // ---- input gradient of the 4-bit products (w4grad.hip)
 constexpr int64_t w4_grad_padded(int64_t N) { return (N + 127) / 128 * 128; }
 struct W4GradPlan {

@@ -54,12 +54,12 @@ __global__ __launch_bounds__(256) void pack_int4_kernel(const uint8_t* __restric
 // loads per slice; the loads of up to 8 slices go out before their adds, one
 // memory round trip per 8 slices; the adds run in slice order). Against 4
 // outputs per thread: 1322 x 2560 at SK 2, 92 -> 88 us for the whole GEMM.
-__global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ ws,
-                                                            uint16_t* __restrict__ y,
-                                                            uint64_t mn, int sk) {
+// The first `count` outputs of slices of mn.
+__device__ __forceinline__ void splitk_reduce(const float* __restrict__ ws, uint16_t* __restrict__ y, uint64_t mn,
+                                              uint64_t count, int sk) {
   // vector path only when every slice starts 16-byte aligned; the last
-  // mn % 8 outputs take the scalar path
-  const uint64_t nvec = (mn % 4 == 0) ? mn / 8 : 0;
+  // count % 8 outputs take the scalar path
+  const uint64_t nvec = (mn % 4 == 0) ? count / 8 : 0;
   const uint64_t stride = (uint64_t)gridDim.x * blockDim.x;
   for (uint64_t v = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; v < nvec; v += stride) {
     f32x4 a0 = {0.f, 0.f, 0.f, 0.f}, a1 = {0.f, 0.f, 0.f, 0.f};
@@ -91,11 +91,30 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restr
     o.w = pack_bf16x2(a1.z, a1.w);
     *reinterpret_cast<u32x4*>(y + v * 8) = o;
   }
-  for (uint64_t i = nvec * 8 + (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < mn; i += stride) {
+  for (uint64_t i = nvec * 8 + (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count; i += stride) {
     float acc = ws[i];
     for (int s = 1; s < sk; ++s) acc = acc + ws[(uint64_t)s * mn + i];
     y[i] = to_bf16(acc);
   }
+}
+
+__global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ ws,
+                                                            uint16_t* __restrict__ y,
+                                                            uint64_t mn, int sk) {
+  splitk_reduce(ws, y, mn, mn, sk);
+}
+
+// The rows of the groups only: each wave adds the sizes up (negative ones count as
+// none, M in all).
+__global__ __launch_bounds__(256) void splitk_reduce_rows_kernel(const float* __restrict__ ws,
+                                                                 uint16_t* __restrict__ y,
+                                                                 const int32_t* __restrict__ m_sizes, int G, int M,
+                                                                 int K, int sk) {
+  int rows = 0;   // (at most 2 M below: no overflow)
+  for (int g = threadIdx.x & 63; g < G; g += 64) rows = min(rows + min(max(m_sizes[g], 0), M), M);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) rows = min(rows + __shfl_xor(rows, d), M);
+  splitk_reduce(ws, y, (uint64_t)M * (uint64_t)K, (uint64_t)rows * (uint64_t)K, sk);
 }
 
 static int grid_for(uint64_t items, int per_block) {
@@ -114,6 +133,13 @@ hipError_t launch_pack_int4(const uint8_t* q, uint8_t* out, uint64_t total_in, h
 hipError_t launch_splitk_reduce(const float* ws, uint16_t* y, uint64_t mn, int sk, hipStream_t stream) {
   hipLaunchKernelGGL(splitk_reduce_kernel, dim3(grid_for((mn % 4 == 0 ? mn / 8 : mn) + 1, 256)), dim3(256), 0, stream,
                      ws, y, mn, sk);
+  return hipGetLastError();
+}
+
+hipError_t launch_splitk_reduce_rows(const float* ws, uint16_t* y, const int32_t* m_sizes, int G, int M, int K, int sk,
+                                     hipStream_t stream) {
+  hipLaunchKernelGGL(splitk_reduce_rows_kernel, dim3(grid_for((uint64_t)M * (uint64_t)K / 8 + 1, 256)), dim3(256), 0,
+                     stream, ws, y, m_sizes, G, M, K, sk);
   return hipGetLastError();
 }
 

@@ -547,6 +547,7 @@ hipError_t launch_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* 
   const hipError_t el = gsize == 32 ? launch_w4_grad_gs<32>(a, p.sk, p.bm, stream)
                                     : launch_w4_grad_gs<128>(a, p.sk, p.bm, stream);
   if (el != hipSuccess || p.sk == 1) return el;
+  if (m_sizes != nullptr) return launch_splitk_reduce_rows(a.part, dx, m_sizes, G, M, K, p.sk, stream);
   return launch_splitk_reduce(a.part, dx, (uint64_t)M * (uint64_t)K, p.sk, stream);
 }
 

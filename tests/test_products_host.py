@@ -153,7 +153,7 @@ def test_forced_choices_are_checked(lib):
 
     def gr4(ms=None, G=1, bm=0, sk=0, wsb=1 << 40):
         return g(A, A, A, ms, A, G, 300, 256, 1024, 128, bm, sk, A, wsb, None)
-    assert gr4(bm=48) == ERR_SHAPE and gr4(sk=17) == ERR_SPLIT and gr4(ms=A, sk=2) == ERR_SPLIT
+    assert gr4(bm=48) == ERR_SHAPE and gr4(sk=17) == ERR_SPLIT and gr4(ms=A, sk=2, wsb=2 * 300 * 1024 * 4) == ERR_WS
     assert gr4(bm=64, sk=4, wsb=4 * 300 * 1024 * 4) == ERR_WS
 
 

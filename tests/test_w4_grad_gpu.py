@@ -59,7 +59,7 @@ def test_exact(M, N, K, gs, tile):
     assert torch.equal(c.run(tile).cpu(), c.want()[0].bfloat16())
 
 
-@pytest.mark.parametrize("tile", [None] + [(h, 1) for h in HEIGHTS], ids=str)
+@pytest.mark.parametrize("tile", [None] + [(h, 1) for h in HEIGHTS] + [(16, 3), (64, 4), (192, 2)], ids=str)
 @pytest.mark.parametrize("gs", [128, 32])
 @pytest.mark.parametrize("sizes", [[5], [0, 3], [40, 1, 0, 17, 100], [0, 0, 300, 20, 0], [0, 0], [1] * 70],
                          ids=lambda s: f"{len(s)}x{sum(s)}")
@@ -72,7 +72,7 @@ def test_grouped_exact(sizes, gs, tile):
     assert torch.equal(dx[:-5].cpu(), want[:-5].bfloat16()) and (dx[-5:] == 7).all()
 
 
-@pytest.mark.parametrize("tile", [None, (16, 1), (64, 1), (256, 1)], ids=str)
+@pytest.mark.parametrize("tile", [None, (16, 1), (64, 1), (256, 1), (16, 2)], ids=str)
 def test_few_rows_far_apart(tile):
     """One row of each of a few experts, the first and the last of many among them,
     so that every tile holds one row; then all rows with the last expert."""

@@ -572,23 +572,32 @@ struct TileTime {
   double us;   // of one contraction step
 };
 
+// Row tiles of height bm of G groups with M rows together, if their sizes spread like
+// an exponential distribution; 2 % fewer, so that barely more than a round counts as
+// one. (By M / bm + G / 2, which short groups exceed, 4096 rows of 32 experts of 2048 x
+// 4096 took 122 us, 87 to 92 so.)
+double expected_tiles(int64_t G, int64_t M, int bm) {
+  const double groups = (double)std::max<int64_t>(std::min(G, M), 1), rows = (double)std::max<int64_t>(M, 1);
+  return 0.98 * groups / (1.0 - std::exp(-(double)bm * groups / rows));
+}
+
 // Least estimated time over the tile heights and (unless `split` is false) the
 // splits whose workgroups, as many as there may be, fit one round (by expert, by the
 // expected number instead: 200 rows of 8 experts of 4096 x 4096 44 -> 56 us); `forced`
 // > 0 fixes the height. half_tiles: past one round a plain problem's last row tile
 // counts as a half if it has at most half the height's rows (waves without rows only
-// load).
+// load). weight_bytes (0: not regarded): no choice takes less than reading them, at a
+// copy's rate (80 x 8192 x 8192: 8 slices of 128 rows 30.8 us, 4 of 64 28.8).
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
-                    int forced, int64_t min_steps, bool half_tiles, bool split) {
+                    int forced, int64_t min_steps, bool half_tiles, bool split, double weight_bytes) {
   RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
   double least = -1.0;
   const int64_t ot = ceil_div(O, 256);
   const double cus = device_cus();
   for (const TileTime& c : cands) {
     if (forced > 0 && c.bm != forced) continue;
-    // grouped: each group's last tile is half full on average
-    const double mt = (double)ceil_div(std::max<int64_t>(M, 1), c.bm) + (G > 0 ? 0.5 * (double)std::min(G, M) : 0.0);
+    const double mt = G > 0 ? expected_tiles(G, M, c.bm) : (double)ceil_div(std::max<int64_t>(M, 1), c.bm);
     const double tiles = mt * (double)ot;
     const double most = G > 0 ? (double)(ot * w4a16::group_tiles_bound((int)M, c.bm, (int)G)) : tiles;
     const bool half = half_tiles && G == 0 && tiles > cus && M % c.bm != 0 && M % c.bm <= c.bm / 2;
@@ -596,7 +605,8 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
       const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
       if (sk > 1 && (!split || most * sk > cus || part < min_steps)) break;
       const double wgs = half ? tiles - 0.5 * (double)ot : tiles * sk;
-      const double us = rounds_us(wgs, (double)part, c.us, extra_us, cus) + split_us(sk, (double)M * (double)O);
+      const double us = std::max(rounds_us(wgs, (double)part, c.us, extra_us, cus), 1.0 + weight_bytes / 5.2e6) +
+                        split_us(sk, (double)M * (double)O);
       if (least < 0.0 || us < least * (1.0 - 1e-9)) {
         least = us;
         best = {c.bm, sk};
@@ -608,9 +618,10 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
 
 // One block of 128 of the 8-bit tile kernel by height, between what it takes
 // alone and with every compute unit busy (lower clocks): at 777 x 9728 x 2560 and
-// 8192^3 256 rows 1.42 and 1.78 us, 128 rows 0.93 and 1.04, 64 rows 0.70 and 0.63.
+// 8192^3 256 rows 1.42 and 1.78 us, 128 rows 0.93 and 1.04, 64 rows 0.70 and 0.63
+// (with the weights from memory 0.81).
 constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1.15},
-                                  {128, 0.99}, {96, 0.82},  {64, 0.66}};
+                                  {128, 0.99}, {96, 0.82},  {64, 0.72}};
 constexpr double kFp8ExtraUs = 6.0;
 
 // The kernel for few rows holds those of a plain product in LDS.
@@ -622,7 +633,8 @@ bool fp8_rows_built(bool grad, int64_t G, int64_t M, int64_t cb) {
 RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
   if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, cb))) return {16, 1};
-  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true, G == 0);
+  const double bytes = G > 0 ? 0.0 : (double)O * (double)cb * kGroup;
+  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true, G == 0, bytes);
 }
 
 w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
@@ -715,7 +727,8 @@ w4a16_status make_w4_grad_plan(int32_t G, int64_t M, int64_t N, int64_t K, int32
     if (!built) return W4A16_ERR_SHAPE;
   }
   const RowsPlan r =
-      plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, false, true);
+      plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, false, true,
+                 G > 1 ? 0.0 : 0.5 * (double)N * (double)K);
   p->bm = r.bm;
   p->sk = r.sk;
   if (sk != 0) {

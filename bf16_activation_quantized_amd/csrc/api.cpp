@@ -637,12 +637,18 @@ RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int fo
   return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true, G == 0, bytes);
 }
 
+// Rows of one call: the row tiles of all experts are found with 32-bit sums of 64
+// sizes. The kernels take their buffers' extents tile by tile, so that the arrays
+// may pass 4 GiB, 256 rows of them not.
+constexpr int64_t kMaxRows = 1 << 24;
+uint64_t tile_rows_of(int64_t M) { return (uint64_t)std::min<int64_t>(M, 256); }
+
 w4a16_status check_fp8(bool grad, bool grouped, int32_t G, int64_t M, int64_t N, int64_t K) {
   if (G < 1 || (!grouped && G != 1)) return W4A16_ERR_SHAPE;
-  if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return W4A16_ERR_SHAPE;
+  if (M < 0 || N < 1 || K < 1 || M > kMaxRows || N > kMaxDim || K > kMaxDim) return W4A16_ERR_SHAPE;
   if (K % kGroup != 0 || (grad && N % kGroup != 0)) return W4A16_ERR_SHAPE;
-  const uint64_t m = (uint64_t)M, n = (uint64_t)N, k = (uint64_t)K;
-  if (n * k > kMaxBytes || m * k * 2u > kMaxBytes || m * n * 4u > kMaxBytes) return W4A16_ERR_SHAPE;
+  const uint64_t m = tile_rows_of(M), n = (uint64_t)N, k = (uint64_t)K;
+  if (n * k > kMaxBytes || m * k * 2u > kMaxBytes || m * n * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
   if (n * k * (uint64_t)G > (uint64_t)INT64_MAX / 2) return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }
@@ -708,12 +714,12 @@ constexpr double kW4GradExtraUs = 6.0;
 
 w4a16_status check_w4_grad(bool grouped, int32_t G, int64_t M, int64_t N, int64_t K, int32_t group_size) {
   if (G < 1 || (!grouped && G != 1)) return W4A16_ERR_SHAPE;
-  const w4a16_status st = check_dims(M, N, K, group_size);
-  if (st != W4A16_OK) return st;
-  if (N % 8 != 0) return W4A16_ERR_SHAPE;
-  const uint64_t np = (uint64_t)w4a16::w4_grad_padded(N);
-  if ((uint64_t)M * np * 2u > kMaxBytes || (uint64_t)M * (uint64_t)K * 4u > kMaxBytes) return W4A16_ERR_SHAPE;
-  if ((uint64_t)G * np * (uint64_t)(K / group_size) * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if (M < 0 || N < 1 || K < 1 || M > kMaxRows || N > kMaxDim || K > kMaxDim) return W4A16_ERR_SHAPE;
+  if ((group_size != kGroup && group_size != kGroupSmall) || K % kGroup != 0) return W4A16_ERR_GROUP_SIZE;
+  if (N % 8 != 0 || (uint64_t)N * (uint64_t)K / 2u > kMaxBytes) return W4A16_ERR_SHAPE;
+  const uint64_t np = (uint64_t)w4a16::w4_grad_padded(N), m = tile_rows_of(M);
+  if (m * np * 2u > kMaxBytes || m * (uint64_t)K * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
+  if (np * (uint64_t)(K / group_size) * 2u > kMaxBytes) return W4A16_ERR_SHAPE;
   if ((uint64_t)N * (uint64_t)K / 2u * (uint64_t)G > (uint64_t)INT64_MAX / 2) return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }

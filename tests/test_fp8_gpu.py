@@ -268,6 +268,36 @@ def test_weights_past_4_gib():
         assert torch.equal(d[r], w4.w4a16_fp8_gemm_grad(dy[r].clone(), dys[r].clone(), w[e], ws[e], tile=(64, 1)))
 
 
+def whole_case(M, N, K):
+    """Whole numbers on the device, scales of one: (x, scales, w, scales)."""
+    x = torch.randint(-4, 5, (M, K), device=DEV, dtype=torch.int8).to(torch.bfloat16).to(E4M3)
+    w = torch.randint(-4, 5, (N, K), device=DEV).float().to(E4M3)
+    return x, torch.ones(M, K // 128, device=DEV), w, torch.ones(-(-N // 128), K // 128, device=DEV)
+
+
+@pytest.mark.parametrize("M,N,K", [(140000, 16392, 128), (140001, 16391, 128), (140000, 64, 32768)])
+def test_rows_past_4_gib(M, N, K):
+    """Y, then X, of more than 2^32 bytes: the first, some middle and the last rows against calls of their own."""
+    x, xs, w, ws = whole_case(M, N, K)
+    for sizes in (None, [M - 5]):
+        m = None if sizes is None else torch.tensor(sizes, dtype=torch.int32, device=DEV)
+        y = w4.w4a16_fp8_gemm(x, xs, w, ws) if m is None else w4.w4a16_fp8_gemm_grouped(
+            x, xs, w[None], ws[None], m, y=torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV))
+        last = M if m is None else M - 5
+        for r in (0, 65500, 131000, last - 50):
+            assert torch.equal(y[r:r + 50], w4.w4a16_fp8_gemm(x[r:r + 50], xs[r:r + 50], w, ws))
+        assert (y[last:] == 7).all()
+
+
+def test_gradient_rows_past_4_gib():
+    M, N, K = 140000, 128, 16384
+    x, xs, _, _ = whole_case(M, N, N)
+    _, _, w, ws = whole_case(1, N, K)
+    d = w4.w4a16_fp8_gemm_grad(x, xs, w, ws)
+    for r in (0, 65500, 131000, M - 50):
+        assert torch.equal(d[r:r + 50], w4.w4a16_fp8_gemm_grad(x[r:r + 50], xs[r:r + 50], w, ws))
+
+
 @pytest.mark.parametrize("grad", [False, True])
 @pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (40, 256, 4096), (300, 512, 512)])
 def test_captured_and_replayed(M, N, K, grad):

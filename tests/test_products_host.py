@@ -62,8 +62,9 @@ COMMON = [
     (dict(M=-1), ERR_SHAPE), (dict(N=0), ERR_SHAPE), (dict(K=0), ERR_SHAPE), (dict(K=192), ERR_SHAPE),
     (dict(M=1 << 31), ERR_SHAPE), (dict(N=1 << 31), ERR_SHAPE), (dict(K=1 << 31), ERR_SHAPE),
     (dict(N=1 << 20, K=1 << 13), ERR_SHAPE),                 # one W of 4 GiB and more
-    (dict(M=1 << 24, N=128, K=256), ERR_SHAPE),              # X
-    (dict(M=1 << 20, N=1 << 11, K=128), ERR_SHAPE),          # Y in fp32
+    (dict(M=(1 << 24) + 1, N=128, K=128), ERR_SHAPE),        # rows
+    (dict(M=256, N=128, K=1 << 23), ERR_SHAPE),              # 256 rows of X or dX
+    (dict(M=256, N=1 << 23, K=128), ERR_SHAPE),              # of Y or dY
     (dict(G=0), ERR_SHAPE), (dict(G=-1), ERR_SHAPE),
     (dict(x=None), ERR_NULL), (dict(xs=None), ERR_NULL), (dict(w=None), ERR_NULL), (dict(ws=None), ERR_NULL),
     (dict(y=None), ERR_NULL),
@@ -96,9 +97,9 @@ def w4_grad(lib, dy=A, w=A, s=A, ms=None, dx=A, G=1, M=4, N=64, K=256, g=128, ws
 @pytest.mark.parametrize("kw,want", [
     (dict(M=-1), ERR_SHAPE), (dict(N=0), ERR_SHAPE), (dict(K=0), ERR_SHAPE), (dict(N=4), ERR_SHAPE),
     (dict(N=63), ERR_SHAPE), (dict(N=100), ERR_SHAPE), (dict(K=192), ERR_GROUP), (dict(g=64), ERR_GROUP),
-    (dict(M=1 << 31), ERR_SHAPE), (dict(N=1 << 21, K=1 << 12), ERR_SHAPE), (dict(M=1 << 22, N=512, K=128), ERR_SHAPE),
-    (dict(M=1 << 23, N=64, K=128), ERR_SHAPE),
-    (dict(G=1 << 20, ms=A, N=1 << 10, K=1 << 10), ERR_SHAPE),   # the scales of all groups
+    (dict(M=1 << 31), ERR_SHAPE), (dict(N=1 << 21, K=1 << 12), ERR_SHAPE), (dict(M=(1 << 24) + 1), ERR_SHAPE),
+    (dict(M=256, N=1 << 23, K=128), ERR_SHAPE), (dict(M=256, N=64, K=1 << 23), ERR_SHAPE),
+    (dict(G=1 << 30, ms=A, N=1 << 17, K=1 << 16), ERR_SHAPE),   # the weights of all groups
     (dict(G=0), ERR_SHAPE), (dict(G=2), ERR_SHAPE), (dict(G=2, ms=MIS2), ERR_ALIGN),
     (dict(dy=None), ERR_NULL), (dict(w=None), ERR_NULL), (dict(s=None), ERR_NULL), (dict(dx=None), ERR_NULL),
     (dict(dy=MIS), ERR_ALIGN), (dict(w=MIS), ERR_ALIGN), (dict(s=MIS), ERR_ALIGN), (dict(dx=MIS), ERR_ALIGN),

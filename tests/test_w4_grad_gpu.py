@@ -228,6 +228,22 @@ def test_weights_past_4_gib():
         assert torch.equal(d[r], w4.w4a16_gemm_grad(dy[r].clone(), w[e], s[e], tile=(16, 1)))
 
 
+@pytest.mark.parametrize("M,N,K", [(140000, 64, 16384), (140000, 16384, 128)])
+def test_rows_past_4_gib(M, N, K):
+    """dX, then dY, of more than 2^32 bytes: some rows against calls of their own (whole numbers: exact)."""
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    s = torch.ones(N, K // 128, device=DEV).bfloat16()
+    dy = torch.randint(-4, 5, (M, N), device=DEV, dtype=torch.int8).bfloat16()
+    for sizes in (None, [M - 5]):
+        m = None if sizes is None else torch.tensor(sizes, dtype=torch.int32, device=DEV)
+        d = w4.w4a16_gemm_grad(dy, w if m is None else w[None], s if m is None else s[None], m_sizes=m,
+                               dx=torch.full((M, K), 7.0, dtype=torch.bfloat16, device=DEV))
+        last = M if m is None else M - 5
+        for r in (0, 65500, 131000, last - 50):
+            assert torch.equal(d[r:r + 50], w4.w4a16_gemm_grad(dy[r:r + 50], w, s))
+        assert (d[last:] == 7).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (40, 2048, 256), (300, 512, 512)])
 def test_captured_and_replayed(M, N, K):
     c = Case(M, N, K)

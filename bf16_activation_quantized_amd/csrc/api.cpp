@@ -584,13 +584,15 @@ double expected_tiles(int64_t G, int64_t M, int bm) {
 // Least estimated time over the tile heights and (unless `split` is false) the
 // splits whose workgroups, as many as there may be, fit one round (by expert, by the
 // expected number instead: 200 rows of 8 experts of 4096 x 4096 44 -> 56 us); `forced`
-// > 0 fixes the height. half_tiles: past one round a plain problem's last row tile
-// counts as a half if it has at most half the height's rows (waves without rows only
-// load). weight_bytes (0: not regarded): no choice takes less than reading them, at a
-// copy's rate (80 x 8192 x 8192: 8 slices of 128 rows 30.8 us, 4 of 64 28.8).
+// > 0 fixes the height. half_from > 0: from this height on, past one round, a plain
+// problem's last row tile counts as a half if it has at most half the height's rows
+// (two rows of waves, of which those without rows only load). weight_bytes (0: not
+// regarded): no choice takes less than reading them, at a copy's rate (80 x 8192 x
+// 8192: 8 slices of 128 rows 30.8 us, 4 of 64 28.8); least_step: nor a step less than
+// this.
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
-                    int forced, int64_t min_steps, bool half_tiles, bool split, double weight_bytes) {
+                    int forced, int64_t min_steps, int half_from, bool split, double weight_bytes, double least_step) {
   RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
   double least = -1.0;
   const int64_t ot = ceil_div(O, 256);
@@ -600,12 +602,14 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
     const double mt = G > 0 ? expected_tiles(G, M, c.bm) : (double)ceil_div(std::max<int64_t>(M, 1), c.bm);
     const double tiles = mt * (double)ot;
     const double most = G > 0 ? (double)(ot * w4a16::group_tiles_bound((int)M, c.bm, (int)G)) : tiles;
-    const bool half = half_tiles && G == 0 && tiles > cus && M % c.bm != 0 && M % c.bm <= c.bm / 2;
+    const bool half = half_from > 0 && c.bm >= half_from && G == 0 && tiles > cus && M % c.bm != 0 &&
+                      M % c.bm <= c.bm / 2;
     for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
       const int64_t part = sk == 1 ? steps : ceil_div(steps, sk);
       if (sk > 1 && (!split || most * sk > cus || part < min_steps)) break;
       const double wgs = half ? tiles - 0.5 * (double)ot : tiles * sk;
-      const double us = std::max(rounds_us(wgs, (double)part, c.us, extra_us, cus), 1.0 + weight_bytes / 5.2e6) +
+      const double step = std::max(c.us, least_step);
+      const double us = std::max(rounds_us(wgs, (double)part, step, extra_us, cus), 1.0 + weight_bytes / 5.2e6) +
                         split_us(sk, (double)M * (double)O);
       if (least < 0.0 || us < least * (1.0 - 1e-9)) {
         least = us;
@@ -619,9 +623,10 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
 // One block of 128 of the 8-bit tile kernel by height, between what it takes
 // alone and with every compute unit busy (lower clocks): at 777 x 9728 x 2560 and
 // 8192^3 256 rows 1.42 and 1.78 us, 128 rows 0.93 and 1.04, 64 rows 0.70 and 0.63
-// (with the weights from memory 0.81).
+// (with the weights from memory 0.81); 32 rows serve experts with few (300 rows of 8
+// experts of 2048 x 4096 22.7 -> 17.7 us, gradient of 1000 rows of 64 139 -> 116).
 constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1.15},
-                                  {128, 0.99}, {96, 0.82},  {64, 0.72}};
+                                  {128, 0.99}, {96, 0.82},  {64, 0.72},  {32, 0.50}};
 constexpr double kFp8ExtraUs = 6.0;
 
 // The kernel for few rows holds those of a plain product in LDS.
@@ -634,7 +639,11 @@ RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int fo
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
   if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, cb))) return {16, 1};
   const double bytes = G > 0 ? 0.0 : (double)O * (double)cb * kGroup;
-  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, true, G == 0, bytes);
+  // (plain: a stage of weights from memory; 17 x 17408 x 5120 at 32 rows: 3 slices 24.3
+  // us, 2 slices, as 0.50 would have it, 27.3)
+  const double least_step = G > 0 ? 0.0 : 0.68;
+  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, 96, G == 0, bytes,
+                    least_step);
 }
 
 // Rows of one call: the row tiles of all experts are found with 32-bit sums of 64
@@ -733,8 +742,8 @@ w4a16_status make_w4_grad_plan(int32_t G, int64_t M, int64_t N, int64_t K, int32
     if (!built) return W4A16_ERR_SHAPE;
   }
   const RowsPlan r =
-      plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, false, true,
-                 G > 1 ? 0.0 : 0.5 * (double)N * (double)K);
+      plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, 0, true,
+                 G > 1 ? 0.0 : 0.5 * (double)N * (double)K, 0.0);
   p->bm = r.bm;
   p->sk = r.sk;
   if (sk != 0) {

@@ -728,7 +728,7 @@ static hipError_t launch_fp8_rows(const Fp8Args& a, int cus, hipStream_t stream)
   return a.M <= 8 ? launch_fp8_rows_t<8>(a, grid, stream) : launch_fp8_rows_t<16>(a, grid, stream);
 }
 
-// stages: three where they fit LDS, else two
+// stages: as many as fit LDS
 template <bool GRAD>
 static hipError_t launch_fp8_tile_bm(const Fp8Args& a, int sk, int bm, hipStream_t stream) {
   switch (bm) {
@@ -739,6 +739,7 @@ static hipError_t launch_fp8_tile_bm(const Fp8Args& a, int sk, int bm, hipStream
     case 128: return launch_fp8_tile_t<128, 2, 3, GRAD>(a, sk, stream);
     case 96: return launch_fp8_tile_t<96, 2, 3, GRAD>(a, sk, stream);
     case 64: return launch_fp8_tile_t<64, 1, 3, GRAD>(a, sk, stream);
+    case 32: return launch_fp8_tile_t<32, 1, 4, GRAD>(a, sk, stream);
     default: return hipErrorInvalidValue;
   }
 }

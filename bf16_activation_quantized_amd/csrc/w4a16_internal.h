@@ -78,8 +78,8 @@ w4a16_status w4a16_gemm_batched_ex(const uint16_t* x, const uint8_t* w_packed,
 /*
  * The 8-bit products and the input gradients with a given tile height and
  * split of the contraction (0: the automatic choice). bm: 16 (the kernel for
- * few rows, w4a16_fp8_gemm and _grouped only, split 1), 64, or 96 .. 256 rows in
- * steps of 32 (w4a16_gemm_grad: 16 and 32 too); sk: 1 .. 16 (w4a16_fp8_*: 1
+ * few rows, w4a16_fp8_gemm and _grouped only, split 1), or 32 .. 256 rows in
+ * steps of 32 (w4a16_gemm_grad: 16 too); sk: 1 .. 16 (w4a16_fp8_*: 1
  * with m_sizes).
  * grad: 0 the products, 1 w4a16_fp8_gemm_grad. Workspace bytes: of the call
  * with these choices.

@@ -17,8 +17,8 @@ from products_ref import E4M3, e4m3_of, fp8_values, grouped_ref, quantize_ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-TILES = [None, (16, 0), (64, 1), (96, 1), (128, 1), (160, 1), (192, 1), (224, 1), (256, 1), (64, 2), (128, 4), (160, 3),
-         (256, 16)]
+TILES = [None, (16, 0), (32, 1), (64, 1), (96, 1), (128, 1), (160, 1), (192, 1), (224, 1), (256, 1), (64, 2), (128, 4),
+         (160, 3), (32, 5), (256, 16)]
 GRAD_TILES = [t for t in TILES if t is None or t[0] != 16]
 
 
@@ -102,7 +102,7 @@ SIZES = [[5], [0, 3], [1, 0, 16, 0, 2], [40, 1, 0, 17, 100], [0, 0, 0, 300, 20, 
          [1] * 70, [2, 0] * 65 + [33]]
 
 
-@pytest.mark.parametrize("tile", [None, (16, 0), (64, 0), (96, 0), (128, 0), (160, 0), (192, 0), (224, 0), (256, 0)],
+@pytest.mark.parametrize("tile", [None] + [(h, 0) for h in (16, 32, 64, 96, 128, 160, 192, 224, 256)],
                          ids=str)
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{sum(s)}")
 @pytest.mark.parametrize("grad", [False, True])
@@ -118,7 +118,7 @@ def test_grouped_exact(sizes, tile, grad):
     assert same(y[:-5], want[:-5]) and (y[-5:] == 7).all()
 
 
-@pytest.mark.parametrize("tile", [None, (64, 0), (128, 0), (256, 0)], ids=str)
+@pytest.mark.parametrize("tile", [None, (32, 0), (64, 0), (128, 0), (256, 0)], ids=str)
 @pytest.mark.parametrize("grad", [False, True])
 def test_few_rows_far_apart(grad, tile):
     """One row of each of a few experts, the first and the last of many among them,
@@ -137,7 +137,7 @@ def close(y, want, size, blocks):
     assert ((y - want).norm() / want.norm()).item() < 2.0 ** -8 + 2.0 ** -10
 
 
-@pytest.mark.parametrize("tile", [None, (64, 1), (128, 2), (256, 1)], ids=str)
+@pytest.mark.parametrize("tile", [None, (32, 3), (64, 1), (128, 2), (256, 1)], ids=str)
 @pytest.mark.parametrize("M,N,K,grad", [(1, 1000, 2560, False), (16, 384, 4096, False), (200, 513, 1024, False),
                                         (300, 1024, 2560, False), (33, 1280, 384, True), (300, 1024, 512, True)])
 def test_random_values(M, N, K, grad, tile):
@@ -213,7 +213,7 @@ def test_non_finite_values_stay_in_their_row_and_column(tile):
 
 
 @pytest.mark.parametrize("grad", [False, True])
-@pytest.mark.parametrize("bm", [0, 16, 64, 96, 128, 160, 192, 224, 256])
+@pytest.mark.parametrize("bm", [0, 16, 32, 64, 96, 128, 160, 192, 224, 256])
 def test_other_experts_do_not_reach_a_row(grad, bm):
     """NaN in an expert, in its rows and in the rows behind the last: the others' outputs are the same bits."""
     if grad and bm == 16:

@@ -147,7 +147,7 @@ def test_forced_choices_are_checked(lib):
 
     def fp8(gr=0, ms=None, G=1, M=300, N=256, K=1024, bm=0, sk=0, wk=None, wkb=0):
         return f(gr, A, A, A, A, ms, A, G, M, N, K, bm, sk, wk, wkb, None)
-    assert fp8(bm=32) == ERR_SHAPE and fp8(bm=-1) == ERR_SHAPE and fp8(gr=1, bm=16) == ERR_SHAPE
+    assert fp8(bm=48) == ERR_SHAPE and fp8(bm=-1) == ERR_SHAPE and fp8(gr=1, bm=16) == ERR_SHAPE
     assert fp8(bm=64, sk=17) == ERR_SPLIT and fp8(bm=16, sk=2) == ERR_SPLIT and fp8(ms=A, bm=64, sk=2) == ERR_SPLIT
     assert fp8(bm=64, sk=2) == ERR_WS
     g = lib.w4a16_gemm_grad_ex

@@ -589,16 +589,19 @@ double expected_tiles(int64_t G, int64_t M, int bm) {
 // (two rows of waves, of which those without rows only load). weight_bytes (0: not
 // regarded): no choice takes less than reading them, at a copy's rate (80 x 8192 x
 // 8192: 8 slices of 128 rows 30.8 us, 4 of 64 28.8); least_step: nor a step less than
-// this.
+// this. row_bytes: the longest row that a tile addresses. Its offsets within a tile are
+// 32 bits, those of the rows past the last one too (they would wrap into the rows that
+// are there), so that only heights are taken whose rows fit one extent; bm = 0: none.
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
-                    int forced, int64_t min_steps, int half_from, bool split, double weight_bytes, double least_step) {
-  RowsPlan best = {forced > 0 ? forced : cands[0].bm, 1};
+                    int forced, int64_t min_steps, int half_from, bool split, double weight_bytes, double least_step,
+                    uint64_t row_bytes) {
+  RowsPlan best = {0, 1};
   double least = -1.0;
   const int64_t ot = ceil_div(O, 256);
   const double cus = device_cus();
   for (const TileTime& c : cands) {
-    if (forced > 0 && c.bm != forced) continue;
+    if ((forced > 0 && c.bm != forced) || (uint64_t)c.bm * row_bytes > kMaxBytes) continue;
     const double mt = G > 0 ? expected_tiles(G, M, c.bm) : (double)ceil_div(std::max<int64_t>(M, 1), c.bm);
     const double tiles = mt * (double)ot;
     const double most = G > 0 ? (double)(ot * w4a16::group_tiles_bound((int)M, c.bm, (int)G)) : tiles;
@@ -629,12 +632,15 @@ constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1
                                   {128, 0.99}, {96, 0.82},  {64, 0.72},  {32, 0.50}};
 constexpr double kFp8ExtraUs = 6.0;
 
-// The kernel for few rows holds those of a plain product in LDS.
+// The kernel for few rows holds those of a plain product in LDS; by expert it takes up
+// to 64 output columns at a time, whose offsets are 32 bits.
 bool fp8_rows_built(bool grad, int64_t G, int64_t M, int64_t cb) {
-  return !grad && (G > 0 || w4a16::fp8_rows_lds(M, cb * kGroup) <= w4a16::kRowsLds);
+  if (grad) return false;
+  return G > 0 ? 64 * (uint64_t)(cb * kGroup) <= kMaxBytes : w4a16::fp8_rows_lds(M, cb * kGroup) <= w4a16::kRowsLds;
 }
 
-// M rows of G groups (0: plain), O output columns, cb contraction blocks
+// M rows of G groups (0: plain), O output columns, cb contraction blocks; bm = 0: no
+// tile can address the rows (or, in the products, 256 output columns' weights)
 RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
   if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, cb))) return {16, 1};
@@ -642,13 +648,16 @@ RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int fo
   // (plain: a stage of weights from memory; 17 x 17408 x 5120 at 32 rows: 3 slices 24.3
   // us, 2 slices, as 0.50 would have it, 27.3)
   const double least_step = G > 0 ? 0.0 : 0.68;
-  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, 96, G == 0, bytes,
-                    least_step);
+  const uint64_t C = (uint64_t)cb * kGroup;
+  if (!grad && 256 * C > kMaxBytes) return {0, 1};
+  return plan_tiles(kFp8Times, kFp8ExtraUs, G, M, O, cb, forced, 4, 96, G == 0, bytes, least_step,
+                    std::max(C, 2 * (uint64_t)O));
 }
 
 // Rows of one call: the row tiles of all experts are found with 32-bit sums of 64
 // sizes. The kernels take their buffers' extents tile by tile, so that the arrays
-// may pass 4 GiB, 256 rows of them not.
+// may pass 4 GiB, 256 rows of them not (nor, where there are fewer, the rows of the
+// tiles that the plan takes).
 constexpr int64_t kMaxRows = 1 << 24;
 uint64_t tile_rows_of(int64_t M) { return (uint64_t)std::min<int64_t>(M, 256); }
 
@@ -672,6 +681,7 @@ w4a16_status make_fp8_plan(bool grad, int64_t G, int64_t M, int64_t N, int64_t K
     if (!built) return W4A16_ERR_SHAPE;
   }
   *p = fp8_plan(grad, G, M, O, cb, bm);
+  if (p->bm == 0) return W4A16_ERR_SHAPE;
   if (sk != 0) {
     if (sk < 1 || sk > 16 || (sk > 1 && (G > 0 || p->bm == 16))) return W4A16_ERR_SPLIT_K;
     p->sk = sk;
@@ -743,7 +753,8 @@ w4a16_status make_w4_grad_plan(int32_t G, int64_t M, int64_t N, int64_t K, int32
   }
   const RowsPlan r =
       plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, 0, true,
-                 G > 1 ? 0.0 : 0.5 * (double)N * (double)K, 0.0);
+                 G > 1 ? 0.0 : 0.5 * (double)N * (double)K, 0.0, 2 * std::max(np, (uint64_t)K));
+  if (r.bm == 0) return W4A16_ERR_SHAPE;
   p->bm = r.bm;
   p->sk = r.sk;
   if (sk != 0) {
@@ -1162,9 +1173,10 @@ w4a16_status w4a16_gemm_grad_auto(int32_t grouped, int32_t G, int64_t M, int64_t
   if (st != W4A16_OK) return st;
   w4a16::W4GradPlan p;
   const w4a16_status sp = make_w4_grad_plan(G, M, N, K, group_size, 0, 0, &p);
+  if (sp != W4A16_OK) return sp;
   *bm_out = p.bm;
   *sk_out = p.sk;
-  return sp;
+  return W4A16_OK;
 }
 
 }  // extern "C"

@@ -36,7 +36,8 @@ __device__ __forceinline__ void tile_rows_bf16(uint8_t* reg, const f32x4 (&acc)[
 }
 
 // The tile's first row is row row0 and its first column column c0 of the output
-// at ry (O columns, a multiple of 8); rows past ry's extent are dropped.
+// at ry (O columns, a multiple of 8); rows past ry's extent are dropped, as long as
+// the offsets of all the workgroup's rows fit 32 bits (the caller's plan sees to it).
 template <int TM, int TN, int MS, int SN, class COL>
 __device__ __forceinline__ void store_tile_bf16(uint8_t* reg, const f32x4 (&acc)[MS][SN], COL col,
                                                 __amdgpu_buffer_rsrc_t ry, int row0, int c0, int O, int lane) {

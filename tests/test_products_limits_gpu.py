@@ -1,0 +1,98 @@
+"""The 8-bit products and the input gradients at the ends of their ranges, on the
+GPU: fewer rows than a tile, so wide that the offsets of a full tile's rows pass
+2^32 bytes. Whole numbers, so that every order of summation gives the same bits."""
+import pytest
+import torch
+
+import bf16_activation_quantized_amd as w4
+from products_ref import E4M3
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def whole(*shape):
+    return torch.randint(-4, 5, shape, device=DEV, dtype=torch.int8)
+
+
+def whole8(*shape):
+    """The same as e4m3, a part at a time."""
+    v = whole(*shape)
+    table = torch.arange(-4, 5, device=DEV).float().to(E4M3).view(torch.uint8)
+    flat = v.view(-1)
+    out = torch.empty(flat.shape, dtype=torch.uint8, device=DEV)
+    for i in range(0, flat.numel(), 1 << 26):
+        out[i:i + (1 << 26)] = table[flat[i:i + (1 << 26)].long() + 4]
+    return out.view(E4M3).view(shape)
+
+
+@pytest.mark.parametrize("M,N", [(65, 33038208), (130, 16500000)])
+def test_product_of_wide_rows(M, N):
+    """Y against columns of its own."""
+    K = 128
+    x, xs = whole8(M, K), torch.ones(M, 1, device=DEV)
+    w, ws = whole8(N, K), torch.ones(-(-N // 128), 1, device=DEV)
+    y = w4.w4a16_fp8_gemm(x, xs, w, ws)
+    step = 1 << 20
+    for n in range(0, N, step):
+        n1 = min(N, n + step)
+        assert torch.equal(y[:, n:n1], w4.w4a16_fp8_gemm(x, xs, w[n:n1], ws[n // 128:-(-n1 // 128)])), n
+
+
+def test_product_of_wide_rows_by_expert():
+    M, N, K, G = 70, 30000000, 128, 2
+    x, xs = whole8(M, K), torch.ones(M, 1, device=DEV)
+    w, ws = whole8(G, N, K), torch.ones(G, -(-N // 128), 1, device=DEV)
+    y = w4.w4a16_fp8_gemm_grouped(x, xs, w, ws, torch.tensor([40, 28], dtype=torch.int32, device=DEV),
+                                  y=torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV))
+    step = 1 << 20
+    for e, r in ((0, slice(0, 40)), (1, slice(40, 68))):
+        for n in range(0, N, step):
+            n1 = min(N, n + step)
+            want = w4.w4a16_fp8_gemm(x[r], xs[r], w[e, n:n1], ws[e, n // 128:-(-n1 // 128)])
+            assert torch.equal(y[r, n:n1], want), (e, n)
+    assert (y[68:] == 7).all()
+
+
+def columns(full, part, K):
+    """dX against the same weights' columns."""
+    step = 1 << 19
+    for k in range(0, K, step):
+        k1 = min(K, k + step)
+        assert torch.equal(full[:, k:k1], part(k, k1)), k
+
+
+def test_8_bit_gradient_of_wide_rows():
+    M, N, K = 65, 128, 33030144
+    dy, dys = whole8(M, N), torch.ones(M, 1, device=DEV)
+    w, ws = whole8(N, K), torch.ones(1, K // 128, device=DEV)
+    columns(w4.w4a16_fp8_gemm_grad(dy, dys, w, ws),
+            lambda a, b: w4.w4a16_fp8_gemm_grad(dy, dys, w[:, a:b].contiguous(), ws[:, a // 128:b // 128].contiguous()),
+            K)
+
+
+@pytest.mark.parametrize("M,K,gs", [(20, 1 << 26, 128), (65, 33030144, 32)])
+def test_4_bit_gradient_of_wide_rows(M, K, gs):
+    N = 8
+    dy = whole(M, N).bfloat16()
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    s = torch.ldexp(torch.ones(1, device=DEV), torch.randint(-2, 3, (N, K // gs), device=DEV)).bfloat16()
+    columns(w4.w4a16_gemm_grad(dy, w, s, group_size=gs),
+            lambda a, b: w4.w4a16_gemm_grad(dy, w[:, a // 2:b // 2].contiguous(), s[:, a // gs:b // gs].contiguous(),
+                                            group_size=gs), K)
+
+
+def test_4_bit_gradient_of_wide_output_gradients():
+    """dY's own rows past 2^32 bytes per full tile: the sum of its parts along N (whole numbers below 2^24)."""
+    M, N, K = 33, 33030144, 128
+    dy = torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)
+    at = torch.randint(0, N, (M, 200), device=DEV)
+    dy.scatter_(1, at, torch.randint(-4, 5, (M, 200), device=DEV).bfloat16())
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=DEV)
+    s = torch.ones(N, K // 128, dtype=torch.bfloat16, device=DEV)
+    dx = w4.w4a16_gemm_grad(dy, w, s)
+    for m in range(M):
+        n = at[m].unique()
+        q = torch.stack((w[n] & 15, w[n] >> 4), dim=-1).reshape(len(n), K).double() - 8
+        want = (dy[m, n].double()[:, None] * q).sum(0)
+        assert torch.equal(dx[m], want.bfloat16()), m

@@ -20,6 +20,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "loadorder.hpp"
 #include "tilemap.hpp"
 #include "tilestore.hpp"
 
@@ -368,14 +369,22 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
   // One stage j: its products, from weights that are in registers, while stage j +
   // 1's weights are unpacked, a fragment at each row tile, and stage j + NS - 1 is
   // loaded, a few loads at each row tile. Its scales were requested kAhead stages
-  // earlier: waiting for a load waits for all that was issued before it, which
-  // should be no more than the barrier waits for anyway. Past the last stage the
-  // last one's loads are repeated, unused: one form of the loop keeps the
-  // registers where they are.
+  // earlier (waiting for a load waits for all that was issued before it). As built,
+  // the first of every kAhead steps waits for more: the loop may end after any step,
+  // the compiler sees ways from each end back to its head, on which the scales that
+  // the first step puts away were requested a moment ago, and waits for all but the
+  // last one to three loads (at all heights but 192 and 256 rows): the ring runs empty
+  // there. Past the last stage the last one's loads are repeated, unused: one form of
+  // the loop keeps the registers where they are.
   constexpr int kPer = NQA / kNW + 2;   // loads issued per stage, by any wave at least
   // (kAhead stages are unrolled: a register with a load in flight cannot be moved)
   constexpr int kAhead = NS > 5 ? 4 : 2;
-  static_assert(kAhead >= NS - 4, "stages in flight");
+  static_assert(kAhead < NS, "a scale word behind each of the last stages ahead of the loop");
+  // Loads in flight that leave stages 0 and 1 landed ahead of the loop, and stage j + 2
+  // at the end of step j. (The first steps' waits count stages 3 .. NS - 2, requested
+  // ahead of the loop, as steps: with one load less each, stage j + 2 might be missing.)
+  constexpr int kStart = (NS - 3) * (kPer - 1) + (kAhead < NS - 3 ? kAhead : NS - 3);
+  constexpr int kStep = (NS - 3) * kPer;
   uint32_t sv[kAhead];                  // the scales of stages j + NS - 1 .. j + NS + kAhead - 2
   auto body = [&](auto P, int stage, int after, int next, int word, int nstage) {
     constexpr int p = P.value & 1;
@@ -403,7 +412,7 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
 #pragma unroll
       for (int f = ms * NF / MS; f < (ms + 1) * NF / MS; ++f) unpack(after, f, wf[1 - p][f]);
     }
-    wait_vm_barrier<(NS - 3) * kPer>();   // stage j + 2 has landed
+    wait_vm_barrier<kStep>();   // stage j + 2 has landed
   };
 
   static_assert(NS >= 3, "stages j, j + 1 (whose weights are unpacked) and j + 2 (being loaded)");
@@ -412,16 +421,23 @@ __global__ __launch_bounds__(64 * kNW) void w4_grad_kernel(const GradArgs a) {
     uint32_t first[NS - 1];
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) first[s] = scale_word(at(s));
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) sv[i] = scale_word(at(NS - 1 + i));
+    // The stages ahead of the loop: the last kAhead of them with a scale word behind
+    // each, as in the steps. (The empty asm keeps the loads in this order, which the
+    // waits count on.)
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) issue(at(s), s, i);
+      asm volatile("" ::: "memory");
+      const int i = s - (NS - 1 - kAhead);
+      if (i >= 0) sv[i] = scale_word(at(NS - 1 + i));
+      asm volatile("" ::: "memory");
     }
 #pragma unroll
     for (int s = 0; s < NS - 1; ++s) put_scales(s, first[s], sup);
-    wait_vm_barrier<(NS - 3) * (kPer - 1)>();
+    static_assert(ring_waits_hold(NS, kPer - 1, NS - 1 - kAhead, kStart, kStep), "waits of the ring");
+    wait_vm_barrier<kStart>();   // stages 0 and 1 have landed
     read_raw(0);
 #pragma unroll
     for (int f = 0; f < NF; ++f) unpack(0, f, wf[0][f]);

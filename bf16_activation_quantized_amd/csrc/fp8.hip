@@ -558,6 +558,8 @@ __global__ __launch_bounds__(64 * kNW) void fp8_rows_kernel(const Fp8Args a) {
       uint8_t* dst = xl + (xin ? b : KB) * XB;
 #pragma unroll
       for (int d = 0; d < XR / 8; ++d) dma16(rx, dst + 1024 * d, xoff[d], so);
+      // ahead of the weights: once those are there, so are the rows (compute())
+      asm volatile("" ::: "memory");
     }
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(wg + (size_t)o0 * K, in ? (uint32_t)min(TC, a.N - o0) * (uint32_t)K : 0u);

@@ -14,6 +14,7 @@
 // output columns of each tile: one product of scales per row tile and block
 // serves all of a wave's column tiles, and the outputs of a lane are
 // contiguous.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -166,15 +167,19 @@ __global__ __launch_bounds__(256) void fp8_quantize_blocks_kernel(const uint16_t
 
 hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int64_t M, int K, int block_rows,
                                hipStream_t stream) {
+  // (a launch takes fewer than 2^32 threads)
   const int kblocks = K / kBlk;
   if (block_rows == 1) {
-    const int64_t grid = (M * kblocks + 31) / 32;
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(fp8_quantize_rows_kernel, dim3((unsigned)grid), dim3(256), 0, stream, x, q, scales,
-                       M * kblocks);
+    const int64_t blocks = M * kblocks, most = (int64_t)1 << 28;   // 2^23 workgroups
+    for (int64_t b = 0; b < blocks; b += most) {
+      const int64_t n = std::min(blocks - b, most);
+      hipLaunchKernelGGL(fp8_quantize_rows_kernel, dim3((unsigned)((n + 31) / 32)), dim3(256), 0, stream,
+                         x + b * kBlk, q + b * kBlk, scales + b, n);
+    }
   } else {
+    // M K < 2^37: fewer than 2^23 + K / 128, and fewer than 2^24 where M <= 128
     const int64_t grid = (M + kBlk - 1) / kBlk * kblocks;
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+    if (grid >= (int64_t)1 << 24) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fp8_quantize_blocks_kernel, dim3((unsigned)grid), dim3(256), 0, stream, x, q, scales, M, K,
                        kblocks);
   }

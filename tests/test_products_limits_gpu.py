@@ -96,3 +96,34 @@ def test_4_bit_gradient_of_wide_output_gradients():
         q = torch.stack((w[n] & 15, w[n] >> 4), dim=-1).reshape(len(n), K).double() - 8
         want = (dy[m, n].double()[:, None] * q).sum(0)
         assert torch.equal(dx[m], want.bfloat16()), m
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_past_2_36_values(rows):
+    """More blocks than one launch has threads for: rows here and there against calls of their own, zeros elsewhere."""
+    M, K = (1 << 23) + 130, 8192
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 3.2 * M * K:
+        pytest.skip("210 GB of device memory are needed")
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    q = torch.empty(M, K, dtype=torch.uint8, device=DEV).fill_(0x55).view(E4M3)
+    at = [0, 1 << 22, (1 << 22) + 128, (1 << 23) - 128, 1 << 23]      # (multiples of 128)
+    for r in at:
+        x[r:r + 130] = torch.randn(130, K, device=DEV).bfloat16()
+    s = torch.full((-(-M // rows), K // 128), -1.0, device=DEV)
+    w4.w4a16_fp8_quantize(x, q=q, scales=s, block_rows=rows)
+    for r in at:
+        r1 = min(M, r + 256)
+        q2, s2 = w4.w4a16_fp8_quantize(x[r:r1].clone(), block_rows=rows)
+        assert torch.equal(q[r:r1].view(torch.uint8), q2.view(torch.uint8)), r
+        assert torch.equal(s[r // rows:-(-r1 // rows)], s2), r
+    step = 1 << 17
+    for r in range(512, M, step):
+        part = q[r:min(M, r + step)].view(torch.uint8)
+        kept = torch.zeros(part.shape[0], dtype=torch.bool, device=DEV)
+        for a in at:
+            kept[max(0, a - r):max(0, a + 130 - r)] = True
+        assert not part.view(torch.int64)[~kept].any(), r
+    assert (s > 0).all()
+    del x, q, s, part
+    torch.cuda.empty_cache()

@@ -591,7 +591,8 @@ double expected_tiles(int64_t G, int64_t M, int bm) {
 // 8192: 8 slices of 128 rows 30.8 us, 4 of 64 28.8); least_step: nor a step less than
 // this. row_bytes: the longest row that a tile addresses. Its offsets within a tile are
 // 32 bits, those of the rows past the last one too (they would wrap into the rows that
-// are there), so that only heights are taken whose rows fit one extent; bm = 0: none.
+// are there), so that only heights are taken whose rows fit one extent, and whose
+// workgroups one launch; bm = 0: none.
 template <size_t NT>
 RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int64_t M, int64_t O, int64_t steps,
                     int forced, int64_t min_steps, int half_from, bool split, double weight_bytes, double least_step,
@@ -605,6 +606,7 @@ RowsPlan plan_tiles(const TileTime (&cands)[NT], double extra_us, int64_t G, int
     const double mt = G > 0 ? expected_tiles(G, M, c.bm) : (double)ceil_div(std::max<int64_t>(M, 1), c.bm);
     const double tiles = mt * (double)ot;
     const double most = G > 0 ? (double)(ot * w4a16::group_tiles_bound((int)M, c.bm, (int)G)) : tiles;
+    if (most > (double)w4a16::kMaxBlocks) continue;
     const bool half = half_from > 0 && c.bm >= half_from && G == 0 && tiles > cus && M % c.bm != 0 &&
                       M % c.bm <= c.bm / 2;
     for (const int32_t sk : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16}) {
@@ -632,18 +634,23 @@ constexpr TileTime kFp8Times[] = {{256, 1.65}, {224, 1.60}, {192, 1.37}, {160, 1
                                   {128, 0.99}, {96, 0.82},  {64, 0.72},  {32, 0.50}};
 constexpr double kFp8ExtraUs = 6.0;
 
-// The kernel for few rows holds those of a plain product in LDS; by expert it takes up
-// to 64 output columns at a time, whose offsets are 32 bits.
-bool fp8_rows_built(bool grad, int64_t G, int64_t M, int64_t cb) {
+// The kernel for few rows holds those of a plain product in LDS (its grid has 16 rows
+// per y); by expert it takes up to 64 output columns at a time, whose offsets are 32
+// bits, a workgroup for each row tile and columns.
+bool fp8_rows_built(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb) {
   if (grad) return false;
-  return G > 0 ? 64 * (uint64_t)(cb * kGroup) <= kMaxBytes : w4a16::fp8_rows_lds(M, cb * kGroup) <= w4a16::kRowsLds;
+  if (G == 0) return w4a16::fp8_rows_lds(M, cb * kGroup) <= w4a16::kRowsLds && M <= 16 * 65535;
+  const int64_t cols = 16 * w4a16::fp8_rows_tiles((int)M, (int)O, (int)G, device_cus());
+  return 64 * (uint64_t)(cb * kGroup) <= kMaxBytes &&
+         w4a16::group_tiles_bound((int)M, 16, (int)G) * ceil_div(O, cols) <= w4a16::kMaxBlocks;
 }
 
 // M rows of G groups (0: plain), O output columns, cb contraction blocks; bm = 0: no
-// tile can address the rows (or, in the products, 256 output columns' weights)
+// tile can address the rows (or, in the products, 256 output columns' weights), or all
+// heights have more workgroups than a launch takes
 RowsPlan fp8_plan(bool grad, int64_t G, int64_t M, int64_t O, int64_t cb, int forced) {
   const int64_t per = G > 0 ? ceil_div(M, G) : M;
-  if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, cb))) return {16, 1};
+  if (forced == 16 || (forced == 0 && per <= 16 && fp8_rows_built(grad, G, M, O, cb))) return {16, 1};
   const double bytes = G > 0 ? 0.0 : (double)O * (double)cb * kGroup;
   // (plain: a stage of weights from memory; 17 x 17408 x 5120 at 32 rows: 3 slices 24.3
   // us, 2 slices, as 0.50 would have it, 27.3)
@@ -676,7 +683,7 @@ w4a16_status make_fp8_plan(bool grad, int64_t G, int64_t M, int64_t N, int64_t K
                            uint64_t* bytes) {
   const int64_t O = grad ? K : N, cb = (grad ? N : K) / kGroup;
   if (bm != 0) {
-    bool built = bm == 16 && fp8_rows_built(grad, G, M, cb);
+    bool built = bm == 16 && fp8_rows_built(grad, G, M, O, cb);
     for (const TileTime& c : kFp8Times) built = built || c.bm == bm;
     if (!built) return W4A16_ERR_SHAPE;
   }
@@ -754,7 +761,7 @@ w4a16_status make_w4_grad_plan(int32_t G, int64_t M, int64_t N, int64_t K, int32
   const RowsPlan r =
       plan_tiles(kW4GradTimes, kW4GradExtraUs, G > 1 ? G : 0, M, K, (int64_t)np / 64, bm, 8, 0, true,
                  G > 1 ? 0.0 : 0.5 * (double)N * (double)K, 0.0, 2 * std::max(np, (uint64_t)K));
-  if (r.bm == 0) return W4A16_ERR_SHAPE;
+  if (r.bm == 0 || w4a16::w4_grad_prep_blocks(G, M, (int)N, (int)kg) > w4a16::kMaxBlocks) return W4A16_ERR_SHAPE;
   p->bm = r.bm;
   p->sk = r.sk;
   if (sk != 0) {

@@ -177,7 +177,7 @@ hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int
                          x + b * kBlk, q + b * kBlk, scales + b, n);
     }
   } else {
-    // M K < 2^37: fewer than 2^23 + K / 128, and fewer than 2^24 where M <= 128
+    // (M K < 2^37: fewer than 2^23 + K / 128 blocks, and than 2^24 where M <= 128)
     const int64_t grid = (M + kBlk - 1) / kBlk * kblocks;
     if (grid >= (int64_t)1 << 24) return hipErrorInvalidValue;
     hipLaunchKernelGGL(fp8_quantize_blocks_kernel, dim3((unsigned)grid), dim3(256), 0, stream, x, q, scales, M, K,
@@ -691,7 +691,7 @@ static hipError_t launch_fp8_tile_t(Fp8Args a, int sk, hipStream_t stream) {
   a.mtiles = a.m_sizes != nullptr ? group_tiles_bound(a.M, BM, a.G) : (a.M + BM - 1) / BM;
   a.otiles = ((GRAD ? a.K : a.N) + kBN - 1) / kBN;
   const long long blocks = (long long)a.mtiles * a.otiles;
-  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   hipLaunchKernelGGL((fp8_tile_kernel<BM, WM, NS, GRAD>), dim3((unsigned)blocks, sk), dim3(64 * kNW), lds_bytes,
                      stream, a);
   return hipGetLastError();
@@ -714,22 +714,19 @@ template <int NT, int U>
 static hipError_t launch_fp8_rows_grouped_t(Fp8Args a, hipStream_t stream) {
   a.otiles = (a.N + 16 * NT - 1) / (16 * NT);
   const long long blocks = (long long)group_tiles_bound(a.M, 16, a.G) * a.otiles;
-  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   hipLaunchKernelGGL((fp8_rows_kernel<NT, U, true, 0>), dim3((unsigned)blocks), dim3(64 * kNW), kRowsSums<NT>, stream,
                      a);
   return hipGetLastError();
 }
 
 // Plain: 16 columns at a time by workgroups that stay, two per compute unit where
-// their LDS allows it. By expert: a workgroup per tile, of 64 columns while that
-// leaves two tiles per compute unit, else of 32 or 16 (96 rows of 64 experts, 2048 x
-// 4096: 77.4 us with 64 columns, 88.7 with 32, 118 with 16).
+// their LDS allows it. By expert: a workgroup per tile (fp8_rows_tiles).
 static hipError_t launch_fp8_rows(const Fp8Args& a, int cus, hipStream_t stream) {
   if (a.m_sizes != nullptr) {
-    const int tiles = min(a.G, a.M);   // at least so many with rows, if rows are spread
-    if ((long long)tiles * ((a.N + 63) / 64) >= 2 * cus) return launch_fp8_rows_grouped_t<4, 2>(a, stream);
-    if ((long long)tiles * ((a.N + 31) / 32) >= 2 * cus) return launch_fp8_rows_grouped_t<2, 4>(a, stream);
-    return launch_fp8_rows_grouped_t<1, 4>(a, stream);
+    const int nt = fp8_rows_tiles(a.M, a.N, a.G, cus);
+    return nt == 4 ? launch_fp8_rows_grouped_t<4, 2>(a, stream)
+           : nt == 2 ? launch_fp8_rows_grouped_t<2, 4>(a, stream) : launch_fp8_rows_grouped_t<1, 4>(a, stream);
   }
   const int grid = 2 * fp8_rows_lds(a.M, a.K) <= kRowsLds ? 2 * cus : cus;
   return a.M <= 8 ? launch_fp8_rows_t<8>(a, grid, stream) : launch_fp8_rows_t<16>(a, grid, stream);

@@ -95,6 +95,10 @@ hipError_t launch_expert_combine_grad(const uint16_t* dy, const uint16_t* z, con
                                       uint16_t* dz, float* dw, int64_t T, int k, int64_t rows, int width,
                                       hipStream_t stream);
 
+// Workgroups of 512 threads in one launch: fewer than 2^32 threads, past which a grid
+// is cut short without an error.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 23) - 1;
+
 // Row tiles of height bm that M rows in G groups take at most: each of the groups
 // that have rows (at most min(G, M)) ends in a tile that may hold a single row.
 inline int group_tiles_bound(int M, int bm, int G) {
@@ -112,6 +116,13 @@ constexpr int64_t fp8_rows_lds(int64_t M, int64_t K) {
   const int64_t kb = K / 128, r = M <= 8 ? 8 : 16;
   return 2 * 8 * 256 * 4 + (kb + 1) * r * 128 + kb * r * 4;
 }
+// The same by expert: column tiles of 16 per workgroup. A workgroup per tile, of 64
+// columns while that leaves two tiles per compute unit, else of 32 or 16 (96 rows of 64
+// experts, 2048 x 4096: 77.4 us with 64 columns, 88.7 with 32, 118 with 16).
+inline int fp8_rows_tiles(int M, int N, int G, int cus) {
+  const long long tiles = G < M ? G : M;   // at least so many with rows, if rows are spread
+  return tiles * ((N + 63) / 64) >= 2 * cus ? 4 : tiles * ((N + 31) / 32) >= 2 * cus ? 2 : 1;
+}
 // grad: the input gradient (x: dY, contraction over N). bm: rows per tile (16:
 // the kernel for few rows, whole contractions of the products only). With
 // part != nullptr slice s of sk, cps contraction blocks, writes fp32
@@ -127,6 +138,22 @@ hipError_t launch_splitk_reduce_rows(const float* ws, uint16_t* y, const int32_t
 
 // ---- input gradient of the 4-bit products (w4grad.hip)
 constexpr int64_t w4_grad_padded(int64_t N) { return (N + 127) / 128 * 128; }
+// Prepass: threads per row of dY, as few as hold it in registers (a row is a chain of a
+// load, a reduction and a store: 2048 rows of 2048 15.5 us with 512 threads each, 8 with
+// 64); workgroups per 128 n of an expert's Kg groups of scales; all workgroups.
+constexpr int kPrepThreads = 512;
+constexpr int kPrepRegs = 5;     // times 8 elements per thread
+constexpr int kPrepWide = 128;   // groups of scales read as one run
+constexpr int w4_grad_row_threads(int N) {
+  int t = 64;
+  while (t < kPrepThreads && N > t * 8 * kPrepRegs) t *= 2;
+  return t;
+}
+constexpr int w4_grad_scale_blocks(int Kg) { return Kg <= kPrepWide ? 1 : (Kg + 63) / 64; }
+constexpr int64_t w4_grad_prep_blocks(int64_t G, int64_t M, int N, int Kg) {
+  const int rows = kPrepThreads / w4_grad_row_threads(N);
+  return G * (w4_grad_padded(N) / 128) * w4_grad_scale_blocks(Kg) + (M + rows - 1) / rows;
+}
 struct W4GradPlan {
   int bm, sk;                       // rows per tile, slices of the contraction
   uint64_t h, up, st, tops, part;   // byte offsets into the workspace

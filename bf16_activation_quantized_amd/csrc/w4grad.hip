@@ -75,10 +75,6 @@ struct GradPrep {
 // groups at a time are read by rows. The others take rows of dY, 64 to 512 threads
 // each, which hold the row in registers between its largest magnitude and its
 // conversion up to kPrepRegs x 8 elements per thread (read again past that).
-constexpr int kPrepThreads = 512;
-constexpr int kPrepRegs = 5;
-constexpr int kPrepWide = 128;
-
 __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep a) {
   __shared__ __attribute__((aligned(16))) uint16_t tile[128 * (kPrepWide + 1)];   // [n][k group], odd pitch
   const int t = threadIdx.x;
@@ -504,7 +500,7 @@ static hipError_t launch_w4_grad_t(GradArgs a, int sk, hipStream_t stream) {
   a.mtiles = a.m_sizes != nullptr ? group_tiles_bound(a.M, BM, a.G) : (a.M + BM - 1) / BM;
   a.otiles = (a.K + kBN - 1) / kBN;
   const long long blocks = (long long)a.mtiles * a.otiles;
-  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
   hipLaunchKernelGGL((w4_grad_kernel<BM, WM, NS, GS>), dim3((unsigned)blocks, sk), dim3(64 * kNW), lds_bytes, stream,
                      a);
   return hipGetLastError();
@@ -541,16 +537,11 @@ hipError_t launch_w4_grad(const uint16_t* dy, const uint8_t* w, const uint16_t* 
   pr.st = reinterpret_cast<uint16_t*>(ws + p.st);
   pr.tops = reinterpret_cast<uint16_t*>(ws + p.tops);
   pr.M = M; pr.N = N; pr.Np = Np; pr.Kg = Kg; pr.G = G;
-  pr.sblocks = Kg <= kPrepWide ? 1 : (Kg + 63) / 64;
-  // as few threads per row as hold it in registers: a row is a chain of a load, a
-  // reduction and a store (2048 rows of 2048: 15.5 us with 512 threads each, 8 with 64)
-  pr.per_row = 64;
-  while (pr.per_row < kPrepThreads && N > pr.per_row * 8 * kPrepRegs) pr.per_row *= 2;
-  const int rows = kPrepThreads / pr.per_row;
-  const long long sblocks = (long long)G * (Np / 128) * pr.sblocks;
-  const long long blocks = sblocks + (M + rows - 1) / rows;
-  if (blocks > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-  pr.stotal = (int)sblocks;
+  pr.sblocks = w4_grad_scale_blocks(Kg);
+  pr.per_row = w4_grad_row_threads(N);
+  const int64_t blocks = w4_grad_prep_blocks(G, M, N, Kg);
+  if (blocks > kMaxBlocks) return hipErrorInvalidValue;
+  pr.stotal = (int)((int64_t)G * (Np / 128) * pr.sblocks);
   hipLaunchKernelGGL(grad_prep_kernel, dim3((unsigned)blocks), dim3(kPrepThreads), 0, stream, pr);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -390,7 +390,8 @@ w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z,
  * weights of fewer than 2^32 bytes per expert; all arrays may be larger, as long
  * as 256 rows of X, dY, Y or dX are not (W4A16_ERR_SHAPE). Fewer rows than that may
  * be wider, while those of the smallest tile (32) fit; K >= 2^24 is refused for the
- * products of more than 16 rows.
+ * products of more than 16 rows, and so are calls of 2^23 tiles or more (half a
+ * million experts, say).
  * Numerics of the three products: the products of each 8 neighbouring elements
  * of the contraction are formed exactly, aligned to the largest of the 8 and cut
  * 13 bits below its leading one; all else is added in fp32. Each block's sum is
@@ -478,7 +479,8 @@ w4a16_status w4a16_fp8_gemm_grad(const uint8_t* dy, const float* dy_scales,
  *   0 <= M <= 2^24 (0: nothing enqueued), N >= 8, N % 8 == 0, K >= 128,
  *   K % 128 == 0; all arrays may be larger than 2^32 bytes, but not the weights or
  *   the scales of one expert, nor 256 rows of dY or dX (fewer rows may be wider,
- *   while those of the smallest tile, 16, fit).
+ *   while those of the smallest tile, 16, fit); calls of 2^23 tiles or more, or
+ *   with as many blocks of 128 x 128 scales, are refused (W4A16_ERR_SHAPE).
  *   workspace: device scratch, overwritten, never NULL when M > 0: at least
  *   w4a16_gemm_grad_workspace_bytes (dY and the scales in fp16, the partial
  *   sums of a split contraction), 16-byte aligned.

@@ -127,3 +127,30 @@ def test_quantize_past_2_36_values(rows):
     assert (s > 0).all()
     del x, q, s, part
     torch.cuda.empty_cache()
+
+
+def test_the_most_threads_of_a_launch():
+    """Between 2^31 and 2^32 of them: quantisation of one very long row in blocks of 128 x 128, and 2^24 rows by expert in
+    tiles of 16."""
+    torch.cuda.empty_cache()
+    K = (1 << 31) - 128
+    x = torch.zeros(1, K, dtype=torch.bfloat16, device=DEV)
+    # (powers of two from the CPU: the device's ldexp is off by 2^-24 at some)
+    two = torch.ldexp(torch.ones(50), torch.arange(50)).to(DEV)[torch.arange(K // 128, device=DEV) % 50]
+    x[0, 5::128] = (7 * two).bfloat16()
+    q, s = w4.w4a16_fp8_quantize(x, block_rows=128)
+    assert torch.equal(s[0], two / 64)
+    v = q.view(torch.uint8).view(-1, 128)
+    assert (v[:, 5] == 0x7E).all() and not v[:, :5].any() and not v[:, 6:].any()      # 448 and zeros
+    del x, q, s, v, two
+    M, N, K, G = 1 << 24, 448, 128, 74
+    x, xs = whole8(M, K), torch.ones(M, 1, device=DEV)
+    w, ws = whole8(G, N, K), torch.ones(G, -(-N // 128), 1, device=DEV)
+    sizes = torch.full((G,), M // G, dtype=torch.int32, device=DEV)
+    sizes[3] += M % G
+    y = w4.w4a16_fp8_gemm_grouped(x, xs, w, ws, sizes, tile=(16, 0))      # 16 rows and 64 columns per workgroup
+    assert torch.equal(y, w4.w4a16_fp8_gemm_grouped(x, xs, w, ws, sizes, tile=(256, 0)))
+    last = M - M // G
+    assert torch.equal(y[last:last + 300], w4.w4a16_fp8_gemm(x[last:last + 300], xs[last:last + 300], w[-1], ws[-1]))
+    del x, xs, y
+    torch.cuda.empty_cache()

@@ -8,10 +8,11 @@
 // by powers of two, each row of dY by its own and each column group of scales
 // by its own, and the accumulator is brought back by their product:
 //  * a row of dY has its largest finite magnitude in [2^14, 2^15): values down
-//    to 2^-29 of it are exact, smaller ones are rounded to 2^-40 of it;
+//    to 2^-31 of it are exact (8 bits from 2^-17 on, the last one 2^-24, the step of
+//    fp16's subnormals), smaller ones are off by half a step, 2^-39 of it at most;
 //  * a group of scales (one k group, all n) has its largest finite magnitude in
-//    [2^10, 2^11): products with q - 8 are exact for scales down to 2^-28 of
-//    it, smaller ones are rounded to 2^-35 of it.
+//    [2^10, 2^11): products with q - 8 are exact for scales down to 2^-27 of
+//    it, smaller scales are off by 2^-35 of it at most.
 // A prepass writes dY in fp16, the scales transposed to [k group, n] and their
 // largest magnitudes per 128 n; both are ordered (0 4 1 5 2 6 3 7) within 8 n,
 // the order in which a word of 8 nibbles unpacks into pairs.

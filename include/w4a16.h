@@ -486,9 +486,9 @@ w4a16_status w4a16_fp8_gemm_grad(const uint8_t* dy, const float* dy_scales,
  *   sums of a split contraction), 16-byte aligned.
  * Numerics: S (q - 8) is exact in fp16, so no weight is rounded; dY and S enter
  * in fp16, scaled by powers of two (dY by one per row, S by one per weight
- * group and column group), which loses nothing of a value down to 2^-29 (dY)
- * and 2^-28 (S) of the largest finite one in its row or column group; smaller
- * values are rounded to 2^-40 (dY) and 2^-35 (S) of it. A non-finite value of
+ * group and column group), which loses nothing of a value down to 2^-31 (dY)
+ * and 2^-27 (S) of the largest finite one in its row or column group; smaller
+ * values are off by at most 2^-39 (dY) and 2^-35 (S) of it. A non-finite value of
  * dY reaches its row only; a non-finite scale reaches its expert's column group
  * only, as NaN. No atomics: bitwise reproducible for a given shape. dX does not
  * overlap the read arrays; gradients of W and S are not computed.

@@ -154,3 +154,27 @@ def test_the_most_threads_of_a_launch():
     assert torch.equal(y[last:last + 300], w4.w4a16_fp8_gemm(x[last:last + 300], xs[last:last + 300], w[-1], ws[-1]))
     del x, xs, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("tile", [None, (16, 1), (128, 1), (256, 1)], ids=str)
+@pytest.mark.parametrize("top", [1.0, 2.0 ** 60, 1.9921875, 2.0 ** -90])
+def test_least_exact_values_of_the_4_bit_gradient(top, tile):
+    """dY down to 2^-31 of its row's largest and scales down to 2^-27 of their column group's are exact; the next
+    smaller power with all 8 bits is off by half a step of fp16's subnormals: 2^-39 and 2^-35 of a power of two."""
+    N, K, odd = 16, 256, 1 + 2.0 ** -7
+    two = 2.0 ** torch.tensor(top).log2().floor().item()
+    w = torch.full((N, K // 2), 0x88, dtype=torch.uint8)
+    w[5] = 0x99                                                    # q - 8 = 1, all others 0
+    dy, s = torch.zeros(2, N), torch.ones(N, K // 128)
+    dy[:, 0] = top
+    dy[0, 5], dy[1, 5] = odd * two * 2.0 ** -31, odd * two * 2.0 ** -32
+    run = lambda dy, s: w4.w4a16_gemm_grad(dy.bfloat16().to(DEV), w.to(DEV), s.bfloat16().to(DEV), tile=tile).double().cpu()  # noqa: E731,E501
+    y = run(dy, s)
+    assert (y[0] == odd * two * 2.0 ** -31).all()
+    assert ((y[1] - odd * two * 2.0 ** -32).abs() == two * 2.0 ** -39).all()
+    dy, s = torch.zeros(1, N), torch.full((N, K // 128), top)
+    dy[0, 5] = 1
+    s[5, 0], s[5, 1] = odd * two * 2.0 ** -27, odd * two * 2.0 ** -28
+    y = run(dy, s)
+    assert (y[0, :128] == odd * two * 2.0 ** -27).all()
+    assert ((y[0, 128:] - odd * two * 2.0 ** -28).abs() == two * 2.0 ** -35).all()

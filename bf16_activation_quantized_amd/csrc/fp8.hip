@@ -129,7 +129,8 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(const uint16_t* 
 }
 
 // Blocks of 128 x 128 (the last rows' may be shorter): one workgroup each, which
-// holds its block in registers between the maximum and the conversion.
+// holds its block in registers between the maximum and the conversion (8192 x 8192: 37.6
+// us, 5.4 TB/s; in blocks of 1 x 128 35.7).
 __global__ __launch_bounds__(256) void fp8_quantize_blocks_kernel(const uint16_t* __restrict__ x,
                                                                   uint8_t* __restrict__ q,
                                                                   float* __restrict__ scales, int64_t M, int K,
@@ -193,8 +194,10 @@ hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int
 // buffer loads that write LDS directly, NS stages in a ring.
 // Work per block of 128 at 256 rows: 256 products of 16 x 16 and, per lane, as many
 // times four scaled additions. The products alone run at 4944 TFLOP/s on this card,
-// with the additions (on the VALU, beside them) at 4000: that is the bound of the
-// large cases, at the clock that the power limit leaves them (about 2 GHz of 2.4).
+// with the additions (on the VALU, beside them) at 4000: two thirds of the largest
+// cases' time at the clock that the power limit leaves them (2.04 GHz of 2.4 at 8192^3,
+// the matrix core busy for 55 % of it). The rest is waits: at 192 rows and more, with
+// two stages, the last loads of a block go out 8 products ahead of the wait for them.
 //  * 8 waves of 128 x 64 (2 x 4), so that a lane's scale product serves 4 tiles and
 //    the two operands' LDS reads (24 KiB per wave and block) stay below the products.
 //  * The loads of a stage are issued between the row tiles: all at the stage's start
@@ -202,8 +205,8 @@ hipError_t launch_fp8_quantize(const uint16_t* x, uint8_t* q, float* scales, int
 //    2560 115 us, spread 79).
 //  * One product of scales per lane and row tile: the activations are the B operand.
 // 8192^3 470 us (2340 TFLOP/s); 1322 x 19456 x 2560 72 us; 16384 rows of 32 experts of
-// 2048 x 4096 185 us; gradient of 777 x 9728 x 2560 37 us (160 workgroups' worth of
-// rows split five ways over the contraction), of 4096 rows of 8 experts 52 us.
+// 2048 x 4096 186 us; gradient of 777 x 9728 x 2560 37 us (50 tiles of 160 rows, split
+// five ways over the contraction), of 4096 rows of 8 experts 52 us.
 struct Fp8Args {
   const uint8_t* x;        // [M, C] e4m3: C = K, gradient: N
   const float* xs;         // [M, C / 128]
@@ -485,8 +488,8 @@ __global__ __launch_bounds__(64 * kNW) void fp8_tile_kernel(const Fp8Args a) {
 // it multiplies, and waits for no one (16 x 8192 x 8192 13.3 us; 16.6 with all rows
 // loaded first, by all waves).
 // Bound by the weights' stream: 1 x 17408 x 5120 16.9 us (5.3 TB/s), 16 x 8192 x 8192
-// 13.3 us (5.0 TB/s), 96 rows of 64 experts of 2048 x 4096 77 us (7.0 TB/s, in part
-// from the last-level cache).
+// 13.3 us (5.0 TB/s), 96 rows of 64 experts of 2048 x 4096 77 us (4.7 TB/s: 43 or 44
+// experts have rows).
 template <int NT>
 constexpr int kRowsSums = 2 * kNW * NT * 256 * 4;   // bytes of the sums, two buffers
 

@@ -180,12 +180,14 @@ __global__ __launch_bounds__(kPrepThreads) void grad_prep_kernel(const GradPrep 
 // NG groups of scales, s and -24 s in fp16 (a nibble reads as 16 + q: (16 + q) s
 // - 24 s = s (q - 8), one exact packed FMA for two weights).
 // Bound by the products in fp16 (the bf16 library product of 8192^3 reaches 1620
-// TFLOP/s, 1380 with this one's operand order), at the clock that the power limit
-// leaves; below 128 rows by the unpacking, which every tile repeats. Hence tall tiles
-// (1322 x 19456 x 2560 145 us with 224 rows and four slices, 183 with 64 rows), waves
+// TFLOP/s, 1380 with this one's operand order) at the clock that the power limit
+// leaves, which keep the matrix core busy for 54 % of the time (1322 x 19456 x 2560, 2.0
+// GHz), by the unpacking, which every tile repeats, and by waits for stages: at most
+// heights the ring runs empty every second or fourth stage (below). Hence tall tiles
+// (1322 x 19456 x 2560 146 us with 224 rows and four slices, 183 with 64 rows), waves
 // side by side so that each unpacks its own columns only, and the next stage's
 // unpacking between the products of this one.
-// 8192^3 900 us (1220 TFLOP/s); 1322 x 19456 x 2560 145 us with its prepass and the
+// 8192^3 900 us (1220 TFLOP/s); 1322 x 19456 x 2560 146 us with its prepass and the
 // reduce; 2048 rows of 8 experts of 2048 x 4096, group 32, 51 us.
 struct GradArgs {
   const uint16_t* h;       // [M, Np] fp16

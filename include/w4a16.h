@@ -389,9 +389,9 @@ w4a16_status w4a16_expert_combine_grad(const uint16_t* dy, const uint16_t* z,
  * do not overlap the read ones. The three products take M <= 2^24 rows and
  * weights of fewer than 2^32 bytes per expert; all arrays may be larger, as long
  * as 256 rows of X, dY, Y or dX are not (W4A16_ERR_SHAPE). Fewer rows than that may
- * be wider, while those of the smallest tile (32) fit; K >= 2^24 is refused for the
- * products of more than 16 rows, and so are calls of 2^23 tiles or more (half a
- * million experts, say).
+ * be wider, while those of the smallest tile (32) fit. K >= 2^24 is refused by the
+ * products (by expert taken up to 2^26 where there are at most 16 rows per expert),
+ * and so are calls of 2^23 tiles or more (half a million experts, say).
  * Numerics of the three products: the products of each 8 neighbouring elements
  * of the contraction are formed exactly, aligned to the largest of the 8 and cut
  * 13 bits below its leading one; all else is added in fp32. Each block's sum is
